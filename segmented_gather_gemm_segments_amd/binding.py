@@ -35,6 +35,8 @@ LORA_PATH_TILE = 3
 LORA_SHRINK_TILE_TOKENS, LORA_SHRINK_TILE_K, LORA_SHRINK_TILE_ITEM_BYTES = 64, 64, 262144
 LORA_DEFAULT_TILE_MIN_TOKENS, LORA_TILE_MIN_RANK_SHORT, LORA_MAX_K_SPLITS = 16, 32, 64
 LORA_TILE_PAYS_BYTES = 24 << 20
+LORA_ATTN_ROWS, LORA_ATTN_TILE_ROWS, LORA_ATTN_MAX_PARTS, LORA_ATTN_CAUSAL = 16, 128, 64, 1
+LORA_KV_HOST_ONLY = 1
 
 
 class LoraError(RuntimeError):
@@ -67,8 +69,31 @@ class lora_cache_stats(ctypes.Structure):
                 ("free_pages_a", ctypes.c_int32), ("free_pages_b", ctypes.c_int32)]
 
 
+class lora_w4_weights(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p)]
+
+
+class lora_kv_view(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("dtype", "head_dim", "kv_heads", "page_tokens", "num_pages",
+                                              "num_seqs", "max_pages", "reserved")] + \
+               [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p)]
+
+
+class lora_attn_plan(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("q_heads", "kv_heads", "head_dim", "flags", "window", "num_tokens",
+                                              "num_row_items", "num_tile_items", "num_joins", "num_part_rows")] + \
+               [("workspace_bytes", ctypes.c_int64)]
+
+
+class lora_kv_stats(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("seqs", "pages", "shared", "spare", "highest", "page_tokens")]
+
+
 _lib = None
-_P, _I32, _U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64
+_P, _I32, _I64, _U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
 
 EXPORTS = {
     "lora_abi_version": ([], _I32),
@@ -107,6 +132,25 @@ EXPORTS = {
     "lora_probe_stream_read": ([_P, ctypes.c_int64, _I32, _I32, _I32, _P, _P], _I32),
     "lora_probe_release": ([_I32, _I32, _P, _P, _P, _P], _I32),
     "lora_debug_flags": ([_P, _I32], _I32),
+    "lora_w4_bytes": ([_I32, _I32, ctypes.POINTER(_I64)], _I32),
+    "lora_w4_pack": ([_I32, _I32, _I32, _P, _P, _P], _I32),
+    "lora_base_w4": ([_I32, _I32, _P, _P, _I64, _P, _I64, _P], _I32),
+    "lora_pages_copy": ([_P, _I64, _I32, _P, _P, _I32, _P], _I32),
+    "lora_page_table_remap": ([_P, _I32, _P, _P, _I64, _P], _I32),
+    "lora_kv_append": ([_P, _P, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
+    "lora_kv_attn_plan": ([_P, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32], _I32),
+    "lora_kv_attn": ([_P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P], _I32),
+    "lora_kv_create": ([_P, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
+    "lora_kv_extend": ([_P, _P, _P, _I32, _P], _I32),
+    "lora_kv_fork": ([_P, _I32, _P, _I32, _P], _I32),
+    "lora_kv_truncate": ([_P, _I32, _I32, _P], _I32),
+    "lora_kv_free": ([_P, _P, _I32, _P], _I32),
+    "lora_kv_compact": ([_P, _P, _P], _I32),
+    "lora_kv_trim": ([_P, _I32, _P], _I32),
+    "lora_kv_seq": ([_P, _I32, _P, _P, _P], _I32),
+    "lora_kv_get_stats": ([_P, _P], _I32),
+    "lora_kv_get_view": ([_P, _P], _I32),
+    "lora_kv_destroy": ([_P], None),
 }
 LORA_DEBUG_BAD_PAGE, LORA_DEBUG_BAD_ADAPTER, LORA_DEBUG_BAD_RANK = 1, 2, 4
 LORA_DEBUG_BAD_TOKEN, LORA_DEBUG_BAD_ITEM = 8, 16
@@ -471,7 +515,10 @@ class Pool:
                                           _dptr(src_scales), _stream(stream)))
 
     def close(self):
+        """Destroys the pool, and before it every KvCache over it."""
         if self._h:
+            for box in self.__dict__.pop("_kv_handles", []):
+                _kv_destroy(box)
             lib().lora_pool_destroy(self._h)
             self._h = None
 
@@ -644,3 +691,352 @@ def prepare_bgmv_fused(w: Weights, token_adapter, x, y, v=None, order: int = LOR
     return Prepared("lora_bgmv_fused", (ctypes.byref(d), _dptr(token_adapter),
                                         int(token_adapter.numel()), _dptr(token_order), n_ord,
                                         order, _dptr(x), _dptr(v), _dptr(y), _stream(stream)), keep)
+
+
+# ---------------------------------------------------------------- 4-bit base projection, paged KV cache
+# These calls take strides from their tensors, so they check what a bare address cannot say: the
+# type, a contiguous last dimension, and that every tensor is on the device the call runs on.
+def _refuse(message: str):
+    raise LoraError(LORA_EINVAL, message)
+
+
+def _tensors(device, *named):
+    """Checks (name, tensor, dtype) triples; None tensors pass."""
+    for name, t, dtype in named:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            _refuse(f"{name} is {t.dtype}, not {dtype}")
+        if t.device != device:
+            _refuse(f"{name} is on {t.device}, not {device}")
+        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+            _refuse(f"{name}'s last dimension is not contiguous")
+
+
+def _flat(name, t):
+    if not t.is_contiguous():
+        _refuse(f"{name} is not contiguous")
+
+
+class _On:
+    """The device of a call made current (a launch goes to the current device), and its stream."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            _refuse(f"tensors must be on a GPU, not {device}")
+        cuda = _torch().cuda
+        self._guard = None if device.index == cuda.current_device() else cuda.device(device)
+        self._device, self._arg = device, stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        s = _torch().cuda.current_stream(self._device) if self._arg is None else self._arg
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def lora_w4_bytes(n: int, k: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().lora_w4_bytes(n, k, ctypes.byref(out)))
+    return int(out.value)
+
+
+def lora_w4_pack(rows, twos_complement: bool = False, stream=None):
+    """Tiled codes [ceil(n/16), ceil(k/128), 64, 16] of row-major ones: rows uint8 [n, k/2] on the
+    device, element 2i in the low nibble."""
+    torch = _torch()
+    _tensors(rows.device, ("rows", rows, torch.uint8))
+    _flat("rows", rows)
+    n, k = int(rows.shape[0]), int(rows.shape[1]) * 2
+    lora_w4_bytes(n, k)
+    with _On(rows.device, stream) as s:
+        codes = torch.empty((-(-n // 16), -(-k // 128), 64, 16), dtype=torch.uint8, device=rows.device)
+        _check(lib().lora_w4_pack(n, k, int(bool(twos_complement)), _dptr(rows), _dptr(codes), s))
+    return codes
+
+
+class W4Weights:
+    """4-bit weights of an n x k projection and their lora_w4_weights descriptor: codes as
+    lora_w4_pack gives them, scales and optional zeros [k / group, n] fp32 or bf16."""
+
+    def __init__(self, n: int, k: int, group: int, codes, scales, zeros=None):
+        torch = _torch()
+        if scales.dtype not in (torch.float32, torch.bfloat16):
+            _refuse(f"scales are {scales.dtype}, not float32 or bfloat16")
+        _tensors(codes.device, ("codes", codes, torch.uint8), ("scales", scales, scales.dtype),
+                 ("zeros", zeros, scales.dtype))
+        for name, t in (("codes", codes), ("scales", scales), ("zeros", zeros)):
+            if t is not None:
+                _flat(name, t)
+        if codes.numel() != lora_w4_bytes(n, k):
+            _refuse(f"codes hold {codes.numel()} bytes, {n} x {k} needs {lora_w4_bytes(n, k)}")
+        for name, t in (("scales", scales), ("zeros", zeros)):
+            if t is not None and (group <= 0 or t.numel() != k // group * n):
+                _refuse(f"{name} hold {t.numel()} values, not [{k} / {group}, {n}]")
+        self.n, self.k, self.group = n, k, group
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.desc = lora_w4_weights(n, k, group, LORA_BF16 if scales.dtype == torch.bfloat16 else LORA_F32,
+                                    _dptr(codes), _dptr(scales), _dptr(zeros))
+
+
+def lora_base_w4(x, w: W4Weights, y, stream=None):
+    """y [m, n] = x [m, k] W^T; x and y may be column blocks of wider arrays (row strides kept)."""
+    torch = _torch()
+    dev = w.codes.device
+    _tensors(dev, ("x", x, torch.bfloat16), ("y", y, torch.bfloat16))
+    m = int(x.shape[0])
+    if tuple(x.shape) != (m, w.k) or tuple(y.shape) != (m, w.n):
+        _refuse(f"x {tuple(x.shape)} and y {tuple(y.shape)} for weights of {w.n} x {w.k}")
+    with _On(dev, stream) as s:
+        _check(lib().lora_base_w4(LORA_BF16, m, ctypes.byref(w.desc), x.data_ptr(),
+                                  x.stride(0) if m > 1 else w.k + (-w.k) % 8, y.data_ptr(),
+                                  y.stride(0) if m > 1 else w.n + (-w.n) % 8, s))
+
+
+class KvView:
+    """A paged KV cache as the kernels read it: k and v [num_pages, kv_heads, page_tokens, head_dim] bf16
+    tensors of the same strides (views of one storage, usually), page_table int32 [num_seqs, max_pages]."""
+
+    def __init__(self, k, v, page_table):
+        torch = _torch()
+        _tensors(k.device, ("k", k, torch.bfloat16), ("v", v, torch.bfloat16), ("page_table", page_table, torch.int32))
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            _refuse(f"k {tuple(k.shape)} {k.stride()} and v {tuple(v.shape)} {v.stride()} differ or are not 4-d")
+        if page_table.dim() != 2:
+            _refuse("page_table is [num_seqs, max_pages]")
+        _flat("page_table", page_table)
+        self.k, self.v, self.page_table = k, v, page_table
+        pages, heads, tokens, dim = (int(n) for n in k.shape)
+        ps, hs, ts = (st if n > 1 else 0 for n, st in zip(k.shape[:3], k.stride()))
+        self.desc = lora_kv_view(LORA_BF16, dim, heads, tokens, pages, int(page_table.shape[0]), int(page_table.shape[1]),
+                                 0, _dptr(k), _dptr(v), ps, hs, ts, _dptr(page_table))
+
+    @property
+    def device(self):
+        return self.k.device
+
+
+def lora_pages_copy(storage, src, dst, stream=None):
+    """Copies page src[i] to page dst[i]; storage [num_pages, ...] contiguous, src and dst int32 on its device."""
+    torch = _torch()
+    _tensors(storage.device, ("src", src, torch.int32), ("dst", dst, torch.int32))
+    for name, t in (("storage", storage), ("src", src), ("dst", dst)):
+        _flat(name, t)
+    if src.numel() != dst.numel():
+        _refuse(f"{src.numel()} source and {dst.numel()} destination pages")
+    pages = int(storage.shape[0])
+    page_bytes = storage.numel() // max(pages, 1) * storage.element_size()
+    with _On(storage.device, stream) as s:
+        _check(lib().lora_pages_copy(storage.data_ptr(), page_bytes, pages, src.data_ptr(), dst.data_ptr(),
+                                     src.numel(), s))
+
+
+def lora_page_table_remap(remap, table_in, table_out, stream=None):
+    """table_out = remap[table_in], entries outside [0, len(remap)) kept; int32 on one device."""
+    torch = _torch()
+    _tensors(remap.device, ("remap", remap, torch.int32), ("table_in", table_in, torch.int32),
+             ("table_out", table_out, torch.int32))
+    for name, t in (("remap", remap), ("table_in", table_in), ("table_out", table_out)):
+        _flat(name, t)
+    if table_in.numel() != table_out.numel():
+        _refuse(f"tables of {table_in.numel()} and {table_out.numel()} entries")
+    with _On(remap.device, stream) as s:
+        _check(lib().lora_page_table_remap(remap.data_ptr(), remap.numel(), table_in.data_ptr(), table_out.data_ptr(),
+                                           table_in.numel(), s))
+
+
+def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None):
+    """Writes k_new, v_new [T, kv_heads, head_dim] at positions token_pos [T] of sequences token_seq [T]."""
+    torch = _torch()
+    _tensors(view.device, ("k_new", k_new, torch.bfloat16), ("v_new", v_new, torch.bfloat16),
+             ("token_seq", token_seq, torch.int32), ("token_pos", token_pos, torch.int32))
+    d = view.desc
+    n = int(k_new.shape[0])
+    want = (n, d.kv_heads, d.head_dim)
+    if tuple(k_new.shape) != want or tuple(v_new.shape) != want or token_seq.numel() != n or token_pos.numel() != n:
+        _refuse(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}, {token_seq.numel()} sequences and "
+                f"{token_pos.numel()} positions: {want} wanted")
+    ts, hs = _row_strides(k_new)
+    if _row_strides(v_new) != (ts, hs):
+        _refuse(f"k_new and v_new have strides {k_new.stride()} and {v_new.stride()}")
+    _flat("token_seq", token_seq)
+    _flat("token_pos", token_pos)
+    with _On(view.device, stream) as s:
+        _check(lib().lora_kv_append(ctypes.byref(d), k_new.data_ptr(), v_new.data_ptr(), ts, hs, token_seq.data_ptr(),
+                                    token_pos.data_ptr(), n, s))
+
+
+def _row_strides(t):
+    """Token and head strides of [T, heads, dim] (0 for a dimension of one: its stride says nothing)."""
+    return tuple(st if n > 1 and t.numel() else 0 for n, st in zip(t.shape[:2], t.stride()))
+
+
+class AttnPlan:
+    """A batch's attention plan: the host items, and after ``to(device)`` the device copy and workspace."""
+
+    def __init__(self, desc: lora_attn_plan, items: np.ndarray):
+        self.desc, self.host_items = desc, items
+        self.items = self.workspace = None
+
+    def to(self, device) -> "AttnPlan":
+        """Uploads the items and allocates a workspace (calls that share the plan must not overlap)."""
+        torch = _torch()
+        self.items = torch.from_numpy(self.host_items).to(device)
+        n = self.desc.workspace_bytes
+        self.workspace = torch.empty(n // 4, dtype=torch.float32, device=device) if n else None
+        return self
+
+
+def lora_kv_attn_plan(q_starts, seqs, kv_lens, q_heads: int, kv_heads: int, head_dim: int, causal: bool = True,
+                      window: int = 0, max_parts: int = 0, num_seqs: Optional[int] = None,
+                      max_kv: int = 2**31 - 1) -> AttnPlan:
+    """Plan of a batch: request r has tokens q_starts[r] .. q_starts[r + 1] of q, sequence seqs[r] of kv_lens[r]
+    positions.  num_seqs, max_kv: the bounds to check against (lora_kv_attn checks the view's on the device)."""
+    starts, sq, kv = _i32(q_starts), _i32(seqs), _i32(kv_lens)
+    if starts.size < 1 or sq.size != starts.size - 1 or kv.size != sq.size:
+        _refuse(f"{starts.size} starts, {sq.size} sequences and {kv.size} lengths")
+    plan = lora_attn_plan()
+    args = (_np_ptr(starts), _np_ptr(sq), _np_ptr(kv), sq.size, 2**31 - 1 if num_seqs is None else num_seqs, max_kv,
+            q_heads, kv_heads, head_dim, LORA_ATTN_CAUSAL if causal else 0, window, max_parts, ctypes.byref(plan))
+    _check(lib().lora_kv_attn_plan(*args, None, 0))
+    n = plan.num_row_items + plan.num_tile_items + plan.num_joins
+    items = np.zeros((max(n, 1), 8), np.int32)
+    _check(lib().lora_kv_attn_plan(*args, _np_ptr(items), n))
+    return AttnPlan(plan, items[:n])
+
+
+def lora_kv_attn(view: KvView, plan: AttnPlan, q, out, lse=None, scale: Optional[float] = None, workspace=None,
+                 stream=None):
+    """out [T, q_heads, head_dim] (and lse [T, q_heads] fp32) of q over the cache; scale defaults to
+    head_dim ** -0.5, workspace to the plan's own."""
+    torch = _torch()
+    if plan.items is None:
+        _refuse("the plan has not been uploaded: call plan.to(device)")
+    p = plan.desc
+    ws = plan.workspace if workspace is None else workspace
+    _tensors(view.device, ("q", q, torch.bfloat16), ("out", out, torch.bfloat16), ("lse", lse, torch.float32),
+             ("the plan's items", plan.items, torch.int32))
+    want = (p.q_heads, p.head_dim)
+    if q.dim() != 3 or q.shape != out.shape or tuple(q.shape[1:]) != want or q.shape[0] < p.num_tokens:
+        _refuse(f"q {tuple(q.shape)} and out {tuple(out.shape)}: [{p.num_tokens} or more, {want[0]}, {want[1]}] wanted")
+    if lse is not None:
+        _flat("lse", lse)
+        if lse.dim() != 2 or lse.shape[0] < p.num_tokens or lse.shape[1] != p.q_heads:
+            _refuse(f"lse {tuple(lse.shape)}: [{p.num_tokens} or more, {p.q_heads}] wanted")
+    if ws is not None:
+        _flat("workspace", ws)
+        if ws.device != view.device:
+            _refuse(f"workspace is on {ws.device}, not {view.device}")
+    wp, wb = _ws_args(ws)
+    qs, os_ = _row_strides(q), _row_strides(out)
+    with _On(view.device, stream) as s:
+        _check(lib().lora_kv_attn(ctypes.byref(view.desc), ctypes.byref(p), plan.items.data_ptr(), q.data_ptr(), *qs,
+                                  out.data_ptr(), *os_, _dptr(lse), p.head_dim ** -0.5 if scale is None else scale,
+                                  wp, wb, s))
+
+
+def _kv_destroy(box: list):
+    if box[0]:
+        lib().lora_kv_destroy(box[0])
+        box[0] = None
+
+
+class KvCache:
+    """lora_kv: sequences over the pages of a Pool (which may hold adapters too).  The pool's storage is a
+    bf16 tensor [num_pages, page_rows, row_width]; the cache owns a device page table it makes itself."""
+
+    def __init__(self, pool: Pool, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int, host_only: bool = False):
+        torch = _torch()
+        self.pool, self.max_pages, self._host_only = pool, max_pages, host_only
+        self.page_table = None
+        h = ctypes.c_void_p()
+        if host_only:
+            _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, None, LORA_KV_HOST_ONLY,
+                                        ctypes.byref(h)))
+            self._own(h)
+            return
+        dev = pool.storage.device
+        with _On(dev, None):
+            self.page_table = torch.empty((max_seqs, max_pages), dtype=torch.int32, device=dev)
+            _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, _dptr(self.page_table), 0,
+                                        ctypes.byref(h)))
+        self._own(h)
+        tokens, size = self.stats()["page_tokens"], kv_heads * head_dim
+        flat = pool.storage.view(pool.storage.shape[0], -1)
+        part = lambda i: flat[:, i * size * tokens:(i + 1) * size * tokens].view(-1, kv_heads, tokens, head_dim)
+        self.view = KvView(part(0), part(1), self.page_table)
+
+    def _own(self, handle):
+        """The handle in a box that the pool knows too: whichever goes first, the cache is destroyed before the pool."""
+        self._box = [handle]
+        self.pool.__dict__.setdefault("_kv_handles", []).append(self._box)
+
+    @property
+    def _h(self):
+        return self._box[0]
+
+    def _call(self, name, *args, stream=None):
+        if self._host_only:
+            _check(getattr(lib(), name)(self._h, *args, None))
+            return
+        with _On(self.page_table.device, stream) as s:
+            _check(getattr(lib(), name)(self._h, *args, s))
+
+    def extend(self, seqs, new_tokens, stream=None):
+        a, b = _i32(seqs), _i32(new_tokens)
+        if a.size != b.size:
+            _refuse(f"{a.size} sequences and {b.size} counts")
+        self._call("lora_kv_extend", _np_ptr(a), _np_ptr(b), a.size, stream=stream)
+
+    def fork(self, src: int, dst, stream=None):
+        a = _i32(dst)
+        self._call("lora_kv_fork", src, _np_ptr(a), a.size, stream=stream)
+
+    def truncate(self, seq: int, new_len: int, stream=None):
+        self._call("lora_kv_truncate", seq, new_len, stream=stream)
+
+    def free(self, seqs, stream=None):
+        a = _i32(seqs)
+        self._call("lora_kv_free", _np_ptr(a), a.size, stream=stream)
+
+    def compact(self, stream=None) -> int:
+        n = ctypes.c_int32(0)
+        self._call("lora_kv_compact", ctypes.byref(n), stream=stream)
+        return n.value
+
+    def trim(self, wait: bool = False) -> int:
+        n = ctypes.c_int32(0)
+        _check(lib().lora_kv_trim(self._h, int(wait), ctypes.byref(n)))
+        return n.value
+
+    def length(self, seq: int) -> int:
+        n = ctypes.c_int32(0)
+        _check(lib().lora_kv_seq(self._h, seq, ctypes.byref(n), None, None))
+        return n.value
+
+    def pages(self, seq: int) -> np.ndarray:
+        ids, n = np.empty(self.max_pages, np.int32), ctypes.c_int32(0)
+        _check(lib().lora_kv_seq(self._h, seq, None, _np_ptr(ids), ctypes.byref(n)))
+        return ids[: n.value].copy()
+
+    def stats(self) -> dict:
+        st = lora_kv_stats()
+        _check(lib().lora_kv_get_stats(self._h, ctypes.byref(st)))
+        return {f: getattr(st, f) for f, _ in lora_kv_stats._fields_}
+
+    def close(self):
+        box = getattr(self, "_box", None)
+        if box is not None:
+            _kv_destroy(box)
+            boxes = self.pool.__dict__.get("_kv_handles", [])
+            boxes[:] = [b for b in boxes if b is not box]
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

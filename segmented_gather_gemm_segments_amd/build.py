@@ -21,9 +21,13 @@ LIB = os.path.join(HERE, "liblora_sgmv.so")
 DEBUG_LIB = os.path.join(HERE, "liblora_sgmv_debug.so")
 SOURCES = [os.path.join(HERE, "csrc", "host.cpp"), os.path.join(HERE, "csrc", "kernels.hip"),
            os.path.join(HERE, "csrc", "base_gemm.hip"), os.path.join(HERE, "csrc", "residency.hip"),
-           os.path.join(HERE, "csrc", "probe.hip")]
+           os.path.join(HERE, "csrc", "probe.hip"), os.path.join(HERE, "csrc", "base_w4.hip"),
+           os.path.join(HERE, "csrc", "kv_host.cpp"), os.path.join(HERE, "csrc", "kv_pages.hip"),
+           os.path.join(HERE, "csrc", "kv_attn.hip")]
 HEADERS = [os.path.join(ROOT, "include", "lora_sgmv.h"), os.path.join(ROOT, "include", "lora_probe.h"),
-           os.path.join(HERE, "csrc", "lora_internal.h")]
+           os.path.join(ROOT, "include", "lora_w4.h"), os.path.join(ROOT, "include", "lora_kv.h"),
+           os.path.join(HERE, "csrc", "lora_internal.h"), os.path.join(HERE, "csrc", "kv_internal.h"),
+           os.path.join(HERE, "csrc", "kv_debug.h")]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",

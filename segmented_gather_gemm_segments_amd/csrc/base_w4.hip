@@ -1,0 +1,236 @@
+// Base projection y = x W^T from 4-bit weights with group scales (lora_w4.h).
+//
+// Per group of k the kernel forms t = sum (128 + u) x and xs = sum x on the
+// matrix cores and adds s (t - (128 + z) xs) to the output's fp32 sum.  128 + u
+// is exact in bf16 (8 significant bits, unit spacing from 128 to 256), and its
+// bit pattern is 0x4300 | u: one AND-OR turns two nibbles of a code word into
+// two operand elements, so a word of 8 codes costs 7 vector instructions.  xs
+// comes from the same x fragments against a constant operand of ones.
+//
+// Bound by HBM: at 4 bits a weight the codes are nearly all the bytes while the
+// tokens of a decode batch are few.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "lora_internal.h"
+#include "lora_w4.h"
+
+using namespace lora;
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+
+constexpr int kTileBytes = 1024;   // codes of 16 rows x 128 k
+constexpr int kTileK = 128;
+constexpr int kWaves = 8;
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));  // nearest even
+}
+
+// Four consecutive scales (or zero points) of one group, widened.
+__device__ __forceinline__ f32x4_t load4(const float *p) { return *reinterpret_cast<const f32x4_t *>(p); }
+__device__ __forceinline__ f32x4_t load4(const uint16_t *p) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+  return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                 __uint_as_float(u.y & 0xffff0000u)};
+}
+
+// The operand of one word of codes: 128 + u, 8 elements.
+__device__ __forceinline__ bf16x8_t widen(uint32_t w) {
+  uint4 o;
+  o.x = (w & 0x000f000fu) | 0x43004300u;
+  o.y = ((w >> 4) & 0x000f000fu) | 0x43004300u;
+  o.z = ((w >> 8) & 0x000f000fu) | 0x43004300u;
+  o.w = ((w >> 12) & 0x000f000fu) | 0x43004300u;
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+
+// One workgroup: 16 rows of W (one row tile) and 16 MT tokens.  Its waves take
+// the tile columns in turn; their fp32 sums are added in wave order through
+// LDS.
+template <int MT, int G, typename S, bool Z>
+__global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int k, int col_tiles,
+                                                              const uint8_t *__restrict__ codes,
+                                                              const S *__restrict__ scales,
+                                                              const S *__restrict__ zeros,
+                                                              const uint16_t *__restrict__ x, int64_t x_stride,
+                                                              uint16_t *__restrict__ y, int64_t y_stride) {
+  __shared__ f32x4_t red[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int fr = lane & 15, fg = lane >> 4;
+  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (16 * MT);
+  const int nrow = min(n0 + 4 * fg, n - 4);  // rows of this lane's results (clamped: results past n are not stored)
+  const uint8_t *cp = codes + (int64_t)blockIdx.x * col_tiles * kTileBytes + lane * 16;
+  const uint16_t *xp[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xp[i] = x + (int64_t)min(t0 + 16 * i + fr, m - 1) * x_stride + fg * 8;
+  const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
+  f32x4_t sum[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  for (int kt = wave; kt < col_tiles; kt += kWaves) {
+    const uint4 c = *reinterpret_cast<const uint4 *>(cp + (int64_t)kt * kTileBytes);
+    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+    bf16x8_t xf[MT][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k0 = kt * kTileK + s * 32;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (k0 < k) q = *reinterpret_cast<const uint4 *>(xp[i] + k0);  // uniform: k is a multiple of 32
+        xf[i][s] = __builtin_bit_cast(bf16x8_t, q);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kTileK / G; ++g) {
+      const int kg = kt * (kTileK / G) + g;
+      if (kg * G >= k) break;
+      const f32x4_t sc = load4(scales + (int64_t)kg * n + nrow);
+      f32x4_t off = f32x4_t{136.f, 136.f, 136.f, 136.f};
+      if constexpr (Z) off = load4(zeros + (int64_t)kg * n + nrow) + 128.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        f32x4_t t = f32x4_t{0.f, 0.f, 0.f, 0.f}, xs = t;
+#pragma unroll
+        for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
+          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(cw[s]), xf[i][s], t, 0, 0, 0);
+          xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf[i][s], xs, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[i][j] += sc[j] * (t[j] - off[j] * xs[0]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    __syncthreads();
+    red[wave][lane] = sum[i];
+    __syncthreads();
+    if (wave == i % kWaves) {
+      f32x4_t a = red[0][lane];
+      for (int w = 1; w < kWaves; ++w) a += red[w][lane];
+      const int t = t0 + 16 * i + fr, col = n0 + 4 * fg;
+      if (t < m && col < n) {
+        uint2 o = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
+        *reinterpret_cast<uint2 *>(y + (int64_t)t * y_stride + col) = o;
+      }
+    }
+  }
+}
+
+// Thread: one 32-bit word of the tiled codes.
+__global__ __launch_bounds__(256) void w4_pack_kernel(int n, int k, int col_tiles, int64_t words, uint32_t flip,
+                                                      const uint32_t *__restrict__ rows,
+                                                      uint32_t *__restrict__ codes) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= words) return;
+  const int w = (int)(i & 3), lane = (int)((i >> 2) & 63);
+  const int64_t tile = i >> 8;
+  const int row = (int)(tile / col_tiles) * 16 + (lane & 15);
+  const int k0 = (int)(tile % col_tiles) * kTileK + w * 32 + (lane >> 4) * 8;
+  uint32_t out = 0x88888888u;
+  if (row < n && k0 < k) {
+    const uint32_t src = rows[((int64_t)row * k + k0) >> 3] ^ flip;  // element e in nibble e
+    out = 0;
+    for (int e = 0; e < 8; ++e) out |= ((src >> (4 * e)) & 15u) << (4 * ((e >> 1) + 4 * (e & 1)));
+  }
+  codes[i] = out;
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+struct W4Call {
+  int m, n, k, col_tiles;
+  const lora_w4_weights *w;
+  const uint16_t *x;
+  int64_t xs;
+  uint16_t *y;
+  int64_t ys;
+  hipStream_t stream;
+};
+
+template <int MT, int G, typename S, bool Z>
+void launch(const W4Call &c) {
+  hipLaunchKernelGGL((base_w4_kernel<MT, G, S, Z>), dim3((c.n + 15) / 16, (c.m + 16 * MT - 1) / (16 * MT)),
+                     dim3(64 * kWaves), 0, c.stream, c.m, c.n, c.k, c.col_tiles, (const uint8_t *)c.w->codes,
+                     (const S *)c.w->scales, (const S *)c.w->zeros, c.x, c.xs, c.y, c.ys);
+}
+template <int MT, int G>
+void pick_scale(const W4Call &c) {
+  if (c.w->scale_dtype == LORA_BF16)
+    c.w->zeros ? launch<MT, G, uint16_t, true>(c) : launch<MT, G, uint16_t, false>(c);
+  else
+    c.w->zeros ? launch<MT, G, float, true>(c) : launch<MT, G, float, false>(c);
+}
+template <int MT>
+void pick_group(const W4Call &c) {
+  if (c.w->group == 32) pick_scale<MT, 32>(c);
+  else if (c.w->group == 64) pick_scale<MT, 64>(c);
+  else pick_scale<MT, 128>(c);
+}
+
+}  // namespace
+
+extern "C" lora_status lora_w4_bytes(int32_t n, int32_t k, int64_t *bytes) {
+  if (!bytes) return fail(LORA_EINVAL, "null bytes");
+  *bytes = 0;
+  if (n <= 0 || k <= 0) return fail(LORA_EINVAL, "4-bit weights n=%d k=%d", n, k);
+  *bytes = (int64_t)kTileBytes * (((int64_t)n + 15) / 16) * (((int64_t)k + kTileK - 1) / kTileK);
+  return ok();
+}
+
+extern "C" lora_status lora_w4_pack(int32_t n, int32_t k, int32_t twos_complement, const void *rows, void *codes,
+                                    hipStream_t stream) {
+  int64_t bytes = 0;
+  lora_status st = lora_w4_bytes(n, k, &bytes);
+  if (st != LORA_OK) return st;
+  if (n % 8 || k % 32) return fail(LORA_EUNSUPPORTED, "4-bit weights need n a multiple of 8 and k of 32");
+  if (twos_complement != 0 && twos_complement != 1) return fail(LORA_EINVAL, "twos_complement is 0 or 1");
+  if (!rows || !codes) return fail(LORA_EINVAL, "null pointer");
+  if (!aligned16(rows) || !aligned16(codes)) return fail(LORA_EINVAL, "device arrays must be 16-byte aligned");
+  const int64_t words = bytes / 4, blocks = (words + 255) / 256;
+  if (blocks > INT32_MAX) return fail(LORA_EUNSUPPORTED, "4-bit weights too large");
+  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, n, k, (k + kTileK - 1) / kTileK,
+                     words, twos_complement ? 0x88888888u : 0u, (const uint32_t *)rows, (uint32_t *)codes);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return hip_fail(e, "4-bit pack launch");
+  return ok();
+}
+
+extern "C" lora_status lora_base_w4(int32_t dtype, int32_t m, const lora_w4_weights *w, const void *x,
+                                    int64_t x_stride, void *y, int64_t y_stride, hipStream_t stream) {
+  if (!w) return fail(LORA_EINVAL, "null weights");
+  if (dtype != LORA_BF16) return fail(LORA_EUNSUPPORTED, "4-bit base projection supports bf16 activations only");
+  if (m < 0 || w->n <= 0 || w->k <= 0) return fail(LORA_EINVAL, "4-bit base projection m=%d n=%d k=%d", m, w->n, w->k);
+  if (w->group != 32 && w->group != 64 && w->group != 128)
+    return fail(LORA_EUNSUPPORTED, "group must be 32, 64 or 128 (got %d)", w->group);
+  if (w->n % 8 || w->k % w->group)
+    return fail(LORA_EUNSUPPORTED, "4-bit base projection needs n a multiple of 8 and k of the group");
+  if (w->scale_dtype != LORA_F32 && w->scale_dtype != LORA_BF16)
+    return fail(LORA_EUNSUPPORTED, "scale dtype %d", w->scale_dtype);
+  if (x_stride < w->k || y_stride < w->n || x_stride % 8 || y_stride % 8)
+    return fail(LORA_EINVAL, "row strides must be multiples of 8 of at least k and n (got %lld and %lld)",
+                (long long)x_stride, (long long)y_stride);
+  if (m == 0) return ok();
+  if (!w->codes || !w->scales || !x || !y) return fail(LORA_EINVAL, "null pointer");
+  if (!aligned16(w->codes) || !aligned16(w->scales) || !aligned16(w->zeros) || !aligned16(x) || !aligned16(y))
+    return fail(LORA_EINVAL, "device arrays must be 16-byte aligned");
+  const int mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+  if ((m + 16 * mt - 1) / (16 * mt) > 65535) return fail(LORA_EUNSUPPORTED, "too many tokens");
+  const W4Call c{m, w->n, w->k, (w->k + kTileK - 1) / kTileK, w, (const uint16_t *)x, x_stride, (uint16_t *)y,
+                 y_stride, stream};
+  if (mt == 1) pick_group<1>(c);
+  else if (mt == 2) pick_group<2>(c);
+  else pick_group<4>(c);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return hip_fail(e, "4-bit base projection launch");
+  return ok();
+}

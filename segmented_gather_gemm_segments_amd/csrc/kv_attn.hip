@@ -1,0 +1,405 @@
+// Attention of new tokens over the paged KV cache (lora_kv.h).
+//
+// One pass over the positions with the running maximum m and sum l of each row's
+// softmax: for a tile of positions, S = scale log2(e) K Q^T, m' = max(m, max S),
+// P = 2^(S - m'), l = l 2^(m - m') + sum P, O = O 2^(m - m') + V^T P.  Products run on
+// the matrix cores with positions as rows (S^T = K Q^T, O^T = V^T P^T): a lane then
+// holds one row's scores in its registers, so maximum and sum are register
+// operations and two exchanges between lane groups, and P^T is already the operand that
+// its product with V needs, up to an order of positions that V's operand is read in too.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kv_internal.h"
+#include "kv_debug.h"
+
+using namespace lora;
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f;
+
+struct Args {
+  lora_kv_view kv;
+  const lora_attn_item *items;
+  const uint16_t *q;
+  uint16_t *out;
+  float *lse;
+  float *part_o;    // [num_part_rows][kv_heads][head_dim]: normalised results of one range
+  float *part_lse;  // [num_part_rows][kv_heads]: base-2 logarithm of its sum
+  int64_t q_ts, q_hs, o_ts, o_hs;
+  float scale2;     // scale log2(e)
+  int32_t num_items, q_heads, group, causal, window, num_tokens, num_part_rows;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));  // nearest even
+}
+__device__ __forceinline__ bool not_finite(uint16_t b) { return (b & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ float bf16_val(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// Maximum or sum over the four lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float max_groups(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_groups(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Whether an item read from the device lies within the plan and the view.
+__device__ __forceinline__ bool good_item(const Args &a, const lora_attn_item &it, int max_rows) {
+  return it.rows >= 1 && it.rows <= max_rows && it.row0 >= 0 && it.q_begin >= 0 && it.row0 <= INT32_MAX - max_rows &&
+         it.q_begin + (int64_t)(it.row0 + it.rows - 1) / a.group < a.num_tokens && it.seq >= 0 &&
+         it.seq < a.kv.num_seqs && it.kv_begin >= 0 && it.kv_begin <= it.kv_end &&
+         it.kv_end <= a.kv.max_pages * a.kv.page_tokens && it.part >= -1 &&
+         (int64_t)it.part + it.rows <= a.num_part_rows + (it.part < 0 ? (int64_t)INT32_MAX : 0);
+}
+
+// Element offset of position p's row of KV head h, or -1 where no page holds it.
+__device__ __forceinline__ int64_t kv_row(const lora_kv_view &kv, int seq, int h, int p) {
+  const int pi = p / kv.page_tokens;
+  const int page = kv.page_table[(int64_t)seq * kv.max_pages + pi];
+  KV_CHECK((unsigned)page < (unsigned)kv.num_pages, LORA_DEBUG_BAD_PAGE);
+  if ((unsigned)page >= (unsigned)kv.num_pages) return -1;
+  return page * kv.page_stride + h * kv.head_stride + (p - pi * kv.page_tokens) * kv.token_stride;
+}
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+  const int lo = __shfl((int)(uint32_t)v, lane), hi = __shfl((int)(v >> 32), lane);
+  return (int64_t)(uint32_t)lo | ((int64_t)hi << 32);
+}
+
+// ----------------------------------------------------------------- row items
+// Up to 16 rows (the query heads of one KV head, for one or a few tokens) against
+// positions [kv_begin, kv_end).  Four waves take tiles of 32 positions in turn, each
+// with a softmax of its own, joined at the end in wave order.
+constexpr int kRowWaves = 4;
+constexpr int kRowKv = 32;
+
+template <int DP>
+struct RowShared {
+  static constexpr int kLd = DP + 16;  // elements; the pad spreads the four rows of a transposed read over the banks
+  union {
+    uint16_t v[kRowWaves][kRowKv * kLd];
+    float o[kRowWaves][16][DP];
+  };
+  float m[kRowWaves][16], l[kRowWaves][16];
+};
+
+template <int DP>
+__global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
+  constexpr int KS = DP / 32, DT = DP / 16;
+  using Sh = RowShared<DP>;
+  __shared__ Sh sh;
+  const lora_kv_view &kv = a.kv;
+  const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
+  const lora_attn_item it = a.items[ii];
+  if (!good_item(a, it, LORA_ATTN_ROWS)) {
+    KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int fr = lane & 15, fg = lane >> 4;
+  const int D = kv.head_dim, nch = D >> 3;
+
+  // this lane's row (a row past the item's computes row 0's token and is not stored)
+  const int row = it.row0 + (fr < it.rows ? fr : 0);
+  const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
+  const int64_t pos = (int64_t)it.pos0 + tok;
+  const int64_t hi64 = a.causal ? pos : INT32_MAX, lo64 = a.window ? pos - a.window + 1 : 0;
+  const int hi = (int)max(hi64, (int64_t)-1), lo = (int)min(max(lo64, (int64_t)0), (int64_t)INT32_MAX);
+  bf16x8_t qf[KS];
+  const uint16_t *qp = a.q + (it.q_begin + tok) * a.q_ts + head * a.q_hs;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (s * 4 + fg < nch) u = *reinterpret_cast<const uint4 *>(qp + (s * 4 + fg) * 8);
+    qf[s] = __builtin_bit_cast(bf16x8_t, u);
+  }
+
+  f32x4_t o[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  uint16_t *vs = sh.v[wave];
+
+  const int first = it.kv_begin / kRowKv * kRowKv;
+  for (int64_t t0l = first + wave * kRowKv; t0l < it.kv_end; t0l += kRowWaves * kRowKv) {
+    const int t0 = (int)t0l;
+    // lane l & 31: the tile's position t0 + (l & 31)
+    const int pt = t0 + (lane & 31);
+    int64_t at = -1;
+    if (pt >= it.kv_begin && pt < it.kv_end) at = kv_row(kv, it.seq, h, pt);
+    const uint32_t there = (uint32_t)__ballot(at >= 0);  // bit i: position t0 + i exists
+    // K: operand rows are positions; rows that do not exist are zeros
+    f32x4_t sc[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int64_t ka = shfl64(at, 16 * half + fr);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (ka >= 0 && s * 4 + fg < nch) u = *reinterpret_cast<const uint4 *>((const uint16_t *)kv.k + ka + (s * 4 + fg) * 8);
+        sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u), qf[s], sc[half], 0, 0, 0);
+      }
+    }
+    // V into LDS as it stands, absent rows and columns past head_dim as zeros
+    bool odd = false;  // a value that is not finite
+    constexpr int CPR = DP / 8, LOADS = kRowKv * CPR / 64;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int c = lane + 64 * i, r = c / CPR, cc = c % CPR;
+      const int64_t va = shfl64(at, r);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (va >= 0 && cc < nch) u = *reinterpret_cast<const uint4 *>((const uint16_t *)kv.v + va + cc * 8);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+      *reinterpret_cast<uint4 *>(vs + r * Sh::kLd + cc * 8) = u;
+    }
+    // scores: element e of this lane is position t0 + 4 fg + e (e < 4) or t0 + 16 + 4 fg + e - 4
+    float s8[8];
+    uint32_t keep = 0;
+    bool hole = false;  // an existing position that this row does not keep
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = (e < 4 ? 4 * fg + e : 16 + 4 * fg + e - 4), p = t0 + i;
+      const bool ex = there >> i & 1, ok = ex && p <= hi && p >= lo;
+      s8[e] = ok ? sc[e >> 2][e & 3] * a.scale2 : -INFINITY;
+      keep |= (uint32_t)ok << e;
+      hole |= ex && !ok;
+    }
+    float mt = s8[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) mt = fmaxf(mt, s8[e]);
+    const float mn = fmaxf(m, max_groups(mt));
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float corr = __builtin_amdgcn_exp2f(m - base);
+    float sum = 0.f, p8[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p8[e] = __builtin_amdgcn_exp2f(s8[e] - base);
+      sum += p8[e];
+    }
+    l = l * corr + sum;
+    m = mn;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[t] *= corr;
+    if (__ballot(odd) && __ballot(hole)) {
+      // some row must not see some value that is not finite, and 0 * inf is NaN: those values are
+      // added where they are kept, term by term, and are zeros in the product
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        for (int g = 0; g < 4; ++g) {
+          const float pv = __shfl(p8[e], 16 * g + fr);
+          const bool ok = __shfl((int)(keep >> e & 1), 16 * g + fr);
+          const uint16_t *vr = vs + (e < 4 ? 4 * g + e : 16 + 4 * g + e - 4) * Sh::kLd + 4 * fg;
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (ok && not_finite(vr[16 * t + j])) o[t][j] += pv * bf16_val(vr[16 * t + j]);
+        }
+      __builtin_amdgcn_wave_barrier();
+      for (int i = lane; i < kRowKv * DP; i += 64) {
+        uint16_t *e = vs + i / DP * Sh::kLd + i % DP;
+        if (not_finite(*e)) *e = 0;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    const bf16x8_t pf = __builtin_bit_cast(
+        bf16x8_t, make_uint4(pack_bf16(p8[0], p8[1]), pack_bf16(p8[2], p8[3]), pack_bf16(p8[4], p8[5]), pack_bf16(p8[6], p8[7])));
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      // transposed reads: a group of 16 lanes names 4 rows x 16 columns, lane i gets column i's 4 values
+      s16x4_t x[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        x[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)(
+            vs + (16 * half + 4 * fg + (fr >> 2)) * Sh::kLd + 16 * t + (fr & 3) * 4));
+      const uint2 x0 = __builtin_bit_cast(uint2, x[0]), x1 = __builtin_bit_cast(uint2, x[1]);
+      o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(x0.x, x0.y, x1.x, x1.y)), pf,
+                                                     o[t], 0, 0, 0);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  l = sum_groups(l);
+
+  // join the waves in order
+  __syncthreads();
+  if (fg == 0) {
+    sh.m[wave][fr] = m;
+    sh.l[wave][fr] = l;
+  }
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sh.o[wave][fr][16 * t + 4 * fg + j] = o[t][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < it.rows * nch; i += 64 * kRowWaves) {
+    const int r = i / nch, c = i % nch;
+    float top = sh.m[0][r];
+    for (int w = 1; w < kRowWaves; ++w) top = fmaxf(top, sh.m[w][r]);
+    float f[kRowWaves], total = 0.f;
+    for (int w = 0; w < kRowWaves; ++w) {
+      f[w] = sh.l[w][r] == 0.f ? 0.f : __builtin_amdgcn_exp2f(sh.m[w][r] - top);  // nothing kept: no weight
+      total += f[w] * sh.l[w][r];
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x = 0.f;
+      for (int w = 0; w < kRowWaves; ++w)
+        if (sh.l[w][r] != 0.f) x += f[w] * sh.o[w][r][8 * c + e];
+      v[e] = x * inv;
+    }
+    const float lse2 = total == 0.f ? -INFINITY : top + log2f(total);
+    if (it.part >= 0) {
+      const int64_t pr = (int64_t)(it.part + r) * kv.kv_heads + h;
+      float *po = a.part_o + pr * D + 8 * c;
+      *reinterpret_cast<f32x4_t *>(po) = f32x4_t{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_t *>(po + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+      if (c == 0) a.part_lse[pr] = lse2;
+    } else {
+      const int rr = it.row0 + r, tk = rr / a.group, hd = h * a.group + rr % a.group;
+      *reinterpret_cast<uint4 *>(a.out + (it.q_begin + tk) * a.o_ts + hd * a.o_hs + 8 * c) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      if (c == 0 && a.lse) a.lse[(int64_t)(it.q_begin + tk) * a.q_heads + hd] = lse2 * kLn2;
+    }
+  }
+}
+
+// ----------------------------------------------------------------- join
+// One thread per 8 columns of a row: the row's parts in order, each weighted with
+// 2^(lse_part - lse).
+__global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
+  const lora_kv_view &kv = a.kv;
+  const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
+  lora_attn_item it = a.items[ii];
+  const int parts = it.part, base = it.kv_begin;
+  it.part = -1;
+  it.kv_begin = it.kv_end = 0;
+  if (!good_item(a, it, LORA_ATTN_TILE_ROWS) || parts < 1 || parts > LORA_ATTN_MAX_PARTS || base < 0 ||
+      base + (int64_t)parts * it.rows > a.num_part_rows) {
+    KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
+    return;
+  }
+  const int D = kv.head_dim, nch = D >> 3;
+  for (int i = threadIdx.x; i < it.rows * nch; i += 256) {
+    const int r = i / nch, c = i % nch;
+    float top = -INFINITY;
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_lse[(int64_t)(base + p * it.rows + r) * kv.kv_heads + h]);
+    float total = 0.f, v[8] = {};
+    for (int p = 0; p < parts; ++p) {
+      const int64_t pr = (int64_t)(base + p * it.rows + r) * kv.kv_heads + h;
+      const float lp = a.part_lse[pr];
+      if (lp == -INFINITY) continue;  // the range kept nothing
+      const float f = __builtin_amdgcn_exp2f(lp - top);
+      total += f;
+      const float *po = a.part_o + pr * D + 8 * c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += f * po[e];
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const float lse2 = total == 0.f ? -INFINITY : top + log2f(total);
+    const int rr = it.row0 + r, tk = rr / a.group, hd = h * a.group + rr % a.group;
+    *reinterpret_cast<uint4 *>(a.out + (it.q_begin + tk) * a.o_ts + hd * a.o_hs + 8 * c) =
+        make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                   pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+    if (c == 0 && a.lse) a.lse[(int64_t)(it.q_begin + tk) * a.q_heads + hd] = lse2 * kLn2;
+  }
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <int DP>
+void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
+  hipLaunchKernelGGL(attn_rows_kernel<DP>, dim3(grid), dim3(64 * kRowWaves), 0, stream, a);
+}
+
+}  // namespace
+
+lora_status lora::kv_attn_debug(uint32_t *flags, int32_t clear) { return kv_debug_word(flags, clear); }
+
+extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, const lora_attn_item *items,
+                                    const void *q, int64_t q_token_stride, int64_t q_head_stride, void *out,
+                                    int64_t out_token_stride, int64_t out_head_stride, float *lse, float scale,
+                                    void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+  lora_status st = check_view(kv);
+  if (st != LORA_OK) return st;
+  if (!plan) return fail(LORA_EINVAL, "null plan");
+  if (plan->kv_heads != kv->kv_heads || plan->head_dim != kv->head_dim)
+    return fail(LORA_EINVAL, "the plan is for %d KV heads of %d, the cache holds %d of %d", plan->kv_heads,
+                plan->head_dim, kv->kv_heads, kv->head_dim);
+  if (plan->q_heads < 1 || plan->q_heads % plan->kv_heads || plan->num_tokens < 0 || plan->num_row_items < 0 ||
+      plan->num_tile_items < 0 || plan->num_joins < 0 || plan->num_part_rows < 0 || plan->window < 0 ||
+      (plan->flags & ~LORA_ATTN_CAUSAL))
+    return fail(LORA_EINVAL, "not a plan");
+  const int64_t strides[4] = {q_token_stride, q_head_stride, out_token_stride, out_head_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s % 8) return fail(LORA_EINVAL, "strides of q and out must be multiples of 8 elements, not negative");
+  if (!std::isfinite(scale)) return fail(LORA_EINVAL, "scale is not finite");
+  const int64_t part_floats = (int64_t)plan->num_part_rows * kv->kv_heads * kv->head_dim;
+  const int64_t need = plan->num_part_rows * (int64_t)kv->kv_heads * (kv->head_dim + 4) * (int64_t)sizeof(float);
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
+    return fail(LORA_EINVAL, "workspace of %lld bytes, 16-byte aligned, needed (got %lld)", (long long)need,
+                (long long)workspace_bytes);
+  const int64_t all = (int64_t)plan->num_row_items + plan->num_tile_items + plan->num_joins;
+  if (all * kv->kv_heads > INT32_MAX) return fail(LORA_EINVAL, "not a plan");
+  if (plan->num_tokens == 0 || all == 0) return ok();
+  if (!items || !q || !out) return fail(LORA_EINVAL, "null pointer");
+  if (!aligned16(items) || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3))
+    return fail(LORA_EINVAL, "q, out and items must be 16-byte aligned");
+  Args a{};
+  a.kv = *kv;
+  a.q = (const uint16_t *)q;
+  a.out = (uint16_t *)out;
+  a.lse = lse;
+  a.part_o = (float *)workspace;
+  a.part_lse = (float *)workspace + part_floats;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.o_ts = out_token_stride;
+  a.o_hs = out_head_stride;
+  a.scale2 = scale * kLog2e;
+  a.q_heads = plan->q_heads;
+  a.group = plan->q_heads / plan->kv_heads;
+  a.causal = plan->flags & LORA_ATTN_CAUSAL;
+  a.window = plan->window;
+  a.num_tokens = plan->num_tokens;
+  a.num_part_rows = plan->num_part_rows;
+  const int dp = (kv->head_dim + 31) / 32 * 32;
+  if (plan->num_row_items) {
+    a.items = items;
+    a.num_items = plan->num_row_items;
+    const unsigned grid = (unsigned)(plan->num_row_items * kv->kv_heads);
+    if (dp <= 64) launch_rows<64>(a, grid, stream);
+    else if (dp <= 96) launch_rows<96>(a, grid, stream);
+    else if (dp <= 128) launch_rows<128>(a, grid, stream);
+    else if (dp <= 192) launch_rows<192>(a, grid, stream);
+    else launch_rows<256>(a, grid, stream);
+  }
+  if (plan->num_joins) {
+    a.items = items + plan->num_row_items + plan->num_tile_items;
+    a.num_items = plan->num_joins;
+    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(plan->num_joins * kv->kv_heads)), dim3(256), 0, stream, a);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
+}
