@@ -11,6 +11,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kv_internal.h"
 #include "kv_debug.h"
@@ -28,8 +29,21 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 
+// n / d for 0 <= n < 2^31 by multiplication: m = floor(2^(31 + s) / d) + 1 with 2^s >= d is off from
+// 2^(31 + s) / d by less than 1, so n m / 2^(31 + s) is off from n / d by less than 2^-s <= 1 / d, and below.
+struct Div {
+  uint64_t m;
+  uint32_t shift;
+  Div(uint32_t d = 1) : shift(31) {
+    while ((1ull << (shift - 31)) < d) ++shift;
+    m = (1ull << shift) / d + 1;
+  }
+  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
 struct Args {
   lora_kv_view kv;
+  Div page_div;  // by kv.page_tokens
   const lora_attn_item *items;
   const uint16_t *q;
   uint16_t *out;
@@ -285,6 +299,296 @@ __global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
   }
 }
 
+// ----------------------------------------------------------------- tile items
+// Up to 128 rows against positions [kv_begin, kv_end): four waves of 32 rows share tiles of
+// 64 positions, which go from the pages straight into LDS (16 bytes a lane, any page
+// per lane) while the tile before is multiplied.
+constexpr int kTileWaves = 4;
+constexpr int kTilePos = 64;
+constexpr float kSlack = 8.f;
+
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+
+__device__ const uint4 g_zeros = {0, 0, 0, 0};  // what an absent row or column reads
+
+// Chunks of 16 bytes of a row are stored permuted so that LDS reads spread over the banks: K
+// is read as 8 rows of one chunk at a time, V as 4 rows of four neighbouring chunks.
+template <int DP>
+struct TileLayout {
+  static constexpr int kCpr = DP / 8;                                    // chunks per row
+  static constexpr int kLoads = kTilePos * kCpr / 64 / kTileWaves;       // per wave and operand
+  __device__ static __forceinline__ int k_slot(int row, int c) { return c ^ (row & (kCpr % 8 ? 3 : 7)); }
+  __device__ static __forceinline__ int v_slot(int row, int c) {
+    if constexpr (kCpr % 16 == 0) return c ^ ((row & 3) << 2);
+    else if constexpr (kCpr % 8 == 0) return c ^ ((row & 2) << 1);
+    else return c;  // rows of 192 bytes are spread by themselves
+  }
+};
+
+template <int DP>
+__global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_kernel(Args a) {
+  using L = TileLayout<DP>;
+  constexpr int KS = DP / 16, DB = DP / 32, SB = kTilePos / 32;
+  // arrays of their own, not one array of two buffers: the compiler then does not wait for the loads into
+  // one before it reads the other
+  __shared__ __attribute__((aligned(16))) uint16_t sk0[kTilePos * DP], sk1[kTilePos * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t sv0[kTilePos * DP], sv1[kTilePos * DP];
+  __shared__ __attribute__((aligned(16))) uint32_t absent[2][kTileWaves][2];  // bit r: position r of the tile has no page
+  const lora_kv_view &kv = a.kv;
+  const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
+  const lora_attn_item it = a.items[ii];
+  if (!good_item(a, it, LORA_ATTN_TILE_ROWS)) {
+    KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int fr = lane & 31, hf = lane >> 5;
+  const int D = kv.head_dim, nch = D >> 3;
+  const bool active = wave * 32 < it.rows;
+
+  // this lane's row (a row past the item's computes the item's first one and is not stored)
+  const int my = wave * 32 + fr;
+  const int row = it.row0 + (my < it.rows ? my : 0);
+  const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
+  const int64_t pos = (int64_t)it.pos0 + tok;
+  const int hi = a.causal ? (int)max(pos, (int64_t)-1) : INT32_MAX;
+  const int lo = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+  // over the wave: positions in [lo_all, hi_all] are kept by every row
+  int hi_all = hi, lo_all = lo;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    hi_all = min(hi_all, __shfl_xor(hi_all, d));
+    lo_all = max(lo_all, __shfl_xor(lo_all, d));
+  }
+  bf16x8_t qf[KS];
+  const uint16_t *qp = a.q + (it.q_begin + tok) * a.q_ts + head * a.q_hs;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (s * 2 + hf < nch) u = *reinterpret_cast<const uint4 *>(qp + (s * 2 + hf) * 8);
+    qf[s] = __builtin_bit_cast(bf16x8_t, u);
+  }
+
+  // loads: chunk c of a tile is row c / kCpr, LDS slot c % kCpr; lane l of the wave's load i takes c = 64 (4 i + wave) + l
+  const int32_t *table = kv.page_table + (int64_t)it.seq * kv.max_pages;
+  auto lookup = [&](int t0, int (&page)[L::kLoads]) {
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      const int p = t0 + (64 * (kTileWaves * i + wave) + lane) / L::kCpr;
+      const bool in = p >= it.kv_begin && p < it.kv_end;
+      page[i] = in ? table[a.page_div(p)] : -2;  // -2: out of the range
+    }
+  };
+  auto issue = [&](int t0, const int (&page)[L::kLoads], uint16_t *kb, uint16_t *vb, uint32_t *gone) {
+    uint64_t none = 0;
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L::kCpr, slot = c % L::kCpr;
+      const bool ok = (unsigned)page[i] < (unsigned)kv.num_pages;
+      const int p = t0 + r;
+      const int64_t at = page[i] * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
+      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
+      const void *kp = ok && kc < nch ? (const void *)((const uint16_t *)kv.k + at + kc * 8) : (const void *)&g_zeros;
+      const void *vp = ok && vc < nch ? (const void *)((const uint16_t *)kv.v + at + vc * 8) : (const void *)&g_zeros;
+      KV_CHECK(ok || page[i] == -2, LORA_DEBUG_BAD_PAGE);
+      if (!ok && page[i] != -2) none |= 1ull << r;
+      const int base = 64 * (kTileWaves * i + wave) * 8;
+      __builtin_amdgcn_global_load_lds(kp, (__attribute__((address_space(3))) void *)(kb + base), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(vp, (__attribute__((address_space(3))) void *)(vb + base), 16, 0, 0);
+    }
+    if (__ballot(none != 0)) {  // some page is absent: tell every wave (rare)
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) none |= (uint64_t)__shfl_xor((unsigned long long)none, d);
+    }
+    if (lane == 0) {
+      gone[wave * 2] = (uint32_t)none;
+      gone[wave * 2 + 1] = (uint32_t)(none >> 32);
+    }
+  };
+
+  f32x16_t o[DB];
+#pragma unroll
+  for (int t = 0; t < DB; ++t) o[t] = f32x16_t{};
+  float m = -INFINITY, l = 0.f;  // l: this lane's half of the positions
+
+  const int first = it.kv_begin / kTilePos * kTilePos;
+  const int tiles = (int)(((int64_t)it.kv_end - first + kTilePos - 1) / kTilePos);
+  int page[L::kLoads];
+
+  auto step = [&](auto bufc, int tile) {
+    constexpr int BUF = decltype(bufc)::value;
+    const uint16_t *kb = BUF ? sk1 : sk0, *vb = BUF ? sv1 : sv0;
+    const int t0 = first + tile * kTilePos;
+    if (tile + 1 < tiles) {
+      issue(t0 + kTilePos, page, BUF ? sk0 : sk1, BUF ? sv0 : sv1, absent[1 - BUF][0]);
+      if (tile + 2 < tiles) lookup(t0 + 2 * kTilePos, page);
+    }
+    if (active) {
+      // S^T: positions are operand rows
+      f32x16_t s[SB];
+#pragma unroll
+      for (int b = 0; b < SB; ++b) {
+        s[b] = f32x16_t{};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int r = 32 * b + fr;
+          const bf16x8_t kf = __builtin_bit_cast(
+              bf16x8_t, *reinterpret_cast<const uint4 *>(kb + r * DP + L::k_slot(r, 2 * ks + hf) * 8));
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[b], 0, 0, 0);
+        }
+      }
+      // element i of block b is position t0 + 32 b + 8 (i / 4) + 4 hf + i % 4
+      uint32_t keep = ~0u;
+      uint64_t gone = 0;
+#pragma unroll
+      for (int w = 0; w < kTileWaves; ++w)
+        gone |= absent[BUF][w][0] | (uint64_t)absent[BUF][w][1] << 32;
+      const bool whole = t0 >= it.kv_begin && it.kv_end - t0 >= kTilePos && hi_all >= t0 + (kTilePos - 1) &&
+                         lo_all <= t0 && __builtin_amdgcn_readfirstlane((uint32_t)gone | (uint32_t)(gone >> 32)) == 0;
+      if (!whole) {
+        keep = 0;
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = 32 * b + 8 * (i / 4) + 4 * hf + i % 4, p = t0 + r;
+            const bool ok = p >= it.kv_begin && p < it.kv_end && p <= hi && p >= lo && !(gone >> r & 1);
+            keep |= (uint32_t)ok << (16 * b + i);
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[b][i] = (keep >> (16 * b + i) & 1) ? s[b][i] * a.scale2 : -INFINITY;
+          mx = fmaxf(mx, s[b][i]);
+        }
+      auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+      mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+      // the running maximum may lag by kSlack: weights then stay below 2^kSlack, and the rescaling of
+      // o, which most tiles would do for some row, is rare
+      if (__ballot(mx > m + kSlack)) {
+        const float mn = fmaxf(m, mx);
+        const float corr = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        l *= corr;
+#pragma unroll
+        for (int t = 0; t < DB; ++t) o[t] *= corr;
+        m = mn;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - base);
+          sum += s[b][i];
+        }
+      l += sum;
+      // a masked tile whose V is not finite somewhere
+      bool odd = false;
+      if (!whole) {
+        for (int c = lane; c < kTilePos * L::kCpr; c += 64) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(vb + c * 8);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+        }
+        odd = __ballot(odd) != 0;
+      }
+      if (odd) {
+        // 0 * inf is NaN: such values are added where they are kept, one position at a time, and are zeros in the product
+        for (int r = 0; r < kTilePos; ++r) {
+          const int idx = 16 * (r >> 5) + 4 * ((r & 31) >> 3) + (r & 3);
+          float pv = 0.f;
+#pragma unroll
+          for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pv = idx == 16 * b + i ? s[b][i] : pv;
+          const int from = fr + 32 * (r >> 2 & 1);
+          pv = __shfl(pv, from);
+          const bool ok = __shfl((int)(keep >> idx & 1), from);
+#pragma unroll
+          for (int t = 0; t < DB; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int d = 32 * t + 8 * (i / 4) + 4 * hf + i % 4;
+              const uint16_t v = vb[r * DP + L::v_slot(r, d >> 3) * 8 + (d & 7)];
+              if (ok && not_finite(v)) o[t][i] += pv * bf16_val(v);
+            }
+        }
+      }
+      // O^T += V^T P^T: k-step ks holds positions 16 ks ..; this lane's half of P has 4 hf .. + 3 and 8 + 4 hf .. + 3
+      const int li = lane & 15, vr = 4 * hf + (li >> 2);
+#pragma unroll
+      for (int ks = 0; ks < kTilePos / 16; ++ks) {
+        const int b = ks / 2, e = 8 * (ks % 2);
+        const bf16x8_t pf = __builtin_bit_cast(
+            bf16x8_t, make_uint4(pack_bf16(s[b][e], s[b][e + 1]), pack_bf16(s[b][e + 2], s[b][e + 3]),
+                                 pack_bf16(s[b][e + 4], s[b][e + 5]), pack_bf16(s[b][e + 6], s[b][e + 7])));
+#pragma unroll
+        for (int t = 0; t < DB; ++t) {
+          uint2 x[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int r = 16 * ks + 8 * half + vr, c = 4 * t + 2 * (lane >> 4 & 1) + ((li & 3) >> 1);
+            x[half] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4_t *)(vb + r * DP + L::v_slot(vr, c) * 8 + (li & 1) * 4)));
+          }
+          uint32_t w[4] = {x[0].x, x[0].y, x[1].x, x[1].y};
+          if (odd) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((w[j] & 0x7f80u) == 0x7f80u) w[j] &= 0xffff0000u;
+              if ((w[j] & 0x7f800000u) == 0x7f800000u) w[j] &= 0xffffu;
+            }
+          }
+          o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3])), pf,
+                                                         o[t], 0, 0, 0);
+        }
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's loads of the next tile have landed
+    __syncthreads();                // everybody's have, and nobody reads this tile any more
+  };
+
+  if (tiles > 0) {
+    lookup(first, page);
+    issue(first, page, sk0, sv0, absent[0][0]);
+    if (tiles > 1) lookup(first + kTilePos, page);
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  for (int t = 0; t < tiles; t += 2) {
+    step(std::integral_constant<int, 0>{}, t);
+    if (t + 1 < tiles) step(std::integral_constant<int, 1>{}, t + 1);
+  }
+  auto ls = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+  l = __uint_as_float(ls[0]) + __uint_as_float(ls[1]);
+  if (my >= it.rows) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+  const int64_t pr = (int64_t)(it.part + my) * kv.kv_heads + h;
+  uint16_t *op = a.out + (it.q_begin + tok) * a.o_ts + head * a.o_hs;
+#pragma unroll
+  for (int t = 0; t < DB; ++t)
+#pragma unroll
+    for (int q4 = 0; q4 < 4; ++q4) {
+      const int d = 32 * t + 8 * q4 + 4 * hf;
+      if (d >= D) continue;
+      f32x4_t v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = l == 0.f ? 0.f : o[t][4 * q4 + j] * inv;
+      if (it.part >= 0) *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d) = v;
+      else *reinterpret_cast<uint2 *>(op + d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+  if (hf == 0) {
+    if (it.part >= 0) a.part_lse[pr] = lse2;
+    else if (a.lse) a.lse[(int64_t)(it.q_begin + tok) * a.q_heads + head] = lse2 * kLn2;
+  }
+}
+
 // ----------------------------------------------------------------- join
 // One thread per 8 columns of a row: the row's parts in order, each weighted with
 // 2^(lse_part - lse).
@@ -333,6 +637,11 @@ void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
   hipLaunchKernelGGL(attn_rows_kernel<DP>, dim3(grid), dim3(64 * kRowWaves), 0, stream, a);
 }
 
+template <int DP>
+void launch_tiles(const Args &a, unsigned grid, hipStream_t stream) {
+  hipLaunchKernelGGL(attn_tile_kernel<DP>, dim3(grid), dim3(64 * kTileWaves), 0, stream, a);
+}
+
 }  // namespace
 
 lora_status lora::kv_attn_debug(uint32_t *flags, int32_t clear) { return kv_debug_word(flags, clear); }
@@ -377,6 +686,7 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   a.q_hs = q_head_stride;
   a.o_ts = out_token_stride;
   a.o_hs = out_head_stride;
+  a.page_div = Div((uint32_t)kv->page_tokens);
   a.scale2 = scale * kLog2e;
   a.q_heads = plan->q_heads;
   a.group = plan->q_heads / plan->kv_heads;
@@ -394,6 +704,16 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
     else if (dp <= 128) launch_rows<128>(a, grid, stream);
     else if (dp <= 192) launch_rows<192>(a, grid, stream);
     else launch_rows<256>(a, grid, stream);
+  }
+  if (plan->num_tile_items) {
+    a.items = items + plan->num_row_items;
+    a.num_items = plan->num_tile_items;
+    const unsigned grid = (unsigned)(plan->num_tile_items * kv->kv_heads);
+    if (dp <= 64) launch_tiles<64>(a, grid, stream);
+    else if (dp <= 96) launch_tiles<96>(a, grid, stream);
+    else if (dp <= 128) launch_tiles<128>(a, grid, stream);
+    else if (dp <= 192) launch_tiles<192>(a, grid, stream);
+    else launch_tiles<256>(a, grid, stream);
   }
   if (plan->num_joins) {
     a.items = items + plan->num_row_items + plan->num_tile_items;

@@ -57,6 +57,7 @@ namespace {
 // own start and the join cost more than the parallelism gives.
 constexpr int64_t kAimUnits = 1024;
 constexpr int64_t kMinRange = 256;
+constexpr int64_t kTileMinRows = 33;  // requests of at least this many rows take tile items
 constexpr int32_t kTileKv = 64;  // range borders are multiples of this
 
 struct Tile {
@@ -97,8 +98,8 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
     for (int32_t r = 0; r < num_reqs; ++r) {
       const int32_t qn = q_starts[r + 1] - q_starts[r];
       const int64_t rows = qn * group, pos0 = (int64_t)kv_len[r] - qn;
-      const int kind = 0;
-      const int64_t step = LORA_ATTN_ROWS;
+      const int kind = rows >= kTileMinRows;
+      const int64_t step = kind ? LORA_ATTN_TILE_ROWS : LORA_ATTN_ROWS;
       for (int64_t row0 = 0; row0 < rows; row0 += step) {
         const int64_t n = std::min(step, rows - row0);
         const int64_t first = pos0 + row0 / group, last = pos0 + (row0 + n - 1) / group;
