@@ -24,6 +24,7 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLn2 = 0.693147180559945309f;
@@ -84,42 +85,51 @@ __device__ __forceinline__ bool good_item(const Args &a, const lora_attn_item &i
          (int64_t)it.part + it.rows <= a.num_part_rows + (it.part < 0 ? (int64_t)INT32_MAX : 0);
 }
 
-// Element offset of position p's row of KV head h, or -1 where no page holds it.
-__device__ __forceinline__ int64_t kv_row(const lora_kv_view &kv, int seq, int h, int p) {
-  const int pi = p / kv.page_tokens;
-  const int page = kv.page_table[(int64_t)seq * kv.max_pages + pi];
-  KV_CHECK((unsigned)page < (unsigned)kv.num_pages, LORA_DEBUG_BAD_PAGE);
-  if ((unsigned)page >= (unsigned)kv.num_pages) return -1;
-  return page * kv.page_stride + h * kv.head_stride + (p - pi * kv.page_tokens) * kv.token_stride;
-}
-
 __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
   const int lo = __shfl((int)(uint32_t)v, lane), hi = __shfl((int)(v >> 32), lane);
   return (int64_t)(uint32_t)lo | ((int64_t)hi << 32);
 }
 
-// ----------------------------------------------------------------- row items
-// Up to 16 rows (the query heads of one KV head, for one or a few tokens) against
-// positions [kv_begin, kv_end).  Four waves take tiles of 32 positions in turn, each
-// with a softmax of its own, joined at the end in wave order.
-constexpr int kRowWaves = 4;
-constexpr int kRowKv = 32;
+constexpr float kSlack = 8.f;
 
+__device__ const uint4 g_zeros = {0, 0, 0, 0};  // what an absent row or column reads
+
+// Chunks of 16 bytes of a row are stored permuted so that LDS reads spread over the banks: K
+// is read as 8 rows of one chunk at a time, V as 4 rows of four neighbouring chunks (tile
+// items) or 8 rows of two (row items).
 template <int DP>
-struct RowShared {
-  static constexpr int kLd = DP + 16;  // elements; the pad spreads the four rows of a transposed read over the banks
-  union {
-    uint16_t v[kRowWaves][kRowKv * kLd];
-    float o[kRowWaves][16][DP];
-  };
-  float m[kRowWaves][16], l[kRowWaves][16];
+struct Layout {
+  static constexpr int kCpr = DP / 8;  // chunks per row
+  __device__ static __forceinline__ int k_slot(int row, int c) { return c ^ (row & (kCpr % 8 ? 3 : 7)); }
+  __device__ static __forceinline__ int v_slot(int row, int c) {
+    if constexpr (kCpr % 16 == 0) return c ^ ((row & 3) << 2);
+    else if constexpr (kCpr % 8 == 0) return c ^ ((row & 2) << 1);
+    else return c;  // rows of 192 bytes are spread by themselves
+  }
+};
+template <int DP>
+struct RowLayout : Layout<DP> {
+  __device__ static __forceinline__ int v_slot(int row, int c) { return Layout<DP>::v_slot(row, c) ^ ((row & 4) >> 1); }
 };
 
-template <int DP>
-__global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
-  constexpr int KS = DP / 32, DT = DP / 16;
-  using Sh = RowShared<DP>;
-  __shared__ Sh sh;
+// ----------------------------------------------------------------- row items
+// Up to 16 rows (the query heads of one KV head, for one or a few tokens) against
+// positions [kv_begin, kv_end).  The waves take tiles of 32 positions in turn, each with a
+// softmax of its own and two LDS stages of its own: while a wave computes on one stage its
+// loads of the next tile go straight into the other (16 bytes a lane, whole lines, any page per
+// lane), with no barrier between waves.  The waves' results are joined at the end in wave order.
+//
+// Bound by HBM: K and V cross the device once.  What counts is bytes in flight: W waves hold
+// W tiles of K and V.
+constexpr int kRowPos = 32;
+
+template <int DP, int W>
+__global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
+  using L = RowLayout<DP>;
+  constexpr int KS = DP / 32, DT = DP / 16, LOADS = kRowPos * L::kCpr / 64;
+  __shared__ __attribute__((aligned(16))) uint16_t sk0[W * kRowPos * DP], sk1[W * kRowPos * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t sv0[W * kRowPos * DP], sv1[W * kRowPos * DP];
+  __shared__ float sm[W][16], sl[W][16];
   const lora_kv_view &kv = a.kv;
   const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
   const lora_attn_item it = a.items[ii];
@@ -130,13 +140,43 @@ __global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int fr = lane & 15, fg = lane >> 4;
   const int D = kv.head_dim, nch = D >> 3;
+  const int off = wave * kRowPos * DP;  // this wave's part of each stage
+
+  // loads: chunk c of a tile is row c / kCpr, LDS slot c % kCpr; lane l of load i takes c = 64 i + l
+  const int32_t *table = kv.page_table + (int64_t)it.seq * kv.max_pages;
+  const int first = it.kv_begin / kRowPos * kRowPos;
+  const int tiles = (int)(((int64_t)it.kv_end - first + kRowPos - 1) / kRowPos);
+  auto lookup = [&](int t0) {  // page of position t0 + (lane & 31); -2: out of the range
+    const int p = t0 + (lane & 31);
+    return p >= it.kv_begin && p < it.kv_end ? table[a.page_div(p)] : -2;
+  };
+  auto issue = [&](int t0, int page, uint16_t *kb, uint16_t *vb) -> uint32_t {
+    const int p = t0 + (lane & 31);
+    const bool ok = (unsigned)page < (unsigned)kv.num_pages;
+    KV_CHECK(ok || page == -2, LORA_DEBUG_BAD_PAGE);
+    const int64_t at = page * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
+    const int64_t mine = ok ? at : -1;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int c = 64 * i + lane, r = c / L::kCpr, slot = c % L::kCpr;
+      const int64_t ra = shfl64(mine, r);
+      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
+      const void *kp = ra >= 0 && kc < nch ? (const void *)((const uint16_t *)kv.k + ra + kc * 8) : (const void *)&g_zeros;
+      const void *vp = ra >= 0 && vc < nch ? (const void *)((const uint16_t *)kv.v + ra + vc * 8) : (const void *)&g_zeros;
+      __builtin_amdgcn_global_load_lds(kp, (__attribute__((address_space(3))) void *)(kb + 512 * i), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(vp, (__attribute__((address_space(3))) void *)(vb + 512 * i), 16, 0, 0);
+    }
+    return (uint32_t)__ballot(ok);  // bit i: position t0 + i exists
+  };
+
+  int page = wave < tiles ? lookup(first + wave * kRowPos) : -2;
 
   // this lane's row (a row past the item's computes row 0's token and is not stored)
   const int row = it.row0 + (fr < it.rows ? fr : 0);
   const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
   const int64_t pos = (int64_t)it.pos0 + tok;
-  const int64_t hi64 = a.causal ? pos : INT32_MAX, lo64 = a.window ? pos - a.window + 1 : 0;
-  const int hi = (int)max(hi64, (int64_t)-1), lo = (int)min(max(lo64, (int64_t)0), (int64_t)INT32_MAX);
+  const int hi = a.causal ? (int)max(pos, (int64_t)-1) : INT32_MAX;
+  const int lo = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
   bf16x8_t qf[KS];
   const uint16_t *qp = a.q + (it.q_begin + tok) * a.q_ts + head * a.q_hs;
 #pragma unroll
@@ -149,47 +189,34 @@ __global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
   f32x4_t o[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
-  uint16_t *vs = sh.v[wave];
+  float m = -INFINITY, l = 0.f;  // l: this lane's share of the positions
+  uint32_t there_next = 0;
 
-  const int first = it.kv_begin / kRowKv * kRowKv;
-  for (int64_t t0l = first + wave * kRowKv; t0l < it.kv_end; t0l += kRowWaves * kRowKv) {
-    const int t0 = (int)t0l;
-    // lane l & 31: the tile's position t0 + (l & 31)
-    const int pt = t0 + (lane & 31);
-    int64_t at = -1;
-    if (pt >= it.kv_begin && pt < it.kv_end) at = kv_row(kv, it.seq, h, pt);
-    const uint32_t there = (uint32_t)__ballot(at >= 0);  // bit i: position t0 + i exists
-    // K: operand rows are positions; rows that do not exist are zeros
+  auto step = [&](auto bufc, int tile) {
+    constexpr int BUF = decltype(bufc)::value;
+    const uint16_t *kb = (BUF ? sk1 : sk0) + off;
+    uint16_t *vb = (BUF ? sv1 : sv0) + off;
+    const int t0 = first + tile * kRowPos;
+    const uint32_t there = there_next;
+    if (tile + W < tiles) {
+      there_next = issue(t0 + W * kRowPos, page, (BUF ? sk0 : sk1) + off, (BUF ? sv0 : sv1) + off);
+      if (tile + 2 * W < tiles) page = lookup(t0 + 2 * W * kRowPos);
+    }
     f32x4_t sc[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t ka = shfl64(at, 16 * half + fr);
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (ka >= 0 && s * 4 + fg < nch) u = *reinterpret_cast<const uint4 *>((const uint16_t *)kv.k + ka + (s * 4 + fg) * 8);
-        sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u), qf[s], sc[half], 0, 0, 0);
+        const int r = 16 * half + fr;
+        const bf16x8_t kf = __builtin_bit_cast(
+            bf16x8_t, *reinterpret_cast<const uint4 *>(kb + r * DP + L::k_slot(r, 4 * s + fg) * 8));
+        sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[s], sc[half], 0, 0, 0);
       }
-    }
-    // V into LDS as it stands, absent rows and columns past head_dim as zeros
-    bool odd = false;  // a value that is not finite
-    constexpr int CPR = DP / 8, LOADS = kRowKv * CPR / 64;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int c = lane + 64 * i, r = c / CPR, cc = c % CPR;
-      const int64_t va = shfl64(at, r);
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (va >= 0 && cc < nch) u = *reinterpret_cast<const uint4 *>((const uint16_t *)kv.v + va + cc * 8);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-      *reinterpret_cast<uint4 *>(vs + r * Sh::kLd + cc * 8) = u;
-    }
     // scores: element e of this lane is position t0 + 4 fg + e (e < 4) or t0 + 16 + 4 fg + e - 4
     float s8[8];
     uint32_t keep = 0;
     bool hole = false;  // an existing position that this row does not keep
+    float mt = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int i = (e < 4 ? 4 * fg + e : 16 + 4 * fg + e - 4), p = t0 + i;
@@ -197,90 +224,117 @@ __global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
       s8[e] = ok ? sc[e >> 2][e & 3] * a.scale2 : -INFINITY;
       keep |= (uint32_t)ok << e;
       hole |= ex && !ok;
+      mt = fmaxf(mt, s8[e]);
     }
-    float mt = s8[0];
+    mt = max_groups(mt);
+    // the running maximum may lag by kSlack (see the tile items)
+    if (__ballot(mt > m + kSlack)) {
+      const float mn = fmaxf(m, mt);
+      const float corr = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      l *= corr;
 #pragma unroll
-    for (int e = 1; e < 8; ++e) mt = fmaxf(mt, s8[e]);
-    const float mn = fmaxf(m, max_groups(mt));
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float corr = __builtin_amdgcn_exp2f(m - base);
+      for (int t = 0; t < DT; ++t) o[t] *= corr;
+      m = mn;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
     float sum = 0.f, p8[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       p8[e] = __builtin_amdgcn_exp2f(s8[e] - base);
       sum += p8[e];
     }
-    l = l * corr + sum;
-    m = mn;
+    l += sum;
+    if (__ballot(hole)) {
+      // 0 * inf is NaN: values that are not finite are added where they are kept, one position at a
+      // time, and are zeros in the product
+      bool odd = false;
+      for (int c = lane; c < kRowPos * L::kCpr; c += 64) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(vb + c * 8);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int t = 0; t < DT; ++t) o[t] *= corr;
-    if (__ballot(odd) && __ballot(hole)) {
-      // some row must not see some value that is not finite, and 0 * inf is NaN: those values are
-      // added where they are kept, term by term, and are zeros in the product
+        for (int e = 0; e < 4; ++e) odd |= not_finite((uint16_t)w[e]) || not_finite((uint16_t)(w[e] >> 16));
+      }
+      if (__ballot(odd)) {
+        for (int r = 0; r < kRowPos; ++r) {
+          const int idx = 4 * (r >> 4) + (r & 3), from = 16 * ((r & 15) >> 2) + fr;
+          float pv = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        for (int g = 0; g < 4; ++g) {
-          const float pv = __shfl(p8[e], 16 * g + fr);
-          const bool ok = __shfl((int)(keep >> e & 1), 16 * g + fr);
-          const uint16_t *vr = vs + (e < 4 ? 4 * g + e : 16 + 4 * g + e - 4) * Sh::kLd + 4 * fg;
+          for (int e = 0; e < 8; ++e) pv = idx == e ? p8[e] : pv;
+          pv = __shfl(pv, from);
+          const bool ok = __shfl((int)(keep >> idx & 1), from);
 #pragma unroll
           for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (ok && not_finite(vr[16 * t + j])) o[t][j] += pv * bf16_val(vr[16 * t + j]);
+            for (int j = 0; j < 4; ++j) {
+              const int d = 16 * t + 4 * fg + j;
+              const uint16_t v = vb[r * DP + L::v_slot(r, d >> 3) * 8 + (d & 7)];
+              if (ok && not_finite(v)) o[t][j] += pv * bf16_val(v);
+            }
         }
-      __builtin_amdgcn_wave_barrier();
-      for (int i = lane; i < kRowKv * DP; i += 64) {
-        uint16_t *e = vs + i / DP * Sh::kLd + i % DP;
-        if (not_finite(*e)) *e = 0;
+        __builtin_amdgcn_wave_barrier();
+        for (int i = lane; i < kRowPos * DP; i += 64)
+          if (not_finite(vb[i])) vb[i] = 0;
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_wave_barrier();
     }
     const bf16x8_t pf = __builtin_bit_cast(
         bf16x8_t, make_uint4(pack_bf16(p8[0], p8[1]), pack_bf16(p8[2], p8[3]), pack_bf16(p8[4], p8[5]), pack_bf16(p8[6], p8[7])));
+    const int vr = 4 * fg + (fr >> 2);
 #pragma unroll
     for (int t = 0; t < DT; ++t) {
       // transposed reads: a group of 16 lanes names 4 rows x 16 columns, lane i gets column i's 4 values
-      s16x4_t x[2];
+      uint2 x[2];
 #pragma unroll
       for (int half = 0; half < 2; ++half)
-        x[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)(
-            vs + (16 * half + 4 * fg + (fr >> 2)) * Sh::kLd + 16 * t + (fr & 3) * 4));
-      const uint2 x0 = __builtin_bit_cast(uint2, x[0]), x1 = __builtin_bit_cast(uint2, x[1]);
-      o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(x0.x, x0.y, x1.x, x1.y)), pf,
-                                                     o[t], 0, 0, 0);
+        x[half] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)(
+            vb + (16 * half + vr) * DP + L::v_slot(vr, 2 * t + ((fr & 3) >> 1)) * 8 + (fr & 1) * 4)));
+      o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8_t, make_uint4(x[0].x, x[0].y, x[1].x, x[1].y)), pf, o[t], 0, 0, 0);
     }
+    __builtin_amdgcn_s_waitcnt(0);  // the next tile is in LDS (only this wave reads it)
     __builtin_amdgcn_wave_barrier();
+  };
+
+  if (wave < tiles) {
+    there_next = issue(first + wave * kRowPos, page, sk0 + off, sv0 + off);
+    if (wave + W < tiles) page = lookup(first + (wave + W) * kRowPos);
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_wave_barrier();
+    for (int t = wave; t < tiles; t += 2 * W) {
+      step(std::integral_constant<int, 0>{}, t);
+      if (t + W < tiles) step(std::integral_constant<int, 1>{}, t + W);
+    }
   }
   l = sum_groups(l);
 
   // join the waves in order
   __syncthreads();
+  float (*so)[16][DP] = reinterpret_cast<float (*)[16][DP]>(sk0);  // the same size
   if (fg == 0) {
-    sh.m[wave][fr] = m;
-    sh.l[wave][fr] = l;
+    sm[wave][fr] = m;
+    sl[wave][fr] = l;
   }
 #pragma unroll
   for (int t = 0; t < DT; ++t)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sh.o[wave][fr][16 * t + 4 * fg + j] = o[t][j];
+    for (int j = 0; j < 4; ++j) so[wave][fr][16 * t + 4 * fg + j] = o[t][j];
   __syncthreads();
-  for (int i = threadIdx.x; i < it.rows * nch; i += 64 * kRowWaves) {
+  for (int i = threadIdx.x; i < it.rows * nch; i += 64 * W) {
     const int r = i / nch, c = i % nch;
-    float top = sh.m[0][r];
-    for (int w = 1; w < kRowWaves; ++w) top = fmaxf(top, sh.m[w][r]);
-    float f[kRowWaves], total = 0.f;
-    for (int w = 0; w < kRowWaves; ++w) {
-      f[w] = sh.l[w][r] == 0.f ? 0.f : __builtin_amdgcn_exp2f(sh.m[w][r] - top);  // nothing kept: no weight
-      total += f[w] * sh.l[w][r];
+    float top = sm[0][r];
+    for (int w = 1; w < W; ++w) top = fmaxf(top, sm[w][r]);
+    float f[W], total = 0.f;
+    for (int w = 0; w < W; ++w) {
+      f[w] = sl[w][r] == 0.f ? 0.f : __builtin_amdgcn_exp2f(sm[w][r] - top);  // nothing kept: no weight
+      total += f[w] * sl[w][r];
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float x = 0.f;
-      for (int w = 0; w < kRowWaves; ++w)
-        if (sh.l[w][r] != 0.f) x += f[w] * sh.o[w][r][8 * c + e];
+      for (int w = 0; w < W; ++w)
+        if (sl[w][r] != 0.f) x += f[w] * so[w][r][8 * c + e];
       v[e] = x * inv;
     }
     const float lse2 = total == 0.f ? -INFINITY : top + log2f(total);
@@ -305,24 +359,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void attn_rows_kernel(Args a) {
 // per lane) while the tile before is multiplied.
 constexpr int kTileWaves = 4;
 constexpr int kTilePos = 64;
-constexpr float kSlack = 8.f;
-
-typedef __attribute__((ext_vector_type(16))) float f32x16_t;
-
-__device__ const uint4 g_zeros = {0, 0, 0, 0};  // what an absent row or column reads
-
-// Chunks of 16 bytes of a row are stored permuted so that LDS reads spread over the banks: K
-// is read as 8 rows of one chunk at a time, V as 4 rows of four neighbouring chunks.
 template <int DP>
-struct TileLayout {
-  static constexpr int kCpr = DP / 8;                                    // chunks per row
-  static constexpr int kLoads = kTilePos * kCpr / 64 / kTileWaves;       // per wave and operand
-  __device__ static __forceinline__ int k_slot(int row, int c) { return c ^ (row & (kCpr % 8 ? 3 : 7)); }
-  __device__ static __forceinline__ int v_slot(int row, int c) {
-    if constexpr (kCpr % 16 == 0) return c ^ ((row & 3) << 2);
-    else if constexpr (kCpr % 8 == 0) return c ^ ((row & 2) << 1);
-    else return c;  // rows of 192 bytes are spread by themselves
-  }
+struct TileLayout : Layout<DP> {
+  static constexpr int kLoads = kTilePos * Layout<DP>::kCpr / 64 / kTileWaves;  // per wave and operand
 };
 
 template <int DP>
@@ -634,7 +673,8 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <int DP>
 void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_rows_kernel<DP>, dim3(grid), dim3(64 * kRowWaves), 0, stream, a);
+  constexpr int W = DP <= 64 ? 4 : 2;
+  hipLaunchKernelGGL((attn_rows_kernel<DP, W>), dim3(grid), dim3(64 * W), 0, stream, a);
 }
 
 template <int DP>
