@@ -52,7 +52,8 @@ struct Args {
   float *part_o;    // [num_part_rows][kv_heads][head_dim]: normalised results of one range
   float *part_lse;  // [num_part_rows][kv_heads]: base-2 logarithm of its sum
   int64_t q_ts, q_hs, o_ts, o_hs;
-  float scale2;     // scale log2(e)
+  float scale2;     // |scale| log2(e), 1 for a scale of 0
+  uint32_t q_and, q_xor;  // see query()
   int32_t num_items, q_heads, group, causal, window, num_tokens, num_part_rows;
 };
 
@@ -61,6 +62,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ bool not_finite(uint16_t b) { return (b & 0x7f80u) == 0x7f80u; }
 __device__ __forceinline__ float bf16_val(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// At most N vector-memory operations of this wave outstanding, the other counters not waited
+// for (vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Every LDS operation of this wave done.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+
+// 16 bytes a lane from anywhere in memory to LDS, lane l's to byte 16 l behind `to` (the same in all
+// lanes).  Written out because the compiler, which cannot tell that a transposed LDS read and such a
+// load in flight touch different stages, would wait for every load before the first of those
+// reads.  It has no register result, and puts m0 back; who reads the stage calls wait_vm first.
+__device__ __forceinline__ void load_lds16(const void *from, const uint16_t *to) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t *)to;
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(from)
+               : "memory");
+}
+
+// A query fragment times the sign of the scale (0 for a scale of 0), so that the factor left over is above 0.
+__device__ __forceinline__ bf16x8_t query(const Args &a, uint4 u) {
+  return __builtin_bit_cast(bf16x8_t, make_uint4((u.x & a.q_and) ^ a.q_xor, (u.y & a.q_and) ^ a.q_xor,
+                                                 (u.z & a.q_and) ^ a.q_xor, (u.w & a.q_and) ^ a.q_xor));
+}
 
 // Maximum or sum over the four lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float max_groups(float v) {
@@ -85,14 +116,20 @@ __device__ __forceinline__ bool good_item(const Args &a, const lora_attn_item &i
          (int64_t)it.part + it.rows <= a.num_part_rows + (it.part < 0 ? (int64_t)INT32_MAX : 0);
 }
 
+// p, or where an absent row or column is read.
+__device__ const uint4 g_zeros = {0, 0, 0, 0};
+__device__ __forceinline__ const void *pick(bool use, const void *p) {
+  const uintptr_t mask = (uintptr_t)0 - (uintptr_t)use;
+  return reinterpret_cast<const void *>((reinterpret_cast<uintptr_t>(p) & mask) |
+                                        (reinterpret_cast<uintptr_t>(&g_zeros) & ~mask));
+}
+
 __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
   const int lo = __shfl((int)(uint32_t)v, lane), hi = __shfl((int)(v >> 32), lane);
   return (int64_t)(uint32_t)lo | ((int64_t)hi << 32);
 }
 
 constexpr float kSlack = 8.f;
-
-__device__ const uint4 g_zeros = {0, 0, 0, 0};  // what an absent row or column reads
 
 // Chunks of 16 bytes of a row are stored permuted so that LDS reads spread over the banks: K
 // is read as 8 rows of one chunk at a time, V as 4 rows of four neighbouring chunks (tile
@@ -137,7 +174,7 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
     KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
   const int D = kv.head_dim, nch = D >> 3;
   const int off = wave * kRowPos * DP;  // this wave's part of each stage
@@ -146,14 +183,17 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
   const int32_t *table = kv.page_table + (int64_t)it.seq * kv.max_pages;
   const int first = it.kv_begin / kRowPos * kRowPos;
   const int tiles = (int)(((int64_t)it.kv_end - first + kRowPos - 1) / kRowPos);
-  auto lookup = [&](int t0) {  // page of position t0 + (lane & 31); -2: out of the range
-    const int p = t0 + (lane & 31);
-    return p >= it.kv_begin && p < it.kv_end ? table[a.page_div(p)] : -2;
+  auto inside = [&](int64_t p) { return p >= it.kv_begin && p < it.kv_end; };
+  auto lookup = [&](int tile) {  // the page-table entry of the tile's position lane & 31, unused where that is outside
+    const int64_t p = first + (int64_t)tile * kRowPos + (lane & 31);
+    return table[inside(p) ? a.page_div((int)p) : 0];
   };
-  auto issue = [&](int t0, int page, uint16_t *kb, uint16_t *vb) -> uint32_t {
-    const int p = t0 + (lane & 31);
-    const bool ok = (unsigned)page < (unsigned)kv.num_pages;
-    KV_CHECK(ok || page == -2, LORA_DEBUG_BAD_PAGE);
+  auto issue = [&](auto bufc, int tile, int page) -> uint32_t {
+    constexpr int BUF = decltype(bufc)::value;
+    uint16_t *kb = (BUF ? sk1 : sk0) + off, *vb = (BUF ? sv1 : sv0) + off;
+    const int p = first + tile * kRowPos + (lane & 31);
+    const bool ok = inside(p) && (unsigned)page < (unsigned)kv.num_pages;
+    KV_CHECK(ok || !inside(p), LORA_DEBUG_BAD_PAGE);
     const int64_t at = page * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
     const int64_t mine = ok ? at : -1;
 #pragma unroll
@@ -161,15 +201,16 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
       const int c = 64 * i + lane, r = c / L::kCpr, slot = c % L::kCpr;
       const int64_t ra = shfl64(mine, r);
       const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
-      const void *kp = ra >= 0 && kc < nch ? (const void *)((const uint16_t *)kv.k + ra + kc * 8) : (const void *)&g_zeros;
-      const void *vp = ra >= 0 && vc < nch ? (const void *)((const uint16_t *)kv.v + ra + vc * 8) : (const void *)&g_zeros;
-      __builtin_amdgcn_global_load_lds(kp, (__attribute__((address_space(3))) void *)(kb + 512 * i), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(vp, (__attribute__((address_space(3))) void *)(vb + 512 * i), 16, 0, 0);
+      load_lds16(pick(ra >= 0 && kc < nch, (const uint16_t *)kv.k + ra + kc * 8), kb + 512 * i);
+      load_lds16(pick(ra >= 0 && vc < nch, (const uint16_t *)kv.v + ra + vc * 8), vb + 512 * i);
     }
-    return (uint32_t)__ballot(ok);  // bit i: position t0 + i exists
+    return (uint32_t)__ballot(ok);  // bit i: the tile's position i exists
   };
 
-  int page = wave < tiles ? lookup(first + wave * kRowPos) : -2;
+  // The order of a wave's loads is tile t, pages of t + 2, tile t + 1, pages of t + 3, ...: loads end in
+  // order, so a tile's pages are there while the tile before it is still on its way.
+  const bool any = wave < tiles;
+  int page[2] = {any ? lookup(wave) : -1, any ? lookup(wave + W) : -1};  // of the next tile of each stage
 
   // this lane's row (a row past the item's computes row 0's token and is not stored)
   const int row = it.row0 + (fr < it.rows ? fr : 0);
@@ -183,25 +224,25 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
   for (int s = 0; s < KS; ++s) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (s * 4 + fg < nch) u = *reinterpret_cast<const uint4 *>(qp + (s * 4 + fg) * 8);
-    qf[s] = __builtin_bit_cast(bf16x8_t, u);
+    qf[s] = query(a, u);
   }
 
   f32x4_t o[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) o[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;  // l: this lane's share of the positions
-  uint32_t there_next = 0;
+  uint32_t exist[2] = {0, 0};     // per stage
 
   auto step = [&](auto bufc, int tile) {
     constexpr int BUF = decltype(bufc)::value;
     const uint16_t *kb = (BUF ? sk1 : sk0) + off;
     uint16_t *vb = (BUF ? sv1 : sv0) + off;
     const int t0 = first + tile * kRowPos;
-    const uint32_t there = there_next;
-    if (tile + W < tiles) {
-      there_next = issue(t0 + W * kRowPos, page, (BUF ? sk0 : sk1) + off, (BUF ? sv0 : sv1) + off);
-      if (tile + 2 * W < tiles) page = lookup(t0 + 2 * W * kRowPos);
-    }
+    const uint32_t there = exist[BUF];
+    // this tile has landed once no more loads than the next tile's are outstanding
+    if (tile + W < tiles) wait_vm<2 * LOADS>();
+    else wait_vm<0>();
+    __builtin_amdgcn_wave_barrier();
     f32x4_t sc[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int half = 0; half < 2; ++half)
@@ -221,26 +262,26 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
     for (int e = 0; e < 8; ++e) {
       const int i = (e < 4 ? 4 * fg + e : 16 + 4 * fg + e - 4), p = t0 + i;
       const bool ex = there >> i & 1, ok = ex && p <= hi && p >= lo;
-      s8[e] = ok ? sc[e >> 2][e & 3] * a.scale2 : -INFINITY;
+      s8[e] = ok ? sc[e >> 2][e & 3] : -INFINITY;
       keep |= (uint32_t)ok << e;
       hole |= ex && !ok;
       mt = fmaxf(mt, s8[e]);
     }
     mt = max_groups(mt);
     // the running maximum may lag by kSlack (see the tile items)
-    if (__ballot(mt > m + kSlack)) {
+    if (__ballot((mt - m) * a.scale2 > kSlack)) {
       const float mn = fmaxf(m, mt);
-      const float corr = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      const float corr = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * a.scale2);
       l *= corr;
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] *= corr;
       m = mn;
     }
-    const float base = m == -INFINITY ? 0.f : m;
+    const float base = m == -INFINITY ? 0.f : m * a.scale2;
     float sum = 0.f, p8[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      p8[e] = __builtin_amdgcn_exp2f(s8[e] - base);
+      p8[e] = __builtin_amdgcn_exp2f(fmaf(s8[e], a.scale2, -base));
       sum += p8[e];
     }
     l += sum;
@@ -291,21 +332,28 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
       o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
           __builtin_bit_cast(bf16x8_t, make_uint4(x[0].x, x[0].y, x[1].x, x[1].y)), pf, o[t], 0, 0, 0);
     }
-    __builtin_amdgcn_s_waitcnt(0);  // the next tile is in LDS (only this wave reads it)
     __builtin_amdgcn_wave_barrier();
+    if (tile + 2 * W < tiles) {
+      wait_lds();  // the reads of this stage are done
+      exist[BUF] = issue(bufc, tile + 2 * W, page[BUF]);
+      page[BUF] = lookup(tile + 4 * W);
+    }
   };
 
-  if (wave < tiles) {
-    there_next = issue(first + wave * kRowPos, page, sk0 + off, sv0 + off);
-    if (wave + W < tiles) page = lookup(first + (wave + W) * kRowPos);
-    __builtin_amdgcn_s_waitcnt(0);
-    __builtin_amdgcn_wave_barrier();
+  if (any) {
+    exist[0] = issue(std::integral_constant<int, 0>{}, wave, page[0]);
+    page[0] = lookup(wave + 2 * W);
+    if (wave + W < tiles) {
+      exist[1] = issue(std::integral_constant<int, 1>{}, wave + W, page[1]);
+      page[1] = lookup(wave + 3 * W);
+    }
     for (int t = wave; t < tiles; t += 2 * W) {
       step(std::integral_constant<int, 0>{}, t);
       if (t + W < tiles) step(std::integral_constant<int, 1>{}, t + W);
     }
   }
   l = sum_groups(l);
+  m *= a.scale2;  // base-2 units; -inf where nothing is kept
 
   // join the waves in order
   __syncthreads();
@@ -368,11 +416,9 @@ template <int DP>
 __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_kernel(Args a) {
   using L = TileLayout<DP>;
   constexpr int KS = DP / 16, DB = DP / 32, SB = kTilePos / 32;
-  // arrays of their own, not one array of two buffers: the compiler then does not wait for the loads into
-  // one before it reads the other
   __shared__ __attribute__((aligned(16))) uint16_t sk0[kTilePos * DP], sk1[kTilePos * DP];
   __shared__ __attribute__((aligned(16))) uint16_t sv0[kTilePos * DP], sv1[kTilePos * DP];
-  __shared__ __attribute__((aligned(16))) uint32_t absent[2][kTileWaves][2];  // bit r: position r of the tile has no page
+  __shared__ uint32_t any_odd[kTileWaves];
   const lora_kv_view &kv = a.kv;
   const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
   const lora_attn_item it = a.items[ii];
@@ -380,91 +426,84 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, hf = lane >> 5;
   const int D = kv.head_dim, nch = D >> 3;
   const bool active = wave * 32 < it.rows;
+
+  // loads: lane l looks up the tile's position l; chunk c of a tile is row c / kCpr, LDS slot c % kCpr, and lane l
+  // of the wave's load i takes c = 64 (4 i + wave) + l
+  const int32_t *table = kv.page_table + (int64_t)it.seq * kv.max_pages;
+  const int first = it.kv_begin / kTilePos * kTilePos;
+  const int tiles = (int)(((int64_t)it.kv_end - first + kTilePos - 1) / kTilePos);
+  auto inside = [&](int64_t p) { return p >= it.kv_begin && p < it.kv_end; };
+  auto lookup = [&](int tile) {  // a page-table entry, unused where the position is outside
+    const int64_t p = first + (int64_t)tile * kTilePos + lane;
+    return table[inside(p) ? a.page_div((int)p) : 0];
+  };
+  auto issue = [&](auto bufc, int tile, int page) -> uint64_t {
+    constexpr int BUF = decltype(bufc)::value;
+    uint16_t *kb = BUF ? sk1 : sk0, *vb = BUF ? sv1 : sv0;
+    const int p = first + tile * kTilePos + lane;
+    const bool ok = inside(p) && (unsigned)page < (unsigned)kv.num_pages;
+    KV_CHECK(ok || !inside(p), LORA_DEBUG_BAD_PAGE);
+    const int64_t at = page * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
+    const int64_t mine = ok ? at : -1;
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L::kCpr, slot = c % L::kCpr;
+      const int64_t ra = shfl64(mine, r);
+      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
+      const int to = 64 * (kTileWaves * i + wave) * 8;
+      load_lds16(pick(ra >= 0 && kc < nch, (const uint16_t *)kv.k + ra + kc * 8), kb + to);
+      load_lds16(pick(ra >= 0 && vc < nch, (const uint16_t *)kv.v + ra + vc * 8), vb + to);
+    }
+    return __ballot(ok);  // bit i: the tile's position i exists
+  };
+  int page = tiles > 0 ? lookup(0) : -1;
 
   // this lane's row (a row past the item's computes the item's first one and is not stored)
   const int my = wave * 32 + fr;
   const int row = it.row0 + (my < it.rows ? my : 0);
   const int tok = row / a.group, head = h * a.group + (row - tok * a.group);
-  const int64_t pos = (int64_t)it.pos0 + tok;
-  const int hi = a.causal ? (int)max(pos, (int64_t)-1) : INT32_MAX;
-  const int lo = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
-  // over the wave: positions in [lo_all, hi_all] are kept by every row
-  int hi_all = hi, lo_all = lo;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    hi_all = min(hi_all, __shfl_xor(hi_all, d));
-    lo_all = max(lo_all, __shfl_xor(lo_all, d));
-  }
+  auto highest = [&](int64_t pos) { return a.causal ? (int)max(pos, (int64_t)-1) : INT32_MAX; };
+  auto lowest = [&](int64_t pos) { return a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0; };
+  const int hi = highest((int64_t)it.pos0 + tok), lo = lowest((int64_t)it.pos0 + tok);
+  // every row of the item keeps the positions in [lo_all, hi_all]
+  const int hi_all = highest((int64_t)it.pos0 + it.row0 / a.group);
+  const int lo_all = lowest((int64_t)it.pos0 + (it.row0 + it.rows - 1) / a.group);
   bf16x8_t qf[KS];
   const uint16_t *qp = a.q + (it.q_begin + tok) * a.q_ts + head * a.q_hs;
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (s * 2 + hf < nch) u = *reinterpret_cast<const uint4 *>(qp + (s * 2 + hf) * 8);
-    qf[s] = __builtin_bit_cast(bf16x8_t, u);
+    qf[s] = query(a, u);
   }
-
-  // loads: chunk c of a tile is row c / kCpr, LDS slot c % kCpr; lane l of the wave's load i takes c = 64 (4 i + wave) + l
-  const int32_t *table = kv.page_table + (int64_t)it.seq * kv.max_pages;
-  auto lookup = [&](int t0, int (&page)[L::kLoads]) {
-#pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
-      const int p = t0 + (64 * (kTileWaves * i + wave) + lane) / L::kCpr;
-      const bool in = p >= it.kv_begin && p < it.kv_end;
-      page[i] = in ? table[a.page_div(p)] : -2;  // -2: out of the range
-    }
-  };
-  auto issue = [&](int t0, const int (&page)[L::kLoads], uint16_t *kb, uint16_t *vb, uint32_t *gone) {
-    uint64_t none = 0;
-#pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
-      const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L::kCpr, slot = c % L::kCpr;
-      const bool ok = (unsigned)page[i] < (unsigned)kv.num_pages;
-      const int p = t0 + r;
-      const int64_t at = page[i] * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
-      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
-      const void *kp = ok && kc < nch ? (const void *)((const uint16_t *)kv.k + at + kc * 8) : (const void *)&g_zeros;
-      const void *vp = ok && vc < nch ? (const void *)((const uint16_t *)kv.v + at + vc * 8) : (const void *)&g_zeros;
-      KV_CHECK(ok || page[i] == -2, LORA_DEBUG_BAD_PAGE);
-      if (!ok && page[i] != -2) none |= 1ull << r;
-      const int base = 64 * (kTileWaves * i + wave) * 8;
-      __builtin_amdgcn_global_load_lds(kp, (__attribute__((address_space(3))) void *)(kb + base), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(vp, (__attribute__((address_space(3))) void *)(vb + base), 16, 0, 0);
-    }
-    if (__ballot(none != 0)) {  // some page is absent: tell every wave (rare)
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) none |= (uint64_t)__shfl_xor((unsigned long long)none, d);
-    }
-    if (lane == 0) {
-      gone[wave * 2] = (uint32_t)none;
-      gone[wave * 2 + 1] = (uint32_t)(none >> 32);
-    }
-  };
 
   f32x16_t o[DB];
 #pragma unroll
   for (int t = 0; t < DB; ++t) o[t] = f32x16_t{};
-  float m = -INFINITY, l = 0.f;  // l: this lane's half of the positions
-
-  const int first = it.kv_begin / kTilePos * kTilePos;
-  const int tiles = (int)(((int64_t)it.kv_end - first + kTilePos - 1) / kTilePos);
-  int page[L::kLoads];
+  float m = -INFINITY, l = 0.f;  // m: of the unscaled scores; l: this lane's half of the positions
+  uint64_t exist[2] = {0, 0};    // per stage
 
   auto step = [&](auto bufc, int tile) {
     constexpr int BUF = decltype(bufc)::value;
-    const uint16_t *kb = BUF ? sk1 : sk0, *vb = BUF ? sv1 : sv0;
+    const uint16_t *kb = BUF ? sk1 : sk0;
+    uint16_t *vb = BUF ? sv1 : sv0;
     const int t0 = first + tile * kTilePos;
+    wait_vm<0>();     // this wave's loads of the tile have landed
+    __syncthreads();  // everybody's have, and nobody reads the other stage any more
     if (tile + 1 < tiles) {
-      issue(t0 + kTilePos, page, BUF ? sk0 : sk1, BUF ? sv0 : sv1, absent[1 - BUF][0]);
-      if (tile + 2 < tiles) lookup(t0 + 2 * kTilePos, page);
+      exist[1 - BUF] = issue(std::integral_constant<int, 1 - BUF>{}, tile + 1, page);
+      page = lookup(tile + 2);
     }
+    const bool whole = exist[BUF] == ~0ull && hi_all >= t0 + (kTilePos - 1) && lo_all <= t0;
+    // element i of block b is position t0 + 32 b + 8 (i / 4) + 4 hf + i % 4
+    f32x16_t s[SB];
+    uint32_t keep = ~0u;
     if (active) {
       // S^T: positions are operand rows
-      f32x16_t s[SB];
 #pragma unroll
       for (int b = 0; b < SB; ++b) {
         s[b] = f32x16_t{};
@@ -476,14 +515,6 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
           s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[b], 0, 0, 0);
         }
       }
-      // element i of block b is position t0 + 32 b + 8 (i / 4) + 4 hf + i % 4
-      uint32_t keep = ~0u;
-      uint64_t gone = 0;
-#pragma unroll
-      for (int w = 0; w < kTileWaves; ++w)
-        gone |= absent[BUF][w][0] | (uint64_t)absent[BUF][w][1] << 32;
-      const bool whole = t0 >= it.kv_begin && it.kv_end - t0 >= kTilePos && hi_all >= t0 + (kTilePos - 1) &&
-                         lo_all <= t0 && __builtin_amdgcn_readfirstlane((uint32_t)gone | (uint32_t)(gone >> 32)) == 0;
       if (!whole) {
         keep = 0;
 #pragma unroll
@@ -491,7 +522,8 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int r = 32 * b + 8 * (i / 4) + 4 * hf + i % 4, p = t0 + r;
-            const bool ok = p >= it.kv_begin && p < it.kv_end && p <= hi && p >= lo && !(gone >> r & 1);
+            const bool ok = p <= hi && p >= lo && (exist[BUF] >> r & 1);
+            s[b][i] = ok ? s[b][i] : -INFINITY;
             keep |= (uint32_t)ok << (16 * b + i);
           }
       }
@@ -499,65 +531,73 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
 #pragma unroll
       for (int b = 0; b < SB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[b][i] = (keep >> (16 * b + i) & 1) ? s[b][i] * a.scale2 : -INFINITY;
-          mx = fmaxf(mx, s[b][i]);
-        }
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
       auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
       mx = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
-      // the running maximum may lag by kSlack: weights then stay below 2^kSlack, and the rescaling of
-      // o, which most tiles would do for some row, is rare
-      if (__ballot(mx > m + kSlack)) {
+      // the running maximum may lag by kSlack (in powers of two): weights then stay below 2^kSlack, and the
+      // rescaling of o, which most tiles would do for some row, is rare
+      if (__ballot((mx - m) * a.scale2 > kSlack)) {
         const float mn = fmaxf(m, mx);
-        const float corr = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        const float corr = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * a.scale2);
         l *= corr;
 #pragma unroll
         for (int t = 0; t < DB; ++t) o[t] *= corr;
         m = mn;
       }
-      const float base = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
+      const float base = m == -INFINITY ? 0.f : m * a.scale2;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < SB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - base);
-          sum += s[b][i];
+          s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], a.scale2, -base));
+          sum[i & 3] += s[b][i];
         }
-      l += sum;
-      // a masked tile whose V is not finite somewhere
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+    if (!whole) {
+      // 0 * inf is NaN: values of V that are not finite are added where they are kept, one position at a
+      // time, and are zeros in the product
       bool odd = false;
-      if (!whole) {
-        for (int c = lane; c < kTilePos * L::kCpr; c += 64) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(vb + c * 8);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int c = threadIdx.x; c < kTilePos * L::kCpr; c += 64 * kTileWaves) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(vb + c * 8);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-        }
-        odd = __ballot(odd) != 0;
+        for (int e = 0; e < 4; ++e) odd |= not_finite((uint16_t)w[e]) || not_finite((uint16_t)(w[e] >> 16));
       }
+      if (lane == 0) any_odd[wave] = 0;
+      if (odd) any_odd[wave] = 1;
+      __syncthreads();
+      odd = false;
+      for (int w = 0; w < kTileWaves; ++w) odd |= any_odd[w] != 0;
       if (odd) {
-        // 0 * inf is NaN: such values are added where they are kept, one position at a time, and are zeros in the product
-        for (int r = 0; r < kTilePos; ++r) {
-          const int idx = 16 * (r >> 5) + 4 * ((r & 31) >> 3) + (r & 3);
-          float pv = 0.f;
+        if (active) {
+          for (int r = 0; r < kTilePos; ++r) {
+            const int idx = 16 * (r >> 5) + 4 * ((r & 31) >> 3) + (r & 3), from = fr + 32 * (r >> 2 & 1);
+            float pv = 0.f;
 #pragma unroll
-          for (int b = 0; b < SB; ++b)
+            for (int b = 0; b < SB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pv = idx == 16 * b + i ? s[b][i] : pv;
-          const int from = fr + 32 * (r >> 2 & 1);
-          pv = __shfl(pv, from);
-          const bool ok = __shfl((int)(keep >> idx & 1), from);
+              for (int i = 0; i < 16; ++i) pv = idx == 16 * b + i ? s[b][i] : pv;
+            pv = __shfl(pv, from);
+            const bool ok = __shfl((int)(keep >> idx & 1), from);
 #pragma unroll
-          for (int t = 0; t < DB; ++t)
+            for (int t = 0; t < DB; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int d = 32 * t + 8 * (i / 4) + 4 * hf + i % 4;
-              const uint16_t v = vb[r * DP + L::v_slot(r, d >> 3) * 8 + (d & 7)];
-              if (ok && not_finite(v)) o[t][i] += pv * bf16_val(v);
-            }
+              for (int i = 0; i < 16; ++i) {
+                const int d = 32 * t + 8 * (i / 4) + 4 * hf + i % 4;
+                const uint16_t v = vb[r * DP + L::v_slot(r, d >> 3) * 8 + (d & 7)];
+                if (ok && not_finite(v)) o[t][i] += pv * bf16_val(v);
+              }
+          }
         }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kTilePos * DP; i += 64 * kTileWaves)
+          if (not_finite(vb[i])) vb[i] = 0;
+        __syncthreads();
       }
+    }
+    if (active) {
       // O^T += V^T P^T: k-step ks holds positions 16 ks ..; this lane's half of P has 4 hf .. + 3 and 8 + 4 hf .. + 3
       const int li = lane & 15, vr = 4 * hf + (li >> 2);
 #pragma unroll
@@ -575,30 +615,17 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
             x[half] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4_t *)(vb + r * DP + L::v_slot(vr, c) * 8 + (li & 1) * 4)));
           }
-          uint32_t w[4] = {x[0].x, x[0].y, x[1].x, x[1].y};
-          if (odd) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((w[j] & 0x7f80u) == 0x7f80u) w[j] &= 0xffff0000u;
-              if ((w[j] & 0x7f800000u) == 0x7f800000u) w[j] &= 0xffffu;
-            }
-          }
-          o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3])), pf,
-                                                         o[t], 0, 0, 0);
+          o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8_t, make_uint4(x[0].x, x[0].y, x[1].x, x[1].y)), pf, o[t], 0, 0, 0);
         }
       }
     }
-    __builtin_amdgcn_s_waitcnt(0);  // this wave's loads of the next tile have landed
-    __syncthreads();                // everybody's have, and nobody reads this tile any more
   };
 
   if (tiles > 0) {
-    lookup(first, page);
-    issue(first, page, sk0, sv0, absent[0][0]);
-    if (tiles > 1) lookup(first + kTilePos, page);
+    exist[0] = issue(std::integral_constant<int, 0>{}, 0, page);
+    page = lookup(1);
   }
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
   for (int t = 0; t < tiles; t += 2) {
     step(std::integral_constant<int, 0>{}, t);
     if (t + 1 < tiles) step(std::integral_constant<int, 1>{}, t + 1);
@@ -607,7 +634,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
   l = __uint_as_float(ls[0]) + __uint_as_float(ls[1]);
   if (my >= it.rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+  const float lse2 = l == 0.f ? -INFINITY : m * a.scale2 + log2f(l);
   const int64_t pr = (int64_t)(it.part + my) * kv.kv_heads + h;
   uint16_t *op = a.out + (it.q_begin + tok) * a.o_ts + head * a.o_hs;
 #pragma unroll
@@ -669,12 +696,17 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
   }
 }
 
+constexpr unsigned kComputeUnits = 256;
+
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <int DP>
 void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
-  constexpr int W = DP <= 64 ? 4 : 2;
-  hipLaunchKernelGGL((attn_rows_kernel<DP, W>), dim3(grid), dim3(64 * W), 0, stream, a);
+  // two workgroups of half the waves share a compute unit's LDS and overlap their ends; a grid that gives
+  // every compute unit one at most takes all the waves at once, for a shorter chain of tiles
+  constexpr int W = DP <= 64 ? 4 : DP <= 128 ? 2 : 1;
+  if (grid <= kComputeUnits) hipLaunchKernelGGL((attn_rows_kernel<DP, 2 * W>), dim3(grid), dim3(128 * W), 0, stream, a);
+  else hipLaunchKernelGGL((attn_rows_kernel<DP, W>), dim3(grid), dim3(64 * W), 0, stream, a);
 }
 
 template <int DP>
@@ -727,7 +759,9 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   a.o_ts = out_token_stride;
   a.o_hs = out_head_stride;
   a.page_div = Div((uint32_t)kv->page_tokens);
-  a.scale2 = scale * kLog2e;
+  a.scale2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
+  a.q_and = scale == 0.f ? 0u : ~0u;
+  a.q_xor = scale < 0.f ? 0x80008000u : 0u;
   a.q_heads = plan->q_heads;
   a.group = plan->q_heads / plan->kv_heads;
   a.causal = plan->flags & LORA_ATTN_CAUSAL;

@@ -52,11 +52,11 @@ lora_status lora::check_view(const lora_kv_view *kv) {
 
 namespace {
 
-// Items of one kind aim at this many (item, KV head) units, four to a compute
-// unit, and at no range of fewer positions than kMinRange: below that a range's
-// own start and the join cost more than the parallelism gives.
-constexpr int64_t kAimUnits = 1024;
-constexpr int64_t kMinRange = 256;
+// Items of one kind aim at this many (item, KV head) units, and at no range of fewer positions than
+// kMinRange: below that a range's own start and the join cost more than the
+// parallelism gives.  [0] row items, [1] tile items.
+constexpr int64_t kAimUnits[2] = {1024, 512};
+constexpr int64_t kMinRange[2] = {256, 1024};
 constexpr int64_t kTileMinRows = 33;  // requests of at least this many rows take tile items
 constexpr int32_t kTileKv = 64;  // range borders are multiples of this
 
@@ -119,7 +119,7 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
       int64_t work = 0;
       for (const Tile &t : tiles[kind]) work += t.span * kv_heads;
       // positions per range: an even share of the work for each unit aimed at
-      const int64_t share = std::max(kMinRange, cdiv(cdiv(work, kAimUnits), kTileKv) * kTileKv);
+      const int64_t share = std::max(kMinRange[kind], cdiv(cdiv(work, kAimUnits[kind]), kTileKv) * kTileKv);
       std::vector<Tile> ranges;
       for (const Tile &t : tiles[kind]) {
         int64_t parts = max_parts == 1 ? 1 : std::max<int64_t>(1, (t.span + share / 2) / share);
