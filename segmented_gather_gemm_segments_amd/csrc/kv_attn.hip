@@ -30,21 +30,22 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 
-// n / d for 0 <= n < 2^31 by multiplication: m = floor(2^(31 + s) / d) + 1 with 2^s >= d is off from
-// 2^(31 + s) / d by less than 1, so n m / 2^(31 + s) is off from n / d by less than 2^-s <= 1 / d, and below.
+// n / d for 0 <= n < 2^31 by multiplication: m = floor(2^(31 + s) / d) + 1 with 2^s >= d > 2^(s - 1) exceeds
+// 2^(31 + s) / d by at most 1, so n m / 2^(31 + s) exceeds n / d by less than 2^-s <= 1 / d: the same
+// whole part.  m fits 32 bits, and so does 2 n.
 struct Div {
-  uint64_t m;
-  uint32_t shift;
-  Div(uint32_t d = 1) : shift(31) {
-    while ((1ull << (shift - 31)) < d) ++shift;
-    m = (1ull << shift) / d + 1;
+  uint32_t m, s;
+  Div(uint32_t d = 1) : s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)((1ull << (31 + s)) / d + 1);
   }
-  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+  __device__ __forceinline__ int operator()(int n) const { return (int)(__umulhi(2u * (uint32_t)n, m) >> s); }
 };
 
 struct Args {
   lora_kv_view kv;
   Div page_div;  // by kv.page_tokens
+  uint32_t page16, token16;  // strides in units of 16 bytes
   const lora_attn_item *items;
   const uint16_t *q;
   uint16_t *out;
@@ -74,17 +75,19 @@ __device__ __forceinline__ void wait_vm() {
 // Every LDS operation of this wave done.
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
-// 16 bytes a lane from anywhere in memory to LDS, lane l's to byte 16 l behind `to` (the same in all
-// lanes).  Written out because the compiler, which cannot tell that a transposed LDS read and such a
-// load in flight touch different stages, would wait for every load before the first of those
-// reads.  It has no register result, and puts m0 back; who reads the stage calls wait_vm first.
-__device__ __forceinline__ void load_lds16(const void *from, const uint16_t *to) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t *)to;
+// 16 bytes a lane from anywhere in memory to LDS, lane l's to byte `to` + 16 l (`to` the same in all lanes).
+// Written out because the compiler, which cannot tell that a transposed LDS read and such a load in
+// flight touch different stages, would wait for every load before the first of those reads.  It has no
+// register result, and puts m0 back; who reads the stage calls wait_vm first.
+__device__ __forceinline__ void load_lds16(const void *from, uint32_t to) {
   uint32_t m0;
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
                : "=&s"(m0)
-               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(from)
+               : "s"(to), "v"(from)
                : "memory");
+}
+__device__ __forceinline__ uint32_t lds_offset(const uint16_t *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t *)p;
 }
 
 // A query fragment times the sign of the scale (0 for a scale of 0), so that the factor left over is above 0.
@@ -149,6 +152,34 @@ struct RowLayout : Layout<DP> {
   __device__ static __forceinline__ int v_slot(int row, int c) { return Layout<DP>::v_slot(row, c) ^ ((row & 4) >> 1); }
 };
 
+// Loads of one wave for a tile of positions: its rows of K and V, chunk c = 64 (S i + W) + lane of load i being row c / kCpr
+// in LDS slot c % kCpr.  `at`: this lane's position's row in units of 16 bytes from the head's first, -1 where it is
+// absent (`exist` has bit l for lane l's position); `first`: this wave's first chunk.
+template <typename L, int LOADS, int STRIDE, int LANES, bool FULL>
+__device__ __forceinline__ void load_tile(const char *k, const char *v, int64_t at, uint64_t exist, int first, int nch,
+                                          uint32_t kb, uint32_t vb) {
+  const int lane = threadIdx.x & 63;
+  constexpr uint64_t kAll = LANES == 64 ? ~0ull : (1ull << LANES) - 1;
+  if (FULL && (exist & kAll) == kAll) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int c = first + 64 * STRIDE * i + lane, r = c / L::kCpr, slot = c % L::kCpr;
+      const int64_t ra = shfl64(at, r) << 4;
+      load_lds16(k + L::k_slot(r, slot) * 16 + ra, kb + (first + 64 * STRIDE * i) * 16);
+      load_lds16(v + L::v_slot(r, slot) * 16 + ra, vb + (first + 64 * STRIDE * i) * 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int c = first + 64 * STRIDE * i + lane, r = c / L::kCpr, slot = c % L::kCpr;
+      const int64_t ra = shfl64(at, r);
+      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
+      load_lds16(pick(ra >= 0 && kc < nch, k + kc * 16 + (ra << 4)), kb + (first + 64 * STRIDE * i) * 16);
+      load_lds16(pick(ra >= 0 && vc < nch, v + vc * 16 + (ra << 4)), vb + (first + 64 * STRIDE * i) * 16);
+    }
+  }
+}
+
 // ----------------------------------------------------------------- row items
 // Up to 16 rows (the query heads of one KV head, for one or a few tokens) against
 // positions [kv_begin, kv_end).  The waves take tiles of 32 positions in turn, each with a
@@ -160,7 +191,7 @@ struct RowLayout : Layout<DP> {
 // W tiles of K and V.
 constexpr int kRowPos = 32;
 
-template <int DP, int W>
+template <int DP, int W, bool FULL>
 __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
   using L = RowLayout<DP>;
   constexpr int KS = DP / 32, DT = DP / 16, LOADS = kRowPos * L::kCpr / 64;
@@ -176,7 +207,7 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
   }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
-  const int D = kv.head_dim, nch = D >> 3;
+  const int D = FULL ? DP : kv.head_dim, nch = D >> 3;
   const int off = wave * kRowPos * DP;  // this wave's part of each stage
 
   // loads: chunk c of a tile is row c / kCpr, LDS slot c % kCpr; lane l of load i takes c = 64 i + l
@@ -188,23 +219,17 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
     const int64_t p = first + (int64_t)tile * kRowPos + (lane & 31);
     return table[inside(p) ? a.page_div((int)p) : 0];
   };
+  const char *kh = (const char *)kv.k + h * kv.head_stride * 2, *vh = (const char *)kv.v + h * kv.head_stride * 2;
   auto issue = [&](auto bufc, int tile, int page) -> uint32_t {
     constexpr int BUF = decltype(bufc)::value;
-    uint16_t *kb = (BUF ? sk1 : sk0) + off, *vb = (BUF ? sv1 : sv0) + off;
     const int p = first + tile * kRowPos + (lane & 31);
     const bool ok = inside(p) && (unsigned)page < (unsigned)kv.num_pages;
     KV_CHECK(ok || !inside(p), LORA_DEBUG_BAD_PAGE);
-    const int64_t at = page * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
-    const int64_t mine = ok ? at : -1;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int c = 64 * i + lane, r = c / L::kCpr, slot = c % L::kCpr;
-      const int64_t ra = shfl64(mine, r);
-      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
-      load_lds16(pick(ra >= 0 && kc < nch, (const uint16_t *)kv.k + ra + kc * 8), kb + 512 * i);
-      load_lds16(pick(ra >= 0 && vc < nch, (const uint16_t *)kv.v + ra + vc * 8), vb + 512 * i);
-    }
-    return (uint32_t)__ballot(ok);  // bit i: the tile's position i exists
+    const int64_t at = (uint64_t)(uint32_t)page * a.page16 + (uint64_t)(uint32_t)(p - a.page_div(p) * kv.page_tokens) * a.token16;
+    const uint64_t exist = __ballot(ok);  // bit i: the tile's position i exists
+    load_tile<L, LOADS, 1, 32, FULL>(kh, vh, ok ? at : -1, exist, 0, nch, lds_offset(BUF ? sk1 : sk0) + off * 2,
+                                     lds_offset(BUF ? sv1 : sv0) + off * 2);
+    return (uint32_t)exist;
   };
 
   // The order of a wave's loads is tile t, pages of t + 2, tile t + 1, pages of t + 3, ...: loads end in
@@ -412,7 +437,24 @@ struct TileLayout : Layout<DP> {
   static constexpr int kLoads = kTilePos * Layout<DP>::kCpr / 64 / kTileWaves;  // per wave and operand
 };
 
-template <int DP>
+// Runs matrix instructions 0 .. N - 1, each with its operand read from LDS kLead instructions earlier.
+// The order is fixed: left to itself the compiler reads each operand just before its use and waits.
+constexpr int kLead = 3;
+template <int N, typename F, typename R, typename M>
+__device__ __forceinline__ void pipelined(R read, M multiply) {
+  F f[kLead + 1];
+#pragma unroll
+  for (int n = 0; n < kLead && n < N; ++n) f[n] = read(n);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (n + kLead < N) f[(n + kLead) % (kLead + 1)] = read(n + kLead);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(n, f[n % (kLead + 1)]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <int DP, bool FULL>
 __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_kernel(Args a) {
   using L = TileLayout<DP>;
   constexpr int KS = DP / 16, DB = DP / 32, SB = kTilePos / 32;
@@ -428,7 +470,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
   }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, hf = lane >> 5;
-  const int D = kv.head_dim, nch = D >> 3;
+  const int D = FULL ? DP : kv.head_dim, nch = D >> 3;
   const bool active = wave * 32 < it.rows;
 
   // loads: lane l looks up the tile's position l; chunk c of a tile is row c / kCpr, LDS slot c % kCpr, and lane l
@@ -441,24 +483,17 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     const int64_t p = first + (int64_t)tile * kTilePos + lane;
     return table[inside(p) ? a.page_div((int)p) : 0];
   };
+  const char *kh = (const char *)kv.k + h * kv.head_stride * 2, *vh = (const char *)kv.v + h * kv.head_stride * 2;
   auto issue = [&](auto bufc, int tile, int page) -> uint64_t {
     constexpr int BUF = decltype(bufc)::value;
-    uint16_t *kb = BUF ? sk1 : sk0, *vb = BUF ? sv1 : sv0;
     const int p = first + tile * kTilePos + lane;
     const bool ok = inside(p) && (unsigned)page < (unsigned)kv.num_pages;
     KV_CHECK(ok || !inside(p), LORA_DEBUG_BAD_PAGE);
-    const int64_t at = page * kv.page_stride + h * kv.head_stride + (p - a.page_div(p) * kv.page_tokens) * kv.token_stride;
-    const int64_t mine = ok ? at : -1;
-#pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
-      const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L::kCpr, slot = c % L::kCpr;
-      const int64_t ra = shfl64(mine, r);
-      const int kc = L::k_slot(r, slot), vc = L::v_slot(r, slot);
-      const int to = 64 * (kTileWaves * i + wave) * 8;
-      load_lds16(pick(ra >= 0 && kc < nch, (const uint16_t *)kv.k + ra + kc * 8), kb + to);
-      load_lds16(pick(ra >= 0 && vc < nch, (const uint16_t *)kv.v + ra + vc * 8), vb + to);
-    }
-    return __ballot(ok);  // bit i: the tile's position i exists
+    const int64_t at = (uint64_t)(uint32_t)page * a.page16 + (uint64_t)(uint32_t)(p - a.page_div(p) * kv.page_tokens) * a.token16;
+    const uint64_t there = __ballot(ok);  // bit i: the tile's position i exists
+    load_tile<L, L::kLoads, kTileWaves, 64, FULL>(kh, vh, ok ? at : -1, there, 64 * wave, nch, lds_offset(BUF ? sk1 : sk0),
+                                                  lds_offset(BUF ? sv1 : sv0));
+    return there;
   };
   int page = tiles > 0 ? lookup(0) : -1;
 
@@ -505,16 +540,15 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     if (active) {
       // S^T: positions are operand rows
 #pragma unroll
-      for (int b = 0; b < SB; ++b) {
-        s[b] = f32x16_t{};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int r = 32 * b + fr;
-          const bf16x8_t kf = __builtin_bit_cast(
-              bf16x8_t, *reinterpret_cast<const uint4 *>(kb + r * DP + L::k_slot(r, 2 * ks + hf) * 8));
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[b], 0, 0, 0);
-        }
-      }
+      for (int b = 0; b < SB; ++b) s[b] = f32x16_t{};
+      pipelined<SB * KS, uint4>(
+          [&](int n) {
+            const int r = 32 * (n / KS) + fr, ks = n % KS;
+            return *reinterpret_cast<const uint4 *>(kb + r * DP + L::k_slot(fr, 2 * ks + hf) * 8);
+          },
+          [&](int n, uint4 kf) {
+            s[n / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), qf[n % KS], s[n / KS], 0, 0, 0);
+          });
       if (!whole) {
         keep = 0;
 #pragma unroll
@@ -600,25 +634,28 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     if (active) {
       // O^T += V^T P^T: k-step ks holds positions 16 ks ..; this lane's half of P has 4 hf .. + 3 and 8 + 4 hf .. + 3
       const int li = lane & 15, vr = 4 * hf + (li >> 2);
+      bf16x8_t pf[kTilePos / 16];
 #pragma unroll
       for (int ks = 0; ks < kTilePos / 16; ++ks) {
         const int b = ks / 2, e = 8 * (ks % 2);
-        const bf16x8_t pf = __builtin_bit_cast(
+        pf[ks] = __builtin_bit_cast(
             bf16x8_t, make_uint4(pack_bf16(s[b][e], s[b][e + 1]), pack_bf16(s[b][e + 2], s[b][e + 3]),
                                  pack_bf16(s[b][e + 4], s[b][e + 5]), pack_bf16(s[b][e + 6], s[b][e + 7])));
-#pragma unroll
-        for (int t = 0; t < DB; ++t) {
-          uint2 x[2];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int r = 16 * ks + 8 * half + vr, c = 4 * t + 2 * (lane >> 4 & 1) + ((li & 3) >> 1);
-            x[half] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4_t *)(vb + r * DP + L::v_slot(vr, c) * 8 + (li & 1) * 4)));
-          }
-          o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8_t, make_uint4(x[0].x, x[0].y, x[1].x, x[1].y)), pf, o[t], 0, 0, 0);
-        }
       }
+      pipelined<kTilePos / 16 * DB, uint4>(
+          [&](int n) {
+            const int ks = n / DB, c = 4 * (n % DB) + 2 * (lane >> 4 & 1) + ((li & 3) >> 1);
+            uint2 x[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              x[half] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (__attribute__((address_space(3))) s16x4_t *)(vb + (16 * ks + 8 * half + vr) * DP + L::v_slot(vr, c) * 8 +
+                                                                (li & 1) * 4)));
+            return make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
+          },
+          [&](int n, uint4 vf) {
+            o[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vf), pf[n / DB], o[n % DB], 0, 0, 0);
+          });
     }
   };
 
@@ -700,18 +737,27 @@ constexpr unsigned kComputeUnits = 256;
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+// Heads of 64, 128 and 256, the usual ones, have kernels without the checks that shorter rows need.
+template <int DP>
+constexpr bool kFull = DP == 64 || DP == 128 || DP == 256;
+template <int DP>
+bool full(const Args &a) { return kFull<DP> && a.kv.head_dim == DP; }
+
 template <int DP>
 void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
   // two workgroups of half the waves share a compute unit's LDS and overlap their ends; a grid that gives
   // every compute unit one at most takes all the waves at once, for a shorter chain of tiles
   constexpr int W = DP <= 64 ? 4 : DP <= 128 ? 2 : 1;
-  if (grid <= kComputeUnits) hipLaunchKernelGGL((attn_rows_kernel<DP, 2 * W>), dim3(grid), dim3(128 * W), 0, stream, a);
-  else hipLaunchKernelGGL((attn_rows_kernel<DP, W>), dim3(grid), dim3(64 * W), 0, stream, a);
+  const auto wide = full<DP>(a) ? attn_rows_kernel<DP, 2 * W, kFull<DP>> : attn_rows_kernel<DP, 2 * W, false>;
+  const auto slim = full<DP>(a) ? attn_rows_kernel<DP, W, kFull<DP>> : attn_rows_kernel<DP, W, false>;
+  if (grid <= kComputeUnits) hipLaunchKernelGGL(wide, dim3(grid), dim3(128 * W), 0, stream, a);
+  else hipLaunchKernelGGL(slim, dim3(grid), dim3(64 * W), 0, stream, a);
 }
 
 template <int DP>
 void launch_tiles(const Args &a, unsigned grid, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_tile_kernel<DP>, dim3(grid), dim3(64 * kTileWaves), 0, stream, a);
+  const auto kernel = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>> : attn_tile_kernel<DP, false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * kTileWaves), 0, stream, a);
 }
 
 }  // namespace
@@ -735,6 +781,8 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   const int64_t strides[4] = {q_token_stride, q_head_stride, out_token_stride, out_head_stride};
   for (int64_t s : strides)
     if (s < 0 || s % 8) return fail(LORA_EINVAL, "strides of q and out must be multiples of 8 elements, not negative");
+  if (kv->page_stride / 8 > UINT32_MAX || kv->token_stride / 8 > UINT32_MAX)
+    return fail(LORA_EUNSUPPORTED, "KV strides of 2^35 elements and more");
   if (!std::isfinite(scale)) return fail(LORA_EINVAL, "scale is not finite");
   const int64_t part_floats = (int64_t)plan->num_part_rows * kv->kv_heads * kv->head_dim;
   const int64_t need = plan->num_part_rows * (int64_t)kv->kv_heads * (kv->head_dim + 4) * (int64_t)sizeof(float);
@@ -759,6 +807,8 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   a.o_ts = out_token_stride;
   a.o_hs = out_head_stride;
   a.page_div = Div((uint32_t)kv->page_tokens);
+  a.page16 = (uint32_t)(kv->page_stride / 8);
+  a.token16 = (uint32_t)(kv->token_stride / 8);
   a.scale2 = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
   a.q_and = scale == 0.f ? 0u : ~0u;
   a.q_xor = scale < 0.f ? 0x80008000u : 0u;
