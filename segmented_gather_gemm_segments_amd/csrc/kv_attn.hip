@@ -140,7 +140,9 @@ constexpr float kSlack = 8.f;
 template <int DP>
 struct Layout {
   static constexpr int kCpr = DP / 8;  // chunks per row
-  __device__ static __forceinline__ int k_slot(int row, int c) { return c ^ (row & (kCpr % 8 ? 3 : 7)); }
+  __device__ static __forceinline__ int k_slot(int row, int c) {
+    return c ^ (row & (kCpr % 16 == 0 ? 15 : kCpr % 8 == 0 ? 7 : 3));
+  }
   __device__ static __forceinline__ int v_slot(int row, int c) {
     if constexpr (kCpr % 16 == 0) return c ^ ((row & 3) << 2);
     else if constexpr (kCpr % 8 == 0) return c ^ ((row & 2) << 1);
@@ -537,17 +539,18 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     // element i of block b is position t0 + 32 b + 8 (i / 4) + 4 hf + i % 4
     f32x16_t s[SB];
     uint32_t keep = ~0u;
+    float base = 0.f;
     if (active) {
-      // S^T: positions are operand rows
+      // S^T: positions are operand rows; the blocks in turn, so that no product waits for the one before
 #pragma unroll
       for (int b = 0; b < SB; ++b) s[b] = f32x16_t{};
       pipelined<SB * KS, uint4>(
           [&](int n) {
-            const int r = 32 * (n / KS) + fr, ks = n % KS;
+            const int r = 32 * (n % SB) + fr, ks = n / SB;
             return *reinterpret_cast<const uint4 *>(kb + r * DP + L::k_slot(fr, 2 * ks + hf) * 8);
           },
           [&](int n, uint4 kf) {
-            s[n / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), qf[n % KS], s[n / KS], 0, 0, 0);
+            s[n % SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), qf[n / SB], s[n % SB], 0, 0, 0);
           });
       if (!whole) {
         keep = 0;
@@ -578,16 +581,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
         for (int t = 0; t < DB; ++t) o[t] *= corr;
         m = mn;
       }
-      const float base = m == -INFINITY ? 0.f : m * a.scale2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int b = 0; b < SB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], a.scale2, -base));
-          sum[i & 3] += s[b][i];
-        }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      base = m == -INFINITY ? 0.f : m * a.scale2;
     }
     if (!whole) {
       // 0 * inf is NaN: values of V that are not finite are added where they are kept, one position at a
@@ -613,7 +607,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
             for (int b = 0; b < SB; ++b)
 #pragma unroll
               for (int i = 0; i < 16; ++i) pv = idx == 16 * b + i ? s[b][i] : pv;
-            pv = __shfl(pv, from);
+            pv = __shfl(__builtin_amdgcn_exp2f(fmaf(pv, a.scale2, -base)), from);
             const bool ok = __shfl((int)(keep >> idx & 1), from);
 #pragma unroll
             for (int t = 0; t < DB; ++t)
@@ -634,14 +628,24 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     if (active) {
       // O^T += V^T P^T: k-step ks holds positions 16 ks ..; this lane's half of P has 4 hf .. + 3 and 8 + 4 hf .. + 3
       const int li = lane & 15, vr = 4 * hf + (li >> 2);
+      // The second block's weights are computed between the first block's products, which leave the vector
+      // units free.
       bf16x8_t pf[kTilePos / 16];
-#pragma unroll
-      for (int ks = 0; ks < kTilePos / 16; ++ks) {
+      float sum[2] = {0.f, 0.f};
+      auto weigh = [&](int b, int i) {
+        s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], a.scale2, -base));
+        sum[i & 1] += s[b][i];
+      };
+      auto round8 = [&](int ks) {
         const int b = ks / 2, e = 8 * (ks % 2);
         pf[ks] = __builtin_bit_cast(
             bf16x8_t, make_uint4(pack_bf16(s[b][e], s[b][e + 1]), pack_bf16(s[b][e + 2], s[b][e + 3]),
                                  pack_bf16(s[b][e + 4], s[b][e + 5]), pack_bf16(s[b][e + 6], s[b][e + 7])));
-      }
+      };
+#pragma unroll
+      for (int i = 0; i < 16; ++i) weigh(0, i);
+      round8(0);
+      round8(1);
       pipelined<kTilePos / 16 * DB, uint4>(
           [&](int n) {
             const int ks = n / DB, c = 4 * (n % DB) + 2 * (lane >> 4 & 1) + ((li & 3) >> 1);
@@ -655,7 +659,14 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
           },
           [&](int n, uint4 vf) {
             o[n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vf), pf[n / DB], o[n % DB], 0, 0, 0);
+            // 16 weights over the 2 DB products of the first block
+#pragma unroll
+            for (int i = 16 * n / (2 * DB); i < 16 * (n + 1) / (2 * DB) && i < 16; ++i) {
+              weigh(1, i);
+              if (i % 8 == 7) round8(2 + i / 8);
+            }
           });
+      l += sum[0] + sum[1];
     }
   };
 
