@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "lora_internal.h"
 #include "lora_w4.h"
@@ -28,15 +29,17 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 constexpr int kTileBytes = 1024;   // codes of 16 rows x 128 k
 constexpr int kTileK = 128;
 constexpr int kWaves = 8;
+constexpr int kComputeUnits = 256;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));  // nearest even
 }
 
-// Four consecutive scales (or zero points) of one group, widened.
-__device__ __forceinline__ f32x4_t load4(const float *p) { return *reinterpret_cast<const f32x4_t *>(p); }
-__device__ __forceinline__ f32x4_t load4(const uint16_t *p) {
-  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+// Four consecutive scales (or zero points) of one group as they are stored, and widened.
+template <typename S>
+using Four = std::conditional_t<sizeof(S) == 2, uint2, f32x4_t>;
+__device__ __forceinline__ f32x4_t values(f32x4_t u) { return u; }
+__device__ __forceinline__ f32x4_t values(uint2 u) {
   return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                  __uint_as_float(u.y & 0xffff0000u)};
 }
@@ -51,33 +54,62 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w) {
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
-// One workgroup: 16 rows of W (one row tile) and 16 MT tokens.  Its waves take
-// the tile columns in turn; their fp32 sums are added in wave order through
-// LDS.
-template <int MT, int G, typename S, bool Z>
-__global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int k, int col_tiles,
+// One workgroup: NT row tiles of W (16 rows each) and 16 MT tokens.  Its waves take the tile columns
+// (128 k) in turn, each with the next column's codes and scales on their way while it works on this one; their
+// fp32 sums are added in wave order through LDS.  Nothing is shared between waves before that, so x goes
+// from the L2 to the registers of the one wave that needs it.
+template <int MT, int NT, int G, typename S, bool Z>
+__global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
                                                               const uint8_t *__restrict__ codes,
                                                               const S *__restrict__ scales,
                                                               const S *__restrict__ zeros,
                                                               const uint16_t *__restrict__ x, int64_t x_stride,
                                                               uint16_t *__restrict__ y, int64_t y_stride) {
+  constexpr int GT = kTileK / G;  // groups per tile column
   __shared__ f32x4_t red[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int fr = lane & 15, fg = lane >> 4;
-  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (16 * MT);
-  const int nrow = min(n0 + 4 * fg, n - 4);  // rows of this lane's results (clamped: results past n are not stored)
-  const uint8_t *cp = codes + (int64_t)blockIdx.x * col_tiles * kTileBytes + lane * 16;
+  const int r0 = blockIdx.x * NT, t0 = blockIdx.y * (16 * MT);
+  const int groups = k / G;
+  const uint8_t *cp[NT];
+  int nrow[NT];  // first of the 4 rows that this lane holds results of (clamped: results past n are not stored)
+#pragma unroll
+  for (int a = 0; a < NT; ++a) {
+    cp[a] = codes + (int64_t)min(r0 + a, row_tiles - 1) * col_tiles * kTileBytes + lane * 16;
+    nrow[a] = min((r0 + a) * 16 + 4 * fg, n - 4);
+  }
   const uint16_t *xp[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) xp[i] = x + (int64_t)min(t0 + 16 * i + fr, m - 1) * x_stride + fg * 8;
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
-  f32x4_t sum[MT];
+  f32x4_t sum[NT][MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sum[a][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+  struct Column {
+    uint4 c[NT];
+    Four<S> s[NT][GT], z[NT][Z ? GT : 1];
+  };
+  auto fetch = [&](int kt, Column &col) {
+    kt = min(kt, col_tiles - 1);
+#pragma unroll
+    for (int a = 0; a < NT; ++a) {
+      col.c[a] = *reinterpret_cast<const uint4 *>(cp[a] + (int64_t)kt * kTileBytes);
+#pragma unroll
+      for (int g = 0; g < GT; ++g) {
+        const int64_t at = (int64_t)min(kt * GT + g, groups - 1) * n + nrow[a];
+        col.s[a][g] = *reinterpret_cast<const Four<S> *>(scales + at);
+        if constexpr (Z) col.z[a][g] = *reinterpret_cast<const Four<S> *>(zeros + at);
+      }
+    }
+  };
+
+  Column next;
+  fetch(wave, next);
   for (int kt = wave; kt < col_tiles; kt += kWaves) {
-    const uint4 c = *reinterpret_cast<const uint4 *>(cp + (int64_t)kt * kTileBytes);
-    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+    const Column col = next;
     bf16x8_t xf[MT][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -89,41 +121,55 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
         xf[i][s] = __builtin_bit_cast(bf16x8_t, q);
       }
     }
+    fetch(kt + kWaves, next);
 #pragma unroll
-    for (int g = 0; g < kTileK / G; ++g) {
-      const int kg = kt * (kTileK / G) + g;
-      if (kg * G >= k) break;
-      const f32x4_t sc = load4(scales + (int64_t)kg * n + nrow);
-      f32x4_t off = f32x4_t{136.f, 136.f, 136.f, 136.f};
-      if constexpr (Z) off = load4(zeros + (int64_t)kg * n + nrow) + 128.f;
+    for (int g = 0; g < GT; ++g) {
+      if ((kt * GT + g) * G >= k) break;  // the last column of a k that is no multiple of 128
+      f32x4_t xs[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        f32x4_t t = f32x4_t{0.f, 0.f, 0.f, 0.f}, xs = t;
+        xs[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s)
+          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf[i][s], xs[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int a = 0; a < NT; ++a) {
+        const uint32_t cw[4] = {col.c[a].x, col.c[a].y, col.c[a].z, col.c[a].w};
+        f32x4_t t[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) t[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
-          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(cw[s]), xf[i][s], t, 0, 0, 0);
-          xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf[i][s], xs, 0, 0, 0);
+          const bf16x8_t wf = widen(cw[s]);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[i][s], t[i], 0, 0, 0);
         }
+        const f32x4_t sc = values(col.s[a][g]);
+        f32x4_t off = f32x4_t{136.f, 136.f, 136.f, 136.f};
+        if constexpr (Z) off = values(col.z[a][g]) + 128.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i][j] += sc[j] * (t[j] - off[j] * xs[0]);
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[a][i][j] += sc[j] * (t[i][j] - off[j] * xs[i][0]);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    __syncthreads();
-    red[wave][lane] = sum[i];
-    __syncthreads();
-    if (wave == i % kWaves) {
-      f32x4_t a = red[0][lane];
-      for (int w = 1; w < kWaves; ++w) a += red[w][lane];
-      const int t = t0 + 16 * i + fr, col = n0 + 4 * fg;
-      if (t < m && col < n) {
-        uint2 o = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
-        *reinterpret_cast<uint2 *>(y + (int64_t)t * y_stride + col) = o;
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      __syncthreads();
+      red[wave][lane] = sum[a][i];
+      __syncthreads();
+      if (wave == (a * MT + i) % kWaves) {
+        f32x4_t v = red[0][lane];
+        for (int w = 1; w < kWaves; ++w) v += red[w][lane];
+        const int t = t0 + 16 * i + fr, c = (r0 + a) * 16 + 4 * fg;
+        if (t < m && c < n)
+          *reinterpret_cast<uint2 *>(y + (int64_t)t * y_stride + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       }
     }
-  }
 }
 
 // Thread: one 32-bit word of the tiled codes.
@@ -157,18 +203,31 @@ struct W4Call {
   hipStream_t stream;
 };
 
-template <int MT, int G, typename S, bool Z>
+template <int MT, int NT, int G, typename S, bool Z>
 void launch(const W4Call &c) {
-  hipLaunchKernelGGL((base_w4_kernel<MT, G, S, Z>), dim3((c.n + 15) / 16, (c.m + 16 * MT - 1) / (16 * MT)),
-                     dim3(64 * kWaves), 0, c.stream, c.m, c.n, c.k, c.col_tiles, (const uint8_t *)c.w->codes,
+  const int row_tiles = (c.n + 15) / 16;
+  hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT - 1) / NT, (c.m + 16 * MT - 1) / (16 * MT)),
+                     dim3(64 * kWaves), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
                      (const S *)c.w->scales, (const S *)c.w->zeros, c.x, c.xs, c.y, c.ys);
+}
+// Row tiles per workgroup: as many as still leave every compute unit a workgroup.  More tiles share the
+// reads of x, which for 16 tokens are four times those of one row tile's codes.  At most kMost, so that the
+// scales and zero points on their way (WORDS registers a tile) and the sums fit the registers.
+template <int MT, int G, typename S, bool Z>
+void pick_tiles(const W4Call &c) {
+  constexpr int kWords = kTileK / G * (int)sizeof(S) * (Z ? 2 : 1);
+  constexpr int kMost = MT == 4 ? (kWords <= 8 ? 2 : 1) : 64 / MT / kWords;
+  const int row_tiles = (c.n + 15) / 16;
+  if (kMost >= 4 && row_tiles >= 4 * kComputeUnits) launch<MT, kMost >= 4 ? 4 : 1, G, S, Z>(c);
+  else if (kMost >= 2 && row_tiles >= 2 * kComputeUnits) launch<MT, kMost >= 2 ? 2 : 1, G, S, Z>(c);
+  else launch<MT, 1, G, S, Z>(c);
 }
 template <int MT, int G>
 void pick_scale(const W4Call &c) {
   if (c.w->scale_dtype == LORA_BF16)
-    c.w->zeros ? launch<MT, G, uint16_t, true>(c) : launch<MT, G, uint16_t, false>(c);
+    c.w->zeros ? pick_tiles<MT, G, uint16_t, true>(c) : pick_tiles<MT, G, uint16_t, false>(c);
   else
-    c.w->zeros ? launch<MT, G, float, true>(c) : launch<MT, G, float, false>(c);
+    c.w->zeros ? pick_tiles<MT, G, float, true>(c) : pick_tiles<MT, G, float, false>(c);
 }
 template <int MT>
 void pick_group(const W4Call &c) {
