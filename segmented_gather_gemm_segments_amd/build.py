@@ -27,7 +27,7 @@ SOURCES = [os.path.join(HERE, "csrc", "host.cpp"), os.path.join(HERE, "csrc", "k
 HEADERS = [os.path.join(ROOT, "include", "lora_sgmv.h"), os.path.join(ROOT, "include", "lora_probe.h"),
            os.path.join(ROOT, "include", "lora_w4.h"), os.path.join(ROOT, "include", "lora_kv.h"),
            os.path.join(HERE, "csrc", "lora_internal.h"), os.path.join(HERE, "csrc", "kv_internal.h"),
-           os.path.join(HERE, "csrc", "kv_debug.h")]
+           os.path.join(HERE, "csrc", "kv_debug.h"), os.path.join(HERE, "csrc", "lds_load.h")]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",

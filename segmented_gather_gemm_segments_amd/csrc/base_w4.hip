@@ -16,6 +16,7 @@
 
 #include "lora_internal.h"
 #include "lora_w4.h"
+#include "lds_load.h"
 
 using namespace lora;
 
@@ -28,7 +29,9 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
 constexpr int kTileBytes = 1024;   // codes of 16 rows x 128 k
 constexpr int kTileK = 128;
-constexpr int kWaves = 8;
+template <int MT>
+constexpr int kWaves = MT == 4 ? 4 : 8;  // what two stages of x leave room for
+__device__ const uint4 g_zeros = {0, 0, 0, 0};  // x behind the last k
 constexpr int kComputeUnits = 256;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -55,19 +58,21 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w) {
 }
 
 // One workgroup: NT row tiles of W (16 rows each) and 16 MT tokens.  Its waves take the tile columns
-// (128 k) in turn, each with the next column's codes and scales on their way while it works on this one; their
-// fp32 sums are added in wave order through LDS.  Nothing is shared between waves before that, so x goes
-// from the L2 to the registers of the one wave that needs it.
+// (128 k) in turn, each with the next column's codes, scales and x on their way while it works on this one;
+// their fp32 sums are added in wave order through LDS.  x goes through LDS stages of the wave's own: read as
+// operands straight from memory, every lane would name a line of its own, and the address units, which
+// take those one by one, would set the time (16 tokens, 28672 x 8192: 33.4 us).
 template <int MT, int NT, int G, typename S, bool Z>
-__global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
+__global__ __launch_bounds__(64 * kWaves<MT>) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
                                                               const uint8_t *__restrict__ codes,
                                                               const S *__restrict__ scales,
                                                               const S *__restrict__ zeros,
                                                               const uint16_t *__restrict__ x, int64_t x_stride,
                                                               uint16_t *__restrict__ y, int64_t y_stride) {
   constexpr int GT = kTileK / G;  // groups per tile column
-  __shared__ f32x4_t red[kWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int W = kWaves<MT>, kStage = 16 * MT * kTileK;  // elements of x
+  __shared__ __attribute__((aligned(16))) uint16_t sx[2 * W * kStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
   const int r0 = blockIdx.x * NT, t0 = blockIdx.y * (16 * MT);
   const int groups = k / G;
@@ -78,9 +83,23 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
     cp[a] = codes + (int64_t)min(r0 + a, row_tiles - 1) * col_tiles * kTileBytes + lane * 16;
     nrow[a] = min((r0 + a) * 16 + 4 * fg, n - 4);
   }
-  const uint16_t *xp[MT];
+  // x: load i of a wave takes 4 tokens of 256 bytes, lane l 16 of them; chunk c of a token is stored in slot
+  // c ^ (token & 15), so that the 16 lanes that read one chunk of 16 tokens hit every bank once
+  const uint16_t *xp[4 * MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) xp[i] = x + (int64_t)min(t0 + 16 * i + fr, m - 1) * x_stride + fg * 8;
+  for (int i = 0; i < 4 * MT; ++i) {
+    const int t = 4 * i + (lane >> 4);
+    xp[i] = x + (int64_t)min(t0 + t, m - 1) * x_stride + ((lane ^ t) & 15) * 8;
+  }
+  uint16_t *stage = sx + wave * 2 * kStage;
+  auto load_x = [&](int kt, int buf) {
+#pragma unroll
+    for (int i = 0; i < 4 * MT; ++i) {
+      const int kk = kt * kTileK + ((lane ^ (4 * i + (lane >> 4))) & 15) * 8;
+      load_lds16(kk < k ? (const void *)(xp[i] + kt * kTileK) : (const void *)&g_zeros,
+                 lds_offset(sx) + (uint32_t)((wave * 2 + buf) * kStage + i * 512) * 2);
+    }
+  };
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
   f32x4_t sum[NT][MT];
 #pragma unroll
@@ -108,20 +127,21 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
 
   Column next;
   fetch(wave, next);
-  for (int kt = wave; kt < col_tiles; kt += kWaves) {
+  if (wave < col_tiles) load_x(wave, 0);
+  int buf = 0;
+  for (int kt = wave; kt < col_tiles; kt += W, buf ^= 1) {
+    wait_vm<0>();  // this column has landed (only this wave reads its stages)
+    wait_lds();    // and the other stage has been read
     const Column col = next;
+    fetch(kt + W, next);
+    if (kt + W < col_tiles) load_x(kt + W, buf ^ 1);
     bf16x8_t xf[MT][4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int k0 = kt * kTileK + s * 32;
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (k0 < k) q = *reinterpret_cast<const uint4 *>(xp[i] + k0);  // uniform: k is a multiple of 32
-        xf[i][s] = __builtin_bit_cast(bf16x8_t, q);
-      }
-    }
-    fetch(kt + kWaves, next);
+      for (int i = 0; i < MT; ++i)
+        xf[i][s] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4 *>(
+            stage + buf * kStage + (16 * i + fr) * kTileK + (((4 * s + fg) ^ fr) & 15) * 8));
 #pragma unroll
     for (int g = 0; g < GT; ++g) {
       if ((kt * GT + g) * G >= k) break;  // the last column of a k that is no multiple of 128
@@ -155,16 +175,17 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
       }
     }
   }
+  f32x4_t *red = reinterpret_cast<f32x4_t *>(sx);  // [W][64]
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       __syncthreads();
-      red[wave][lane] = sum[a][i];
+      red[wave * 64 + lane] = sum[a][i];
       __syncthreads();
-      if (wave == (a * MT + i) % kWaves) {
-        f32x4_t v = red[0][lane];
-        for (int w = 1; w < kWaves; ++w) v += red[w][lane];
+      if (wave == (a * MT + i) % W) {
+        f32x4_t v = red[lane];
+        for (int w = 1; w < W; ++w) v += red[w * 64 + lane];
         const int t = t0 + 16 * i + fr, c = (r0 + a) * 16 + 4 * fg;
         if (t < m && c < n)
           *reinterpret_cast<uint2 *>(y + (int64_t)t * y_stride + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
@@ -207,7 +228,7 @@ template <int MT, int NT, int G, typename S, bool Z>
 void launch(const W4Call &c) {
   const int row_tiles = (c.n + 15) / 16;
   hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT - 1) / NT, (c.m + 16 * MT - 1) / (16 * MT)),
-                     dim3(64 * kWaves), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
+                     dim3(64 * kWaves<MT>), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
                      (const S *)c.w->scales, (const S *)c.w->zeros, c.x, c.xs, c.y, c.ys);
 }
 // Row tiles per workgroup: as many as still leave every compute unit a workgroup.  More tiles share the
