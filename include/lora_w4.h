@@ -67,7 +67,7 @@ lora_status lora_w4_pack(int32_t n, int32_t k, int32_t twos_complement, const vo
  * m == 0 is a no-op.  x and y must not overlap.
  * Errors: LORA_EINVAL (null or misaligned pointers, sizes, strides),
  * LORA_EUNSUPPORTED (dtype, scale_dtype, group, n or k not multiples as
- * above), LORA_EHIP. */
+ * above, an x_stride above 2^24), LORA_EHIP. */
 lora_status lora_base_w4(int32_t dtype, int32_t m, const lora_w4_weights *w, const void *x,
                          int64_t x_stride, void *y, int64_t y_stride, hipStream_t stream);
 

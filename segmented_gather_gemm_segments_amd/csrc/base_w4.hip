@@ -29,8 +29,9 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
 constexpr int kTileBytes = 1024;   // codes of 16 rows x 128 k
 constexpr int kTileK = 128;
+constexpr int kWaves = 8;
 template <int MT>
-constexpr int kWaves = MT == 4 ? 4 : 8;  // what two stages of x leave room for
+constexpr int kRowWaves = MT == 4 ? 2 : 1;  // waves that share stages of x, so that two of each fit the LDS
 __device__ const uint4 g_zeros = {0, 0, 0, 0};  // x behind the last k
 constexpr int kComputeUnits = 256;
 
@@ -57,47 +58,55 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w) {
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
-// One workgroup: NT row tiles of W (16 rows each) and 16 MT tokens.  Its waves take the tile columns
-// (128 k) in turn, each with the next column's codes, scales and x on their way while it works on this one;
-// their fp32 sums are added in wave order through LDS.  x goes through LDS stages of the wave's own: read as
-// operands straight from memory, every lane would name a line of its own, and the address units, which
+// One workgroup: R NT row tiles of W (16 rows each) and 16 MT tokens.  Its waves, in groups of R that share
+// x and have NT row tiles each, take the tile columns (128 k) in turn, each with the next column's codes,
+// scales and x on their way while it works on this one; their fp32 sums are added in order through LDS.
+// x goes through two LDS stages of each group: read as operands straight from memory, every lane would name a line of its own, and the address units, which
 // take those one by one, would set the time (16 tokens, 28672 x 8192: 33.4 us).
 template <int MT, int NT, int G, typename S, bool Z>
-__global__ __launch_bounds__(64 * kWaves<MT>) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
+__global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
                                                               const uint8_t *__restrict__ codes,
                                                               const S *__restrict__ scales,
                                                               const S *__restrict__ zeros,
                                                               const uint16_t *__restrict__ x, int64_t x_stride,
                                                               uint16_t *__restrict__ y, int64_t y_stride) {
   constexpr int GT = kTileK / G;  // groups per tile column
-  constexpr int W = kWaves<MT>, kStage = 16 * MT * kTileK;  // elements of x
+  constexpr int R = kRowWaves<MT>, W = kWaves / R, kStage = 16 * MT * kTileK;  // elements of x
   __shared__ __attribute__((aligned(16))) uint16_t sx[2 * W * kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
-  const int r0 = blockIdx.x * NT, t0 = blockIdx.y * (16 * MT);
+  const int kw = wave / R, r0 = (blockIdx.x * R + wave % R) * NT, t0 = blockIdx.y * (16 * MT);
   const int groups = k / G;
+  // Addresses are a part that all lanes share, which the scalar unit steps, and a fixed 32-bit offset per lane.
   const uint8_t *cp[NT];
-  int nrow[NT];  // first of the 4 rows that this lane holds results of (clamped: results past n are not stored)
+  uint32_t nrow[NT];  // first of the 4 rows that this lane holds results of (clamped: results past n are not stored)
 #pragma unroll
   for (int a = 0; a < NT; ++a) {
-    cp[a] = codes + (int64_t)min(r0 + a, row_tiles - 1) * col_tiles * kTileBytes + lane * 16;
+    cp[a] = codes + (int64_t)min(r0 + a, row_tiles - 1) * col_tiles * kTileBytes;
     nrow[a] = min((r0 + a) * 16 + 4 * fg, n - 4);
   }
   // x: load i of a wave takes 4 tokens of 256 bytes, lane l 16 of them; chunk c of a token is stored in slot
   // c ^ (token & 15), so that the 16 lanes that read one chunk of 16 tokens hit every bank once
-  const uint16_t *xp[4 * MT];
+  constexpr int LOADS = 4 * MT / R;
+  uint32_t xo[LOADS];
 #pragma unroll
-  for (int i = 0; i < 4 * MT; ++i) {
-    const int t = 4 * i + (lane >> 4);
-    xp[i] = x + (int64_t)min(t0 + t, m - 1) * x_stride + ((lane ^ t) & 15) * 8;
+  for (int i = 0; i < LOADS; ++i) {
+    const int t = 4 * (LOADS * (wave % R) + i) + (lane >> 4);
+    xo[i] = ((uint32_t)min(t, m - 1 - t0) * (uint32_t)x_stride + ((lane ^ t) & 15) * 8) * 2;
   }
-  uint16_t *stage = sx + wave * 2 * kStage;
+  const uint16_t *xt = x + (int64_t)t0 * x_stride;
+  uint16_t *stage = sx + kw * 2 * kStage;
   auto load_x = [&](int kt, int buf) {
+    const uint32_t to = lds_offset(sx) + (uint32_t)((kw * 2 + buf) * kStage + LOADS * (wave % R) * 512) * 2;
+    if ((kt + 1) * kTileK <= k) {
 #pragma unroll
-    for (int i = 0; i < 4 * MT; ++i) {
-      const int kk = kt * kTileK + ((lane ^ (4 * i + (lane >> 4))) & 15) * 8;
-      load_lds16(kk < k ? (const void *)(xp[i] + kt * kTileK) : (const void *)&g_zeros,
-                 lds_offset(sx) + (uint32_t)((wave * 2 + buf) * kStage + i * 512) * 2);
+      for (int i = 0; i < LOADS; ++i) load_lds16(xt + kt * kTileK, xo[i], to + i * 1024);
+    } else {  // zeros behind the last k
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int t = 4 * (LOADS * (wave % R) + i) + (lane >> 4), kk = kt * kTileK + ((lane ^ t) & 15) * 8;
+        load_lds16(kk < k ? (const char *)(xt + kt * kTileK) + xo[i] : (const char *)&g_zeros, to + i * 1024);
+      }
     }
   };
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
@@ -115,23 +124,28 @@ __global__ __launch_bounds__(64 * kWaves<MT>) void base_w4_kernel(int m, int n, 
     kt = min(kt, col_tiles - 1);
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
-      col.c[a] = *reinterpret_cast<const uint4 *>(cp[a] + (int64_t)kt * kTileBytes);
+      col.c[a] = *reinterpret_cast<const uint4 *>(cp[a] + (int64_t)kt * kTileBytes + (uint32_t)lane * 16);
 #pragma unroll
       for (int g = 0; g < GT; ++g) {
-        const int64_t at = (int64_t)min(kt * GT + g, groups - 1) * n + nrow[a];
-        col.s[a][g] = *reinterpret_cast<const Four<S> *>(scales + at);
-        if constexpr (Z) col.z[a][g] = *reinterpret_cast<const Four<S> *>(zeros + at);
+        const int64_t at = (int64_t)min(kt * GT + g, groups - 1) * n;
+        col.s[a][g] = *reinterpret_cast<const Four<S> *>(scales + at + nrow[a]);
+        if constexpr (Z) col.z[a][g] = *reinterpret_cast<const Four<S> *>(zeros + at + nrow[a]);
       }
     }
   };
 
   Column next;
-  fetch(wave, next);
-  if (wave < col_tiles) load_x(wave, 0);
+  fetch(kw, next);
+  if (kw < col_tiles) load_x(kw, 0);
   int buf = 0;
-  for (int kt = wave; kt < col_tiles; kt += W, buf ^= 1) {
-    wait_vm<0>();  // this column has landed (only this wave reads its stages)
+  // waves that share stages go through the loop together, the last time some without a column
+  for (int kt = kw; R > 1 ? kt - kw < col_tiles : kt < col_tiles; kt += W, buf ^= 1) {
+    wait_vm<0>();  // this column has landed
     wait_lds();    // and the other stage has been read
+    if constexpr (R > 1) {
+      __syncthreads();
+      if (kt >= col_tiles) continue;
+    }
     const Column col = next;
     fetch(kt + W, next);
     if (kt + W < col_tiles) load_x(kt + W, buf ^ 1);
@@ -175,7 +189,7 @@ __global__ __launch_bounds__(64 * kWaves<MT>) void base_w4_kernel(int m, int n, 
       }
     }
   }
-  f32x4_t *red = reinterpret_cast<f32x4_t *>(sx);  // [W][64]
+  f32x4_t *red = reinterpret_cast<f32x4_t *>(sx);  // [kWaves][64]
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -183,9 +197,9 @@ __global__ __launch_bounds__(64 * kWaves<MT>) void base_w4_kernel(int m, int n, 
       __syncthreads();
       red[wave * 64 + lane] = sum[a][i];
       __syncthreads();
-      if (wave == (a * MT + i) % W) {
-        f32x4_t v = red[lane];
-        for (int w = 1; w < W; ++w) v += red[w * 64 + lane];
+      if (kw == (a * MT + i) % W) {
+        f32x4_t v = red[wave % R * 64 + lane];
+        for (int w = 1; w < W; ++w) v += red[(w * R + wave % R) * 64 + lane];
         const int t = t0 + 16 * i + fr, c = (r0 + a) * 16 + 4 * fg;
         if (t < m && c < n)
           *reinterpret_cast<uint2 *>(y + (int64_t)t * y_stride + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
@@ -227,8 +241,8 @@ struct W4Call {
 template <int MT, int NT, int G, typename S, bool Z>
 void launch(const W4Call &c) {
   const int row_tiles = (c.n + 15) / 16;
-  hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT - 1) / NT, (c.m + 16 * MT - 1) / (16 * MT)),
-                     dim3(64 * kWaves<MT>), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
+  hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT * kRowWaves<MT> - 1) / (NT * kRowWaves<MT>), (c.m + 16 * MT - 1) / (16 * MT)),
+                     dim3(64 * kWaves), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
                      (const S *)c.w->scales, (const S *)c.w->zeros, c.x, c.xs, c.y, c.ys);
 }
 // Row tiles per workgroup: as many as still leave every compute unit a workgroup.  More tiles share the
@@ -238,7 +252,7 @@ template <int MT, int G, typename S, bool Z>
 void pick_tiles(const W4Call &c) {
   constexpr int kWords = kTileK / G * (int)sizeof(S) * (Z ? 2 : 1);
   constexpr int kMost = MT == 4 ? (kWords <= 8 ? 2 : 1) : 64 / MT / kWords;
-  const int row_tiles = (c.n + 15) / 16;
+  const int row_tiles = (c.n + 15) / 16 / kRowWaves<MT>;
   if (kMost >= 4 && row_tiles >= 4 * kComputeUnits) launch<MT, kMost >= 4 ? 4 : 1, G, S, Z>(c);
   else if (kMost >= 2 && row_tiles >= 2 * kComputeUnits) launch<MT, kMost >= 2 ? 2 : 1, G, S, Z>(c);
   else launch<MT, 1, G, S, Z>(c);
@@ -299,6 +313,7 @@ extern "C" lora_status lora_base_w4(int32_t dtype, int32_t m, const lora_w4_weig
   if (x_stride < w->k || y_stride < w->n || x_stride % 8 || y_stride % 8)
     return fail(LORA_EINVAL, "row strides must be multiples of 8 of at least k and n (got %lld and %lld)",
                 (long long)x_stride, (long long)y_stride);
+  if (x_stride > (1 << 24)) return fail(LORA_EUNSUPPORTED, "an x row stride above 2^24");
   if (m == 0) return ok();
   if (!w->codes || !w->scales || !x || !y) return fail(LORA_EINVAL, "null pointer");
   if (!aligned16(w->codes) || !aligned16(w->scales) || !aligned16(w->zeros) || !aligned16(x) || !aligned16(y))
