@@ -739,6 +739,27 @@ class _On:
             self._guard.__exit__(*exc)
 
 
+def _launch(name: str, index: int, stream, *args):
+    """Calls a device function on the current stream of device `index` (or `stream`); what these calls cost on the
+    host is what a small one costs in all, so this is the short way to what _On does."""
+    fn = getattr(_lib or lib(), name)
+    torch = _torch()
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != LORA_OK:
+        _check(status)
+
+
+def _gpu(device) -> int:
+    if device.type != "cuda":
+        _refuse(f"tensors must be on a GPU, not {device}")
+    return device.index
+
+
 def lora_w4_bytes(n: int, k: int) -> int:
     out = ctypes.c_int64(0)
     _check(lib().lora_w4_bytes(n, k, ctypes.byref(out)))
@@ -781,20 +802,24 @@ class W4Weights:
         self.codes, self.scales, self.zeros = codes, scales, zeros
         self.desc = lora_w4_weights(n, k, group, LORA_BF16 if scales.dtype == torch.bfloat16 else LORA_F32,
                                     _dptr(codes), _dptr(scales), _dptr(zeros))
+        self.ref, self.index, self.bf16 = ctypes.byref(self.desc), codes.get_device(), torch.bfloat16
+        self.one_x, self.one_y = k + -k % 8, n + -n % 8  # the row strides of a single row, whose own say nothing
 
 
 def lora_base_w4(x, w: W4Weights, y, stream=None):
     """y [m, n] = x [m, k] W^T; x and y may be column blocks of wider arrays (row strides kept)."""
-    torch = _torch()
-    dev = w.codes.device
-    _tensors(dev, ("x", x, torch.bfloat16), ("y", y, torch.bfloat16))
-    m = int(x.shape[0])
-    if tuple(x.shape) != (m, w.k) or tuple(y.shape) != (m, w.n):
-        _refuse(f"x {tuple(x.shape)} and y {tuple(y.shape)} for weights of {w.n} x {w.k}")
-    with _On(dev, stream) as s:
-        _check(lib().lora_base_w4(LORA_BF16, m, ctypes.byref(w.desc), x.data_ptr(),
-                                  x.stride(0) if m > 1 else w.k + (-w.k) % 8, y.data_ptr(),
-                                  y.stride(0) if m > 1 else w.n + (-w.n) % 8, s))
+    index, bf16 = w.index, w.bf16
+    m = x.shape[0]
+    xs, ys = x.stride(), y.stride()
+    if not (x.dtype is bf16 and y.dtype is bf16 and x.get_device() == index and y.get_device() == index and
+            x.shape == (m, w.k) and y.shape == (m, w.n) and xs[1] == 1 and ys[1] == 1):
+        _tensors(w.codes.device, ("x", x, bf16), ("y", y, bf16))
+        if tuple(x.shape) != (m, w.k) or tuple(y.shape) != (m, w.n):
+            _refuse(f"x {tuple(x.shape)} and y {tuple(y.shape)} for weights of {w.n} x {w.k}")
+    if index < 0:
+        _gpu(w.codes.device)
+    _launch("lora_base_w4", index, stream, LORA_BF16, m, w.ref, x.data_ptr(), xs[0] if m > 1 else w.one_x,
+            y.data_ptr(), ys[0] if m > 1 else w.one_y)
 
 
 class KvView:
@@ -814,72 +839,82 @@ class KvView:
         ps, hs, ts = (st if n > 1 else 0 for n, st in zip(k.shape[:3], k.stride()))
         self.desc = lora_kv_view(LORA_BF16, dim, heads, tokens, pages, int(page_table.shape[0]), int(page_table.shape[1]),
                                  0, _dptr(k), _dptr(v), ps, hs, ts, _dptr(page_table))
-
-    @property
-    def device(self):
-        return self.k.device
+        self.ref, self.index, self.device = ctypes.byref(self.desc), k.get_device(), k.device
+        self.bf16, self.int32, self.fp32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def lora_pages_copy(storage, src, dst, stream=None):
     """Copies page src[i] to page dst[i]; storage [num_pages, ...] contiguous, src and dst int32 on its device."""
-    torch = _torch()
-    _tensors(storage.device, ("src", src, torch.int32), ("dst", dst, torch.int32))
-    for name, t in (("storage", storage), ("src", src), ("dst", dst)):
-        _flat(name, t)
-    if src.numel() != dst.numel():
+    index, n = storage.get_device(), src.numel()
+    i32 = _torch().int32
+    if not (index >= 0 and src.dtype is i32 and dst.dtype is i32 and src.get_device() == index and
+            dst.get_device() == index and dst.numel() == n and storage.is_contiguous() and src.is_contiguous() and
+            dst.is_contiguous()):
+        _gpu(storage.device)
+        _tensors(storage.device, ("src", src, i32), ("dst", dst, i32))
+        for name, t in (("storage", storage), ("src", src), ("dst", dst)):
+            _flat(name, t)
         _refuse(f"{src.numel()} source and {dst.numel()} destination pages")
-    pages = int(storage.shape[0])
-    page_bytes = storage.numel() // max(pages, 1) * storage.element_size()
-    with _On(storage.device, stream) as s:
-        _check(lib().lora_pages_copy(storage.data_ptr(), page_bytes, pages, src.data_ptr(), dst.data_ptr(),
-                                     src.numel(), s))
+    pages = storage.shape[0]
+    _launch("lora_pages_copy", index, stream, storage.data_ptr(), storage.nbytes // max(pages, 1), pages, src.data_ptr(),
+            dst.data_ptr(), n)
 
 
 def lora_page_table_remap(remap, table_in, table_out, stream=None):
     """table_out = remap[table_in], entries outside [0, len(remap)) kept; int32 on one device."""
-    torch = _torch()
-    _tensors(remap.device, ("remap", remap, torch.int32), ("table_in", table_in, torch.int32),
-             ("table_out", table_out, torch.int32))
-    for name, t in (("remap", remap), ("table_in", table_in), ("table_out", table_out)):
-        _flat(name, t)
-    if table_in.numel() != table_out.numel():
-        _refuse(f"tables of {table_in.numel()} and {table_out.numel()} entries")
-    with _On(remap.device, stream) as s:
-        _check(lib().lora_page_table_remap(remap.data_ptr(), remap.numel(), table_in.data_ptr(), table_out.data_ptr(),
-                                           table_in.numel(), s))
-
-
-def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None):
-    """Writes k_new, v_new [T, kv_heads, head_dim] at positions token_pos [T] of sequences token_seq [T]."""
-    torch = _torch()
-    _tensors(view.device, ("k_new", k_new, torch.bfloat16), ("v_new", v_new, torch.bfloat16),
-             ("token_seq", token_seq, torch.int32), ("token_pos", token_pos, torch.int32))
-    d = view.desc
-    n = int(k_new.shape[0])
-    want = (n, d.kv_heads, d.head_dim)
-    if tuple(k_new.shape) != want or tuple(v_new.shape) != want or token_seq.numel() != n or token_pos.numel() != n:
-        _refuse(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}, {token_seq.numel()} sequences and "
-                f"{token_pos.numel()} positions: {want} wanted")
-    ts, hs = _row_strides(k_new)
-    if _row_strides(v_new) != (ts, hs):
-        _refuse(f"k_new and v_new have strides {k_new.stride()} and {v_new.stride()}")
-    _flat("token_seq", token_seq)
-    _flat("token_pos", token_pos)
-    with _On(view.device, stream) as s:
-        _check(lib().lora_kv_append(ctypes.byref(d), k_new.data_ptr(), v_new.data_ptr(), ts, hs, token_seq.data_ptr(),
-                                    token_pos.data_ptr(), n, s))
+    index, n = remap.get_device(), table_in.numel()
+    i32 = _torch().int32
+    if not (index >= 0 and remap.dtype is i32 and table_in.dtype is i32 and table_out.dtype is i32 and
+            table_in.get_device() == index and table_out.get_device() == index and table_out.numel() == n and
+            remap.is_contiguous() and table_in.is_contiguous() and table_out.is_contiguous()):
+        _tensors(remap.device, ("remap", remap, i32), ("table_in", table_in, i32), ("table_out", table_out, i32))
+        for name, t in (("remap", remap), ("table_in", table_in), ("table_out", table_out)):
+            _flat(name, t)
+        if table_in.numel() != table_out.numel():
+            _refuse(f"tables of {table_in.numel()} and {table_out.numel()} entries")
+        _gpu(remap.device)
+    _launch("lora_page_table_remap", index, stream, remap.data_ptr(), remap.numel(), table_in.data_ptr(),
+            table_out.data_ptr(), n)
 
 
 def _row_strides(t):
     """Token and head strides of [T, heads, dim] (0 for a dimension of one: its stride says nothing)."""
-    return tuple(st if n > 1 and t.numel() else 0 for n, st in zip(t.shape[:2], t.stride()))
+    a, b, _ = t.stride()
+    n, h, _ = t.shape
+    return (a if n > 1 else 0, b if h > 1 else 0) if n else (0, 0)
+
+
+def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None):
+    """Writes k_new, v_new [T, kv_heads, head_dim] at positions token_pos [T] of sequences token_seq [T]."""
+    d, index, bf16, i32 = view.desc, view.index, view.bf16, view.int32
+    n = k_new.shape[0]
+    shape = (n, d.kv_heads, d.head_dim)
+    if not (k_new.dtype is bf16 and v_new.dtype is bf16 and token_seq.dtype is i32 and token_pos.dtype is i32 and
+            k_new.get_device() == index and v_new.get_device() == index and token_seq.get_device() == index and
+            token_pos.get_device() == index and k_new.shape == shape and v_new.shape == shape and
+            token_seq.numel() == n and token_pos.numel() == n and token_seq.is_contiguous() and
+            token_pos.is_contiguous() and (n == 0 or (k_new.stride(2) == 1 and v_new.stride(2) == 1))):
+        _tensors(view.device, ("k_new", k_new, bf16), ("v_new", v_new, bf16), ("token_seq", token_seq, i32),
+                 ("token_pos", token_pos, i32))
+        if tuple(k_new.shape) != shape or tuple(v_new.shape) != shape or token_seq.numel() != n or token_pos.numel() != n:
+            _refuse(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}, {token_seq.numel()} sequences and "
+                    f"{token_pos.numel()} positions: {shape} wanted")
+        _flat("token_seq", token_seq)
+        _flat("token_pos", token_pos)
+    if index < 0:
+        _gpu(view.device)
+    ts, hs = _row_strides(k_new)
+    if _row_strides(v_new) != (ts, hs):
+        _refuse(f"k_new and v_new have strides {k_new.stride()} and {v_new.stride()}")
+    _launch("lora_kv_append", index, stream, view.ref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, token_seq.data_ptr(),
+            token_pos.data_ptr(), n)
 
 
 class AttnPlan:
     """A batch's attention plan: the host items, and after ``to(device)`` the device copy and workspace."""
 
     def __init__(self, desc: lora_attn_plan, items: np.ndarray):
-        self.desc, self.host_items = desc, items
+        self.desc, self.host_items, self.ref = desc, items, ctypes.byref(desc)
         self.items = self.workspace = None
 
     def to(self, device) -> "AttnPlan":
@@ -913,30 +948,38 @@ def lora_kv_attn(view: KvView, plan: AttnPlan, q, out, lse=None, scale: Optional
                  stream=None):
     """out [T, q_heads, head_dim] (and lse [T, q_heads] fp32) of q over the cache; scale defaults to
     head_dim ** -0.5, workspace to the plan's own."""
-    torch = _torch()
-    if plan.items is None:
+    items = plan.items
+    if items is None:
         _refuse("the plan has not been uploaded: call plan.to(device)")
-    p = plan.desc
+    p, index, bf16, fp32 = plan.desc, view.index, view.bf16, view.fp32
     ws = plan.workspace if workspace is None else workspace
-    _tensors(view.device, ("q", q, torch.bfloat16), ("out", out, torch.bfloat16), ("lse", lse, torch.float32),
-             ("the plan's items", plan.items, torch.int32))
-    want = (p.q_heads, p.head_dim)
-    if q.dim() != 3 or q.shape != out.shape or tuple(q.shape[1:]) != want or q.shape[0] < p.num_tokens:
-        _refuse(f"q {tuple(q.shape)} and out {tuple(out.shape)}: [{p.num_tokens} or more, {want[0]}, {want[1]}] wanted")
+    heads, dim, tokens = p.q_heads, p.head_dim, p.num_tokens
+    t = q.shape[0]
+    if not (q.dtype is bf16 and out.dtype is bf16 and q.get_device() == index and out.get_device() == index and
+            items.get_device() == index and t >= tokens and q.shape == (t, heads, dim) and out.shape == q.shape and
+            (t == 0 or (q.stride(2) == 1 and out.stride(2) == 1))):
+        _tensors(view.device, ("q", q, bf16), ("out", out, bf16), ("the plan's items", items, view.int32))
+        if q.dim() != 3 or q.shape != out.shape or tuple(q.shape[1:]) != (heads, dim) or t < tokens:
+            _refuse(f"q {tuple(q.shape)} and out {tuple(out.shape)}: [{tokens} or more, {heads}, {dim}] wanted")
+    lse_ptr = None
     if lse is not None:
-        _flat("lse", lse)
-        if lse.dim() != 2 or lse.shape[0] < p.num_tokens or lse.shape[1] != p.q_heads:
-            _refuse(f"lse {tuple(lse.shape)}: [{p.num_tokens} or more, {p.q_heads}] wanted")
+        if not (lse.dtype is fp32 and lse.get_device() == index and lse.is_contiguous() and lse.dim() == 2 and
+                lse.shape[0] >= tokens and lse.shape[1] == heads):
+            _tensors(view.device, ("lse", lse, fp32))
+            _flat("lse", lse)
+            _refuse(f"lse {tuple(lse.shape)}: [{tokens} or more, {heads}] wanted")
+        lse_ptr = lse.data_ptr()
+    wp, wb = None, 0
     if ws is not None:
-        _flat("workspace", ws)
-        if ws.device != view.device:
+        if not ws.is_contiguous() or ws.get_device() != index:
+            _flat("workspace", ws)
             _refuse(f"workspace is on {ws.device}, not {view.device}")
-    wp, wb = _ws_args(ws)
+        wp, wb = ws.data_ptr(), ws.nbytes
+    if index < 0:
+        _gpu(view.device)
     qs, os_ = _row_strides(q), _row_strides(out)
-    with _On(view.device, stream) as s:
-        _check(lib().lora_kv_attn(ctypes.byref(view.desc), ctypes.byref(p), plan.items.data_ptr(), q.data_ptr(), *qs,
-                                  out.data_ptr(), *os_, _dptr(lse), p.head_dim ** -0.5 if scale is None else scale,
-                                  wp, wb, s))
+    _launch("lora_kv_attn", index, stream, view.ref, plan.ref, items.data_ptr(), q.data_ptr(), *qs, out.data_ptr(), *os_,
+            lse_ptr, dim ** -0.5 if scale is None else scale, wp, wb)
 
 
 def _kv_destroy(box: list):
