@@ -24,6 +24,7 @@ namespace {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
@@ -124,7 +125,8 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
     kt = min(kt, col_tiles - 1);
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
-      col.c[a] = *reinterpret_cast<const uint4 *>(cp[a] + (int64_t)kt * kTileBytes + (uint32_t)lane * 16);
+      const u32x4_t *c = reinterpret_cast<const u32x4_t *>(cp[a] + (int64_t)kt * kTileBytes + (uint32_t)lane * 16);
+      col.c[a] = __builtin_bit_cast(uint4, MT < 4 ? __builtin_nontemporal_load(c) : *c);  // read once, for one token tile
 #pragma unroll
       for (int g = 0; g < GT; ++g) {
         const int64_t at = (int64_t)min(kt * GT + g, groups - 1) * n;
