@@ -431,13 +431,17 @@ __device__ __forceinline__ void pipelined(R read, M multiply) {
   }
 }
 
-template <int DP, bool FULL>
-__global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_kernel(Args a) {
+// GR: groups of four waves with the same rows that take tiles in turn, each group with stages of its own, and are
+// joined at the end: for grids that leave compute units with one workgroup, half as many tiles one
+// after the other.
+template <int DP, bool FULL, int GR>
+__global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_tile_kernel(Args a) {
   using L = TileLayout<DP>;
   constexpr int KS = DP / 16, DB = DP / 32, SB = kTilePos / 32;
-  __shared__ __attribute__((aligned(16))) uint16_t sk0[kTilePos * DP], sk1[kTilePos * DP];
-  __shared__ __attribute__((aligned(16))) uint16_t sv0[kTilePos * DP], sv1[kTilePos * DP];
-  __shared__ uint32_t any_odd[kTileWaves];
+  constexpr int kStage = kTilePos * DP;
+  __shared__ __attribute__((aligned(16))) uint16_t sk0[GR * kStage], sk1[GR * kStage];
+  __shared__ __attribute__((aligned(16))) uint16_t sv0[GR * kStage], sv1[GR * kStage];
+  __shared__ uint32_t any_odd[kTileWaves * GR], masked[2][GR];
   const lora_kv_view &kv = a.kv;
   const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
   const lora_attn_item it = a.items[ii];
@@ -445,10 +449,10 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wid / kTileWaves, wave = wid % kTileWaves;
   const int fr = lane & 31, hf = lane >> 5;
   const int D = FULL ? DP : kv.head_dim, nch = D >> 3;
-  const bool active = wave * 32 < it.rows;
 
   // loads: lane l looks up the tile's position l; chunk c of a tile is row c / kCpr, LDS slot c % kCpr, and lane l
   // of the wave's load i takes c = 64 (4 i + wave) + l
@@ -468,11 +472,12 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     KV_CHECK(ok || !inside(p), LORA_DEBUG_BAD_PAGE);
     const int64_t at = (uint64_t)(uint32_t)page * a.page16 + (uint64_t)(uint32_t)(p - a.page_div(p) * kv.page_tokens) * a.token16;
     const uint64_t there = __ballot(ok);  // bit i: the tile's position i exists
-    load_tile<L, L::kLoads, kTileWaves, 64, FULL>(kh, vh, ok ? at : -1, there, 64 * wave, nch, lds_offset(BUF ? sk1 : sk0),
-                                                  lds_offset(BUF ? sv1 : sv0));
+    load_tile<L, L::kLoads, kTileWaves, 64, FULL>(kh, vh, ok ? at : -1, there, 64 * wave, nch,
+                                                  lds_offset(BUF ? sk1 : sk0) + group * kStage * 2,
+                                                  lds_offset(BUF ? sv1 : sv0) + group * kStage * 2);
     return there;
   };
-  int page = tiles > 0 ? lookup(0) : -1;
+  int page = tiles > 0 ? lookup(group) : -1;
 
   // this lane's row (a row past the item's computes the item's first one and is not stored)
   const int my = wave * 32 + fr;
@@ -501,16 +506,19 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
 
   auto step = [&](auto bufc, int tile) {
     constexpr int BUF = decltype(bufc)::value;
-    const uint16_t *kb = BUF ? sk1 : sk0;
-    uint16_t *vb = BUF ? sv1 : sv0;
+    const uint16_t *kb = (BUF ? sk1 : sk0) + group * kStage;
+    uint16_t *vb = (BUF ? sv1 : sv0) + group * kStage;
+    const bool mine = GR == 1 || tile < tiles, active = mine && wave * 32 < it.rows;
     const int t0 = first + tile * kTilePos;
+    bool whole = !mine || (exist[BUF] == ~0ull && hi_all >= t0 + (kTilePos - 1) && lo_all <= t0);
+    if (GR > 1 && wave == 0 && lane == 0) masked[BUF][group] = !whole;
     wait_vm<0>();     // this wave's loads of the tile have landed
     __syncthreads();  // everybody's have, and nobody reads the other stage any more
-    if (tile + 1 < tiles) {
-      exist[1 - BUF] = issue(std::integral_constant<int, 1 - BUF>{}, tile + 1, page);
-      page = lookup(tile + 2);
+    if constexpr (GR > 1) whole = (masked[BUF][0] | masked[BUF][GR - 1]) == 0;  // the groups mask together: there are barriers
+    if (tile + GR < tiles) {
+      exist[1 - BUF] = issue(std::integral_constant<int, 1 - BUF>{}, tile + GR, page);
+      page = lookup(tile + 2 * GR);
     }
-    const bool whole = exist[BUF] == ~0ull && hi_all >= t0 + (kTilePos - 1) && lo_all <= t0;
     // element i of block b is position t0 + 32 b + 8 (i / 4) + 4 hf + i % 4
     f32x16_t s[SB];
     uint32_t keep = ~0u;
@@ -562,17 +570,17 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
       // 0 * inf is NaN: values of V that are not finite are added where they are kept, one position at a
       // time, and are zeros in the product
       bool odd = false;
-      for (int c = threadIdx.x; c < kTilePos * L::kCpr; c += 64 * kTileWaves) {
+      for (int c = 64 * wave + lane; mine && c < kTilePos * L::kCpr; c += 64 * kTileWaves) {
         const uint4 u = *reinterpret_cast<const uint4 *>(vb + c * 8);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) odd |= not_finite((uint16_t)w[e]) || not_finite((uint16_t)(w[e] >> 16));
       }
-      if (lane == 0) any_odd[wave] = 0;
-      if (odd) any_odd[wave] = 1;
+      odd = __ballot(odd) != 0;
+      if (lane == 0) any_odd[wid] = odd;
       __syncthreads();
       odd = false;
-      for (int w = 0; w < kTileWaves; ++w) odd |= any_odd[w] != 0;
+      for (int w = 0; w < kTileWaves * GR; ++w) odd |= any_odd[w] != 0;
       if (odd) {
         if (active) {
           for (int r = 0; r < kTilePos; ++r) {
@@ -595,7 +603,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
           }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < kTilePos * DP; i += 64 * kTileWaves)
+        for (int i = 64 * wave + lane; i < kTilePos * DP; i += 64 * kTileWaves)
           if (not_finite(vb[i])) vb[i] = 0;
         __syncthreads();
       }
@@ -645,16 +653,48 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void attn_tile_
     }
   };
 
-  if (tiles > 0) {
-    exist[0] = issue(std::integral_constant<int, 0>{}, 0, page);
-    page = lookup(1);
+  if (group < tiles) {
+    exist[0] = issue(std::integral_constant<int, 0>{}, group, page);
+    page = lookup(group + GR);
   }
-  for (int t = 0; t < tiles; t += 2) {
-    step(std::integral_constant<int, 0>{}, t);
-    if (t + 1 < tiles) step(std::integral_constant<int, 1>{}, t + 1);
+  for (int t = 0; t < tiles; t += 2 * GR) {
+    step(std::integral_constant<int, 0>{}, t + group);
+    if (t + GR < tiles) step(std::integral_constant<int, 1>{}, t + GR + group);
   }
   auto ls = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
   l = __uint_as_float(ls[0]) + __uint_as_float(ls[1]);
+  if constexpr (GR > 1) {
+    // the second group's results through LDS, lane by lane: the stages hold them
+    static_assert(GR == 2 && 4 * GR * kStage * 2 >= kTileWaves * 64 * (16 * DB + 2) * 4);
+    constexpr int kHalf = 16 * DB / 2 * 64 * kTileWaves;  // floats of half the rows' results: one of the four arrays
+    static_assert(kHalf * 4 <= GR * kStage * 2 && 2 * 64 * kTileWaves * 4 <= GR * kStage * 2);
+    float *part[2] = {reinterpret_cast<float *>(sk0), reinterpret_cast<float *>(sk1)};
+    float *ml = reinterpret_cast<float *>(sv0);
+    const int at = 64 * wave + lane;
+    __syncthreads();
+    if (group == 1) {
+#pragma unroll
+      for (int t = 0; t < DB; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(t * 16 + i) / (8 * DB)][(t * 16 + i) % (8 * DB) * 64 * kTileWaves + at] = o[t][i];
+      ml[at] = m;
+      ml[64 * kTileWaves + at] = l;
+    }
+    __syncthreads();
+    if (group == 1) return;
+    const float m1 = ml[at], l1 = ml[64 * kTileWaves + at], mn = fmaxf(m, m1);
+    const float f0 = l == 0.f ? 0.f : __builtin_amdgcn_exp2f((m - mn) * a.scale2);  // nothing kept: no weight
+    const float f1 = l1 == 0.f ? 0.f : __builtin_amdgcn_exp2f((m1 - mn) * a.scale2);
+#pragma unroll
+    for (int t = 0; t < DB; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float o1 = part[(t * 16 + i) / (8 * DB)][(t * 16 + i) % (8 * DB) * 64 * kTileWaves + at];
+        o[t][i] = (l == 0.f ? 0.f : o[t][i] * f0) + (l1 == 0.f ? 0.f : o1 * f1);
+      }
+    l = l * f0 + l1 * f1;
+    m = mn;
+  }
   if (my >= it.rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const float lse2 = l == 0.f ? -INFINITY : m * a.scale2 + log2f(l);
@@ -742,8 +782,11 @@ void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
 
 template <int DP>
 void launch_tiles(const Args &a, unsigned grid, hipStream_t stream) {
-  const auto kernel = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>> : attn_tile_kernel<DP, false>;
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * kTileWaves), 0, stream, a);
+  constexpr int G2 = DP <= 128 ? 2 : 1;  // what the LDS holds
+  const auto one = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>, 1> : attn_tile_kernel<DP, false, 1>;
+  const auto two = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>, G2> : attn_tile_kernel<DP, false, G2>;
+  if (grid <= kComputeUnits) hipLaunchKernelGGL(two, dim3(grid), dim3(64 * kTileWaves * G2), 0, stream, a);
+  else hipLaunchKernelGGL(one, dim3(grid), dim3(64 * kTileWaves), 0, stream, a);
 }
 
 }  // namespace
