@@ -116,6 +116,10 @@ def parse():
     ap.add_argument("--decode-sweep", action="store_true",
                     help="the fused decode launch on decode batches of 32 .. 256 tokens (one workgroup per "
                          "token): how one workgroup's pass times against the number of workgroups")
+    ap.add_argument("--serving", type=int, default=0, metavar="CONTEXT",
+                    help="a decode step of the 70B-shape layer's attention block for 64 sequences of about CONTEXT "
+                         "cached positions: 4-bit base projections with 64 rank-16 adapters' deltas, append and "
+                         "attention over KV pages in the adapters' pool")
     ap.add_argument("--floor", action="store_true",
                     help="only time bare streaming reads and a read-modify-write of given sizes "
                          "and workgroup counts (the device's floors for launches of that size)")
@@ -867,6 +871,54 @@ def run_floor(args, torch):
     print(json.dumps({"floor": table, "steps": K, "peak_gbs": HBM_PEAK_GBS}), flush=True)
 
 
+def bench_serving(args, torch):
+    """One decode step of the attention block (8192 wide, 64 query heads, 8 KV heads of 128, 64 rank-16
+    adapters): q, k, v and o from 4-bit weights plus deltas, append, attention over 64 sequences of --serving
+    positions, as one graph; and the same launches in parts, each part a graph of its own."""
+    from segmented_gather_gemm_segments_amd import binding as B
+    from segmented_gather_gemm_segments_amd import runner as R
+    d, heads, kv_heads, dim, n_ad, rank, seqs, ctx = 8192, 64, 8, 128, 64, 16, 64, args.serving
+    pages = -(-(ctx + 1) // 64)
+    block = R.ServingBlock(d, heads, kv_heads, dim, n_ad, rank, seqs, pages, seqs * pages + 4 * n_ad + 8, seed=1)
+    block.pool.storage[:] = torch.randn(block.pool.storage.shape[1:], device="cuda").bfloat16() * 0.1
+    block.kv.extend(list(range(seqs)), [ctx] * seqs)
+    block.kv.extend(list(range(seqs)), [1] * seqs)
+    stream = torch.cuda.Stream()
+    ids = torch.arange(seqs, dtype=torch.int32, device="cuda") % n_ad
+    seq = torch.arange(seqs, dtype=torch.int32, device="cuda")
+    pos = torch.full((seqs,), ctx, dtype=torch.int32, device="cuda")
+    plan = B.lora_kv_attn_plan(list(range(seqs + 1)), list(range(seqs)), [ctx + 1] * seqs, heads, kv_heads, dim).to("cuda")
+    hidden = torch.randn((seqs, d), device="cuda").bfloat16()
+    q, o, y = (torch.zeros((seqs, d), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    k, v = (torch.zeros((seqs, kv_heads * dim), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def base():
+        for name, src, dst in (("q", hidden, q), ("k", hidden, k), ("v", hidden, v), ("o", o, y)):
+            B.lora_base_w4(src, block.base[name], dst)
+
+    def delta():
+        for name, src, dst in (("q", hidden, q), ("k", hidden, k), ("v", hidden, v), ("o", o, y)):
+            B.lora_bgmv_fused(block.delta[name], ids, src, dst)
+
+    def attend():
+        B.lora_kv_append(block.kv.view, k.view(seqs, kv_heads, dim), v.view(seqs, kv_heads, dim), seq, pos)
+        B.lora_kv_attn(block.kv.view, plan, q.view(seqs, heads, dim), o.view(seqs, heads, dim))
+
+    def on_stream(f):
+        def run():
+            with torch.cuda.stream(stream):
+                f()
+        return run
+    torch.cuda.synchronize()
+    parts = {n: graph_span(torch, stream, [on_stream(f)] * args.steps, 3)
+             for n, f in (("base_w4", base), ("delta", delta), ("append_attention", attend))}
+    step = graph_span(torch, stream, [on_stream(lambda: block.run(hidden, plan, seq, pos, ids))] * args.steps, 3)
+    print(json.dumps({"serving": {"sequences": seqs, "context": ctx, "d_model": d, "q_heads": heads, "kv_heads": kv_heads,
+                                  "head_dim": dim, "adapters": n_ad, "rank": rank, "steps": args.steps,
+                                  "us_per_step": round(step * 1e6, 2), "tokens_per_s_per_layer": round(seqs / step, 1),
+                                  "us_parts": {n: round(t * 1e6, 2) for n, t in parts.items()}}}), flush=True)
+
+
 def main():
     args = parse()
     if args.gpus != 1:
@@ -900,6 +952,8 @@ def main():
         return bench_churn(args, torch)
     if args.multi:
         return bench_multi(args, torch)
+    if args.serving > 0:
+        return bench_serving(args, torch)
     if args.config == 5:
         out = run_layer(args, torch)
     elif args.config:

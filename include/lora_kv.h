@@ -222,6 +222,11 @@ lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view);
  * must still exist) and frees the object. */
 void lora_kv_destroy(lora_kv *kv);
 
+/* ------------------------------------------------------------------------ */
+/* lora_debug_flags of lora_sgmv.h for the kernels declared here, which keep words of their
+ * own: LORA_DEBUG_BAD_PAGE, _BAD_TOKEN and _BAD_ITEM as named above. */
+lora_status lora_kv_debug_flags(uint32_t *flags, int32_t clear);
+
 #ifdef __cplusplus
 }
 #endif

@@ -151,6 +151,7 @@ EXPORTS = {
     "lora_kv_get_stats": ([_P, _P], _I32),
     "lora_kv_get_view": ([_P, _P], _I32),
     "lora_kv_destroy": ([_P], None),
+    "lora_kv_debug_flags": ([_P, _I32], _I32),
 }
 LORA_DEBUG_BAD_PAGE, LORA_DEBUG_BAD_ADAPTER, LORA_DEBUG_BAD_RANK = 1, 2, 4
 LORA_DEBUG_BAD_TOKEN, LORA_DEBUG_BAD_ITEM = 8, 16
@@ -196,6 +197,13 @@ def lora_debug_flags(clear: bool = False) -> int:
     """The debug build's error word (LORA_DEBUG_* bits); waits for the device."""
     out = ctypes.c_uint32(0)
     _check(lib().lora_debug_flags(ctypes.byref(out), int(clear)))
+    return int(out.value)
+
+
+def lora_kv_debug_flags(clear: bool = False) -> int:
+    """The debug build's error word of the paged KV cache's kernels; waits for the device."""
+    out = ctypes.c_uint32(0)
+    _check(lib().lora_kv_debug_flags(ctypes.byref(out), int(clear)))
     return int(out.value)
 
 

@@ -30,7 +30,6 @@
 #include <cstdint>
 #include <utility>
 
-#include "kv_internal.h"
 #include "lora_internal.h"
 
 using namespace lora;
@@ -2611,10 +2610,7 @@ extern "C" lora_status lora_debug_flags(uint32_t *flags, int32_t clear) {
     e = hipMemcpyToSymbol(HIP_SYMBOL(g_debug_flags), &zero, sizeof(uint32_t), 0, hipMemcpyHostToDevice);
     if (e != hipSuccess) return hip_fail(e, "clearing the debug word");
   }
-  // the paged KV cache's kernels keep words of their own
-  lora_status st = kv_pages_debug(flags, clear);
-  if (st == LORA_OK) st = kv_attn_debug(flags, clear);
-  return st == LORA_OK ? ok() : st;
+  return ok();
 #else
   (void)clear;
   return fail(LORA_EUNSUPPORTED, "library built without LORA_DEBUG (load liblora_sgmv_debug.so)");

@@ -27,8 +27,7 @@ bool kv_mark_done(const std::shared_ptr<void> &mark, bool wait);
 lora_status kv_not_capturing(hipStream_t stream);
 void kv_device_wait();
 
-// The debug words of kv_pages.hip and kv_attn.hip (bits 0 in release builds).
-lora_status kv_pages_debug(uint32_t *flags, int32_t clear);
+// The debug word of kv_attn.hip (lora_kv_debug_flags adds that of kv_pages.hip; 0 in release builds).
 lora_status kv_attn_debug(uint32_t *flags, int32_t clear);
 
 }  // namespace lora

@@ -185,7 +185,17 @@ lora_status lora::kv_not_capturing(hipStream_t stream) {
 
 void lora::kv_device_wait() { (void)hipDeviceSynchronize(); }
 
-lora_status lora::kv_pages_debug(uint32_t *flags, int32_t clear) { return kv_debug_word(flags, clear); }
+extern "C" lora_status lora_kv_debug_flags(uint32_t *flags, int32_t clear) {
+  if (!flags) return fail(LORA_EINVAL, "null flags");
+  *flags = 0;
+#if LORA_DEBUG
+  lora_status st = kv_debug_word(flags, clear);
+  if (st == LORA_OK) st = kv_attn_debug(flags, clear);
+  return st == LORA_OK ? ok() : st;
+#else
+  return fail(LORA_EUNSUPPORTED, "library built without LORA_DEBUG (load liblora_sgmv_debug.so)");
+#endif
+}
 
 // --------------------------------------------------------------- entry points
 

@@ -309,3 +309,88 @@ class DeviceProblem:
             pairs.append(B.prepare_sgmv(self.weights, perm_d, spd, epd, self.x, v, y, stream=stream))
         self._serial_keep = keep
         return pairs
+
+
+class ServingBlock:
+    """The attention block of a decoder layer as a multi-adapter server runs it: q, k, v and o projections from 4-bit
+    base weights, each with its adapters' deltas, and attention over a KV cache whose pages come from the pool that also
+    holds the adapters' rows.  Weights and adapters are seeded; the arithmetic is the library's.
+
+    ``step(hidden, seqs, new_tokens)`` runs the new tokens of some sequences (one each for decode, a chunk for a prompt)
+    through the block and returns their output; ``fork``, ``free`` and ``compact`` act on the cache."""
+
+    def __init__(self, d_model: int, q_heads: int, kv_heads: int, head_dim: int, num_adapters: int, rank: int,
+                 max_seqs: int, max_pages: int, pool_pages: int, group: int = 128, seed: int = 0, device="cuda"):
+        torch = _torch()
+        gen = torch.Generator(device=device).manual_seed(seed)
+        self.device, self.d_model, self.head_dim = torch.device(device), d_model, head_dim
+        self.q_heads, self.kv_heads = q_heads, kv_heads
+        self.widths = {"q": (d_model, q_heads * head_dim), "k": (d_model, kv_heads * head_dim),
+                       "v": (d_model, kv_heads * head_dim), "o": (q_heads * head_dim, d_model)}
+        if q_heads * head_dim != d_model:
+            raise ValueError("the pool's rows are as long as the hidden state: q_heads * head_dim == d_model")
+        rows = 16
+        storage = torch.zeros((pool_pages, rows, d_model), dtype=torch.bfloat16, device=device)
+        self.pool = B.Pool(storage, rows, shuffle_seed=seed + 1)
+        # adapters of q and o (square) share the pool with the KV pages; those of k and v have B^T rows of another width
+        # and keep them in stacks of their own
+        self.base, self.delta, self.rows16, self.scales = {}, {}, {}, {}
+        rank_dev = torch.full((num_adapters,), rank, dtype=torch.int32, device=device)
+        ranks = np.full(num_adapters, rank, np.int32)
+        pages = -(-rank // rows)
+
+        def paged(d):
+            table = np.zeros((num_adapters, pages), np.int32)
+            for a in range(num_adapters):
+                table[a] = self.pool.alloc(rank)
+                r = (torch.randn((rank, d), generator=gen, device=device) * d ** -0.5).bfloat16()
+                self.pool.write_rows(table[a], r)
+            return torch.from_numpy(table).to(device)
+
+        for name, (k, n) in self.widths.items():
+            codes = torch.randint(0, 256, (n, k // 2), generator=gen, device=device, dtype=torch.uint8)
+            scales = ((0.5 + torch.rand((k // group, n), generator=gen, device=device)) / (4.6 * k ** 0.5)).bfloat16()
+            self.rows16[name], self.scales[name] = codes, scales
+            self.base[name] = B.W4Weights(n, k, group, B.lora_w4_pack(codes), scales)
+            if n == k == d_model:
+                a_pt, b_pt = paged(k), paged(n)
+                self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rows, storage, storage, rank_dev, ranks, a_pt, b_pt,
+                                             pages)
+            else:
+                a = (torch.randn((num_adapters, rank, k), generator=gen, device=device) * k ** -0.5).bfloat16()
+                b = (torch.randn((num_adapters, rank, n), generator=gen, device=device) * rank ** -0.5).bfloat16()
+                self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rank, a, b, rank_dev, ranks)
+        self.kv = B.KvCache(self.pool, kv_heads, head_dim, max_seqs, max_pages)
+
+    def project(self, name, x, y, token_adapter):
+        """y = W x + B (A x), the base from 4-bit codes, the delta of each token's adapter."""
+        B.lora_base_w4(x, self.base[name], y)
+        B.lora_bgmv_fused(self.delta[name], token_adapter, x, y)
+
+    def step(self, hidden, seqs, new_tokens, token_adapter):
+        """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device."""
+        torch = _torch()
+        self.kv.extend(seqs, new_tokens)
+        lens = [self.kv.length(s) for s in seqs]
+        starts = np.concatenate([[0], np.cumsum(new_tokens)]).astype(np.int32)
+        seq = np.repeat(np.asarray(seqs, np.int32), new_tokens)
+        pos = np.concatenate([np.arange(n - q, n, dtype=np.int32) for q, n in zip(new_tokens, lens)])
+        to = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(self.device)
+        plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim).to(self.device)
+        return self.run(hidden, plan, to(seq), to(pos), token_adapter)
+
+    def run(self, hidden, plan, token_seq, token_pos, token_adapter):
+        """The device work of a step, launches only (every buffer is new; the plan and indices may serve many layers)."""
+        torch = _torch()
+        t = hidden.shape[0]
+        new = lambda n: torch.empty((t, n), dtype=torch.bfloat16, device=self.device)
+        q, k, v = (new(self.widths[n][1]) for n in "qkv")
+        for name, y in (("q", q), ("k", k), ("v", v)):
+            self.project(name, hidden, y, token_adapter)
+        heads = lambda y, h: y.view(t, h, self.head_dim)
+        B.lora_kv_append(self.kv.view, heads(k, self.kv_heads), heads(v, self.kv_heads), token_seq, token_pos)
+        out = new(self.q_heads * self.head_dim)
+        B.lora_kv_attn(self.kv.view, plan, heads(q, self.q_heads), heads(out, self.q_heads))
+        y = new(self.d_model)
+        self.project("o", out, y, token_adapter)
+        return y
