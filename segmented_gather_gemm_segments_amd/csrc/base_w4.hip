@@ -24,15 +24,11 @@ namespace {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
 constexpr int kTileBytes = 1024;   // codes of 16 rows x 128 k
 constexpr int kTileK = 128;
-constexpr int kWaves = 8;
-template <int MT>
-constexpr int kRowWaves = MT == 4 ? 2 : 1;  // waves that share stages of x, so that two of each fit the LDS
 __device__ const uint4 g_zeros = {0, 0, 0, 0};  // x behind the last k
 constexpr int kComputeUnits = 256;
 
@@ -60,24 +56,36 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w) {
 }
 
 // One workgroup: R NT row tiles of W (16 rows each) and 16 MT tokens.  Its waves, in groups of R that share
-// x and have NT row tiles each, take the tile columns (128 k) in turn, each with the next column's codes,
+// x and have NT row tiles each, take the steps of KC k in turn, each with the next step's codes,
 // scales and x on their way while it works on this one; their fp32 sums are added in order through LDS.
-// x goes through two LDS stages of each group: read as operands straight from memory, every lane would name a line of its own, and the address units, which
-// take those one by one, would set the time (16 tokens, 28672 x 8192: 33.4 us).
+// x goes through two LDS stages of each group: read as operands straight from memory, every lane would
+// name a line of its own, and the address units, which take those one by one, would set the time
+// (16 tokens, 28672 x 8192: 33.4 us).
+template <int MT>
+struct Shape {
+  static constexpr int kWaves = MT == 4 ? 16 : 8;
+  static constexpr int kRow = MT == 4 ? 2 : 1;    // R: so that two stages of each group fit the LDS
+  static constexpr int kStep = MT == 4 ? 64 : 128;  // KC
+};
+
 template <int MT, int NT, int G, typename S, bool Z>
-__global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
+__global__ __launch_bounds__(64 * Shape<MT>::kWaves) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
                                                               const uint8_t *__restrict__ codes,
                                                               const S *__restrict__ scales,
                                                               const S *__restrict__ zeros,
                                                               const uint16_t *__restrict__ x, int64_t x_stride,
                                                               uint16_t *__restrict__ y, int64_t y_stride) {
-  constexpr int GT = kTileK / G;  // groups per tile column
-  constexpr int R = kRowWaves<MT>, W = kWaves / R, kStage = 16 * MT * kTileK;  // elements of x
+  constexpr int WAVES = Shape<MT>::kWaves, R = Shape<MT>::kRow, KC = Shape<MT>::kStep, W = WAVES / R;
+  constexpr int WORDS = KC / 32;                 // words of codes per lane and step
+  constexpr int GT = KC > G ? KC / G : 1;        // groups per step (a larger group is met in several)
+  constexpr int GW = WORDS / GT;                 // words per group and step
+  constexpr int kStage = 16 * MT * KC;           // elements of x
+  constexpr int CPR = KC / 8, TPL = 64 / CPR;    // chunks per token, tokens per load
   __shared__ __attribute__((aligned(16))) uint16_t sx[2 * W * kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
   const int kw = wave / R, r0 = (blockIdx.x * R + wave % R) * NT, t0 = blockIdx.y * (16 * MT);
-  const int groups = k / G;
+  const int groups = k / G, steps = (k + KC - 1) / KC;
   // Addresses are a part that all lanes share, which the scalar unit steps, and a fixed 32-bit offset per lane.
   const uint8_t *cp[NT];
   uint32_t nrow[NT];  // first of the 4 rows that this lane holds results of (clamped: results past n are not stored)
@@ -86,27 +94,28 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
     cp[a] = codes + (int64_t)min(r0 + a, row_tiles - 1) * col_tiles * kTileBytes;
     nrow[a] = min((r0 + a) * 16 + 4 * fg, n - 4);
   }
-  // x: load i of a wave takes 4 tokens of 256 bytes, lane l 16 of them; chunk c of a token is stored in slot
-  // c ^ (token & 15), so that the 16 lanes that read one chunk of 16 tokens hit every bank once
-  constexpr int LOADS = 4 * MT / R;
+  // x: a load takes TPL tokens, lane l 16 bytes of one; chunk c of a token is stored in slot(token, c), so that the 16
+  // lanes that read one chunk of 16 tokens hit every bank once
+  auto slot = [](int t, int c) { return KC == 128 ? c ^ (t & 15) : c ^ ((t >> 1) & 7); };
+  constexpr int LOADS = 16 * MT / TPL / R;
   uint32_t xo[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    const int t = 4 * (LOADS * (wave % R) + i) + (lane >> 4);
-    xo[i] = ((uint32_t)min(t, m - 1 - t0) * (uint32_t)x_stride + ((lane ^ t) & 15) * 8) * 2;
+    const int t = TPL * (LOADS * (wave % R) + i) + lane / CPR;
+    xo[i] = ((uint32_t)min(t, m - 1 - t0) * (uint32_t)x_stride + slot(t, lane % CPR) * 8) * 2;
   }
   const uint16_t *xt = x + (int64_t)t0 * x_stride;
-  uint16_t *stage = sx + kw * 2 * kStage;
-  auto load_x = [&](int kt, int buf) {
+  const uint16_t *stage = sx + kw * 2 * kStage;
+  auto load_x = [&](int st, int buf) {
     const uint32_t to = lds_offset(sx) + (uint32_t)((kw * 2 + buf) * kStage + LOADS * (wave % R) * 512) * 2;
-    if ((kt + 1) * kTileK <= k) {
+    if ((st + 1) * KC <= k) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) load_lds16(xt + kt * kTileK, xo[i], to + i * 1024);
+      for (int i = 0; i < LOADS; ++i) load_lds16(xt + st * KC, xo[i], to + i * 1024);
     } else {  // zeros behind the last k
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int t = 4 * (LOADS * (wave % R) + i) + (lane >> 4), kk = kt * kTileK + ((lane ^ t) & 15) * 8;
-        load_lds16(kk < k ? (const char *)(xt + kt * kTileK) + xo[i] : (const char *)&g_zeros, to + i * 1024);
+        const int t = TPL * (LOADS * (wave % R) + i) + lane / CPR, kk = st * KC + slot(t, lane % CPR) * 8;
+        load_lds16(kk < k ? (const char *)(xt + st * KC) + xo[i] : (const char *)&g_zeros, to + i * 1024);
       }
     }
   };
@@ -117,73 +126,74 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
 #pragma unroll
     for (int i = 0; i < MT; ++i) sum[a][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  struct Column {
-    uint4 c[NT];
+  typedef __attribute__((ext_vector_type(WORDS))) uint32_t words_t;
+  struct Step {
+    words_t c[NT];
     Four<S> s[NT][GT], z[NT][Z ? GT : 1];
   };
-  auto fetch = [&](int kt, Column &col) {
-    kt = min(kt, col_tiles - 1);
+  auto fetch = [&](int st, Step &p) {
+    st = min(st, steps - 1);
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
-      const u32x4_t *c = reinterpret_cast<const u32x4_t *>(cp[a] + (int64_t)kt * kTileBytes + (uint32_t)lane * 16);
-      col.c[a] = __builtin_bit_cast(uint4, MT < 4 ? __builtin_nontemporal_load(c) : *c);  // read once, for one token tile
+      const int64_t at = (int64_t)(st * KC / kTileK) * kTileBytes + st * KC % kTileK / 8;
+      const words_t *c = reinterpret_cast<const words_t *>(cp[a] + at + (uint32_t)lane * 16);
+      p.c[a] = MT < 4 ? __builtin_nontemporal_load(c) : *c;  // read once, for one token tile
 #pragma unroll
       for (int g = 0; g < GT; ++g) {
-        const int64_t at = (int64_t)min(kt * GT + g, groups - 1) * n;
-        col.s[a][g] = *reinterpret_cast<const Four<S> *>(scales + at + nrow[a]);
-        if constexpr (Z) col.z[a][g] = *reinterpret_cast<const Four<S> *>(zeros + at + nrow[a]);
+        const int64_t row = (int64_t)min(st * KC / G + g, groups - 1) * n;
+        p.s[a][g] = *reinterpret_cast<const Four<S> *>(scales + row + nrow[a]);
+        if constexpr (Z) p.z[a][g] = *reinterpret_cast<const Four<S> *>(zeros + row + nrow[a]);
       }
     }
   };
 
-  Column next;
+  Step next;
   fetch(kw, next);
-  if (kw < col_tiles) load_x(kw, 0);
+  if (kw < steps) load_x(kw, 0);
   int buf = 0;
-  // waves that share stages go through the loop together, the last time some without a column
-  for (int kt = kw; R > 1 ? kt - kw < col_tiles : kt < col_tiles; kt += W, buf ^= 1) {
-    wait_vm<0>();  // this column has landed
+  // waves that share stages go through the loop together, the last time some without a step
+  for (int st = kw; R > 1 ? st - kw < steps : st < steps; st += W, buf ^= 1) {
+    wait_vm<0>();  // this step's loads have landed
     wait_lds();    // and the other stage has been read
     if constexpr (R > 1) {
       __syncthreads();
-      if (kt >= col_tiles) continue;
+      if (st >= steps) continue;
     }
-    const Column col = next;
-    fetch(kt + W, next);
-    if (kt + W < col_tiles) load_x(kt + W, buf ^ 1);
-    bf16x8_t xf[MT][4];
+    const Step now = next;
+    fetch(st + W, next);
+    if (st + W < steps) load_x(st + W, buf ^ 1);
+    bf16x8_t xf[MT][WORDS];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < WORDS; ++s)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         xf[i][s] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4 *>(
-            stage + buf * kStage + (16 * i + fr) * kTileK + (((4 * s + fg) ^ fr) & 15) * 8));
+            stage + buf * kStage + (16 * i + fr) * KC + slot(fr, 4 * s + fg) * 8));
 #pragma unroll
     for (int g = 0; g < GT; ++g) {
-      if ((kt * GT + g) * G >= k) break;  // the last column of a k that is no multiple of 128
+      if (st * KC + g * G >= k) break;  // the last step of a k that is no multiple of KC
       f32x4_t xs[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         xs[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s)
+        for (int s = g * GW; s < (g + 1) * GW; ++s)
           xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf[i][s], xs[i], 0, 0, 0);
       }
 #pragma unroll
       for (int a = 0; a < NT; ++a) {
-        const uint32_t cw[4] = {col.c[a].x, col.c[a].y, col.c[a].z, col.c[a].w};
         f32x4_t t[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) t[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
-          const bf16x8_t wf = widen(cw[s]);
+        for (int s = g * GW; s < (g + 1) * GW; ++s) {
+          const bf16x8_t wf = widen(now.c[a][s]);
 #pragma unroll
           for (int i = 0; i < MT; ++i) t[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[i][s], t[i], 0, 0, 0);
         }
-        const f32x4_t sc = values(col.s[a][g]);
+        const f32x4_t sc = values(now.s[a][g]);
         f32x4_t off = f32x4_t{136.f, 136.f, 136.f, 136.f};
-        if constexpr (Z) off = values(col.z[a][g]) + 128.f;
+        if constexpr (Z) off = values(now.z[a][g]) + 128.f;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -191,7 +201,7 @@ __global__ __launch_bounds__(64 * kWaves) void base_w4_kernel(int m, int n, int 
       }
     }
   }
-  f32x4_t *red = reinterpret_cast<f32x4_t *>(sx);  // [kWaves][64]
+  f32x4_t *red = reinterpret_cast<f32x4_t *>(sx);  // [WAVES][64]
 #pragma unroll
   for (int a = 0; a < NT; ++a)
 #pragma unroll
@@ -243,8 +253,8 @@ struct W4Call {
 template <int MT, int NT, int G, typename S, bool Z>
 void launch(const W4Call &c) {
   const int row_tiles = (c.n + 15) / 16;
-  hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT * kRowWaves<MT> - 1) / (NT * kRowWaves<MT>), (c.m + 16 * MT - 1) / (16 * MT)),
-                     dim3(64 * kWaves), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
+  hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT * Shape<MT>::kRow - 1) / (NT * Shape<MT>::kRow), (c.m + 16 * MT - 1) / (16 * MT)),
+                     dim3(64 * Shape<MT>::kWaves), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
                      (const S *)c.w->scales, (const S *)c.w->zeros, c.x, c.xs, c.y, c.ys);
 }
 // Row tiles per workgroup: as many as still leave every compute unit a workgroup.  More tiles share the
@@ -254,7 +264,7 @@ template <int MT, int G, typename S, bool Z>
 void pick_tiles(const W4Call &c) {
   constexpr int kWords = kTileK / G * (int)sizeof(S) * (Z ? 2 : 1);
   constexpr int kMost = MT == 4 ? (kWords <= 8 ? 2 : 1) : 64 / MT / kWords;
-  const int row_tiles = (c.n + 15) / 16 / kRowWaves<MT>;
+  const int row_tiles = (c.n + 15) / 16 / Shape<MT>::kRow;
   if (kMost >= 4 && row_tiles >= 4 * kComputeUnits) launch<MT, kMost >= 4 ? 4 : 1, G, S, Z>(c);
   else if (kMost >= 2 && row_tiles >= 2 * kComputeUnits) launch<MT, kMost >= 2 ? 2 : 1, G, S, Z>(c);
   else launch<MT, 1, G, S, Z>(c);

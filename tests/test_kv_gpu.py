@@ -194,6 +194,51 @@ def test_masks(causal, window):
     check_masks(c, [300, 33, 65, 1], 2, causal, window)
 
 
+@pytest.mark.parametrize("dim", [40, 64, 80, 128, 256])
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_many_requests(dim, page, q_len):
+    """More requests times KV heads than the card has compute units: other variants than few of them take."""
+    kv_lens = [1 + (37 * i) % 190 for i in range(36)]
+    c = Paged(kv_lens, 8, dim, page, seed=dim + page)
+    q_lens = [min(q_len, n) for n in kv_lens]
+    check_attention(c, q_lens, 8 if q_len > 1 else 24, label="many")
+    check_attention(c, q_lens, 8, window=50, label="many, windowed")
+    check_masks(c, q_lens, 8, True, 50)
+    check_masks(c, [q_len] * 36, 8, True, 0)
+    check_masks(c, q_lens, 8, False, 0)
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_len", [3, 70])
+def test_many_requests_with_bad_places(dim, bad, q_len):
+    """As above, with a position that is not finite and a page that is absent."""
+    n, at, many = 150, 150 - q_len + 1, 34
+    c = Paged([n], 8, dim, 16, seed=dim)
+    plan, q, out, lse = check_attention(c, [q_len] * many, 8, seqs=[0] * many, label="many, clean")
+    t = q_len * many
+    first = torch.arange(0, t, q_len, device="cuda")
+    page, slot = int(c.table[0, at // 16]), at % 16
+    for which in (0, 1):
+        keep = c.store[page, which, :, slot].clone()
+        c.store[page, which, :, slot] = bad
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        B.lora_kv_attn(c.view, plan, q, o2, lse=l2)
+        assert torch.equal(o2[first], out[first]) and torch.equal(l2[first], lse[first])
+        if which == 1:
+            reached = torch.ones(t, dtype=torch.bool, device="cuda")
+            reached[first] = False
+            assert not bool(torch.isfinite(o2[:t][reached]).any())
+        c.store[page, which, :, slot] = keep
+    table = c.table.clone()
+    table[0, [0, 2]] = torch.tensor([-1, 1 << 30], dtype=torch.int32)
+    q0, o2, l2 = torch.zeros_like(q), torch.empty_like(out), torch.empty_like(lse)
+    B.lora_kv_attn(B.KvView(c.view.k, c.view.v, table.cuda()), plan, q0, o2, lse=l2)
+    want = (torch.arange(q_len) + (n - q_len + 1 - 32)).double().repeat(many)[:, None]
+    assert bool(((l2[:t].double().exp().cpu() - want).abs() <= 1e-4 * want).all()) and bool(torch.isfinite(o2[:t]).all())
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_rows_that_keep_nothing(causal):
     """Chunks longer than their sequence, and sequences without positions."""

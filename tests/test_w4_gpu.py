@@ -77,6 +77,16 @@ def test_exact_integers(m, n, k, group, zeros, dtype):
     assert torch.equal(y.cpu(), want)
 
 
+@pytest.mark.parametrize("n", [8200, 16400])
+@pytest.mark.parametrize("m", [3, 20, 50])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros,dtype", [(False, torch.bfloat16), (False, torch.float32), (True, torch.bfloat16),
+                                         (True, torch.float32)])
+def test_many_rows(n, m, group, zeros, dtype):
+    """So many rows of W that a workgroup takes several row tiles, the last of them past the end."""
+    test_exact_integers(m, n, 672, group, zeros, dtype)
+
+
 @pytest.mark.parametrize("m,n,k,group,zeros,dtype", [
     (1, 4096, 4096, 128, False, torch.bfloat16), (16, 512, 8192, 64, True, torch.float32),
     (40, 136, 14336, 32, True, torch.bfloat16), (200, 256, 1024, 128, False, torch.float32)])
