@@ -719,9 +719,15 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
 }
 
 // ----------------------------------------------------------------- join
-// One thread per 8 columns of a row: the row's parts in order, each weighted with
-// 2^(lse_part - lse).
-__global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
+// An item's parts, each weighted with 2^(lse_part - lse).  The weights first, in LDS; then a thread adds 8 columns
+// of a row over a slice of the parts, and the slices are added in order.  As many slices as the
+// threads allow: one thread going through all the parts of its columns would wait for each of them
+// in turn (64 / 8 heads of 128, one token over 8192 positions in 32 parts: 41 us in all, so 18).
+constexpr int kJoinThreads = 1024;
+
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(Args a) {
+  __shared__ float sw[LORA_ATTN_MAX_PARTS * LORA_ATTN_TILE_ROWS], slse[LORA_ATTN_TILE_ROWS];
+  __shared__ __attribute__((aligned(16))) f32x4_t sv[2][kJoinThreads];
   const lora_kv_view &kv = a.kv;
   const int h = blockIdx.x % kv.kv_heads, ii = blockIdx.x / kv.kv_heads;
   lora_attn_item it = a.items[ii];
@@ -733,29 +739,60 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
     KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);
     return;
   }
-  const int D = kv.head_dim, nch = D >> 3;
-  for (int i = threadIdx.x; i < it.rows * nch; i += 256) {
-    const int r = i / nch, c = i % nch;
-    float top = -INFINITY;
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_lse[(int64_t)(base + p * it.rows + r) * kv.kv_heads + h]);
-    float total = 0.f, v[8] = {};
-    for (int p = 0; p < parts; ++p) {
-      const int64_t pr = (int64_t)(base + p * it.rows + r) * kv.kv_heads + h;
-      const float lp = a.part_lse[pr];
-      if (lp == -INFINITY) continue;  // the range kept nothing
-      const float f = __builtin_amdgcn_exp2f(lp - top);
-      total += f;
-      const float *po = a.part_o + pr * D + 8 * c;
+  const int D = kv.head_dim, nch = D >> 3, units = it.rows * nch;
+  // a wave per row, a lane per part
+  constexpr int kWaves = kJoinThreads / 64, kTurns = LORA_ATTN_TILE_ROWS / kWaves;
+  static_assert(LORA_ATTN_MAX_PARTS <= 64 && kTurns * kWaves == LORA_ATTN_TILE_ROWS);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float lp[kTurns];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += f * po[e];
+  for (int t = 0; t < kTurns; ++t) {
+    const int r = wave + t * kWaves;
+    lp[t] = r < it.rows && lane < parts ? a.part_lse[(int64_t)(base + lane * it.rows + r) * kv.kv_heads + h] : -INFINITY;
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const int r = wave + t * kWaves;
+    if (r >= it.rows) break;
+    float top = lp[t];
+    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const float f = lp[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(lp[t] - top);  // the range kept nothing: no weight
+    float total = f;
+    for (int x = 1; x < 64; x <<= 1) total += __shfl_xor(total, x);
+    if (lane < parts) sw[lane * it.rows + r] = total == 0.f ? 0.f : f / total;
+    if (lane == 0) slse[r] = total == 0.f ? -INFINITY : top + log2f(total);
+  }
+  __syncthreads();
+  const int slices = max(1, min(parts, kJoinThreads / units)), per = (parts + slices - 1) / slices;
+  // with one slice several turns, else the threads behind the last slice have none
+  for (int i0 = 0; i0 < units; i0 += slices > 1 ? units : kJoinThreads) {
+    const int slice = slices > 1 ? (int)threadIdx.x / units : 0, i = slices > 1 ? (int)threadIdx.x % units : i0 + (int)threadIdx.x;
+    const int r = i / nch, c = i % nch;
+    f32x4_t v[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+    if (slice < slices && i < units) {
+#pragma unroll 4
+      for (int p = slice * per; p < min(parts, (slice + 1) * per); ++p) {
+        const float f = sw[p * it.rows + r];
+        const f32x4_t *po = reinterpret_cast<const f32x4_t *>(a.part_o + ((int64_t)(base + p * it.rows + r) * kv.kv_heads + h) * D + 8 * c);
+        v[0] += f * po[0];
+        v[1] += f * po[1];
+      }
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const float lse2 = total == 0.f ? -INFINITY : top + log2f(total);
+    if (slices > 1) {
+      sv[0][threadIdx.x] = v[0];
+      sv[1][threadIdx.x] = v[1];
+      __syncthreads();
+      if (slice == 0)
+        for (int w = 1; w < slices; ++w) {
+          v[0] += sv[0][w * units + i];
+          v[1] += sv[1][w * units + i];
+        }
+    }
+    if (slice > 0 || i >= units) continue;
     const int rr = it.row0 + r, tk = rr / a.group, hd = h * a.group + rr % a.group;
     *reinterpret_cast<uint4 *>(a.out + (it.q_begin + tk) * a.o_ts + hd * a.o_hs + 8 * c) =
-        make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                   pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
-    if (c == 0 && a.lse) a.lse[(int64_t)(it.q_begin + tk) * a.q_heads + hd] = lse2 * kLn2;
+        make_uint4(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]), pack_bf16(v[1][0], v[1][1]), pack_bf16(v[1][2], v[1][3]));
+    if (c == 0 && a.lse) a.lse[(int64_t)(it.q_begin + tk) * a.q_heads + hd] = slse[r] * kLn2;
   }
 }
 
@@ -763,7 +800,8 @@ constexpr unsigned kComputeUnits = 256;
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
-// Heads of 64, 128 and 256, the usual ones, have kernels without the checks that shorter rows need.
+// Heads of 64, 128 and 256, the usual ones, have kernels without the checks that shorter rows need (chunks of 64
+// over 512 positions, 12 heads of 64: 12.8 us, with the checks 13.8; 8 chunks of 128 over 4096: 171 and 178).
 template <int DP>
 constexpr bool kFull = DP == 64 || DP == 128 || DP == 256;
 template <int DP>
@@ -772,7 +810,8 @@ bool full(const Args &a) { return kFull<DP> && a.kv.head_dim == DP; }
 template <int DP>
 void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
   // two workgroups of half the waves share a compute unit's LDS and overlap their ends; a grid that gives
-  // every compute unit one at most takes all the waves at once, for a shorter chain of tiles
+  // every compute unit one at most takes all the waves at once, for a shorter chain of tiles (heads of 128, 4 tokens
+  // over 300 positions: 10.2 us, with half the waves 11.2; 8 tokens over 2048, 512 units: 32 us and 26)
   constexpr int W = DP <= 64 ? 4 : DP <= 128 ? 2 : 1;
   const auto wide = full<DP>(a) ? attn_rows_kernel<DP, 2 * W, kFull<DP>> : attn_rows_kernel<DP, 2 * W, false>;
   const auto slim = full<DP>(a) ? attn_rows_kernel<DP, W, kFull<DP>> : attn_rows_kernel<DP, W, false>;
@@ -782,6 +821,8 @@ void launch_rows(const Args &a, unsigned grid, hipStream_t stream) {
 
 template <int DP>
 void launch_tiles(const Args &a, unsigned grid, hipStream_t stream) {
+  // a grid of one workgroup per compute unit at most takes two groups of waves (4 chunks of 64 over 512 positions, 12
+  // heads of 64: 12.8 us, with one group 13.9; 40 such chunks, 480 units: 86 us and 20)
   constexpr int G2 = DP <= 128 ? 2 : 1;  // what the LDS holds
   const auto one = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>, 1> : attn_tile_kernel<DP, false, 1>;
   const auto two = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>, G2> : attn_tile_kernel<DP, false, G2>;
@@ -871,7 +912,8 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   if (plan->num_joins) {
     a.items = items + plan->num_row_items + plan->num_tile_items;
     a.num_items = plan->num_joins;
-    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(plan->num_joins * kv->kv_heads)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(plan->num_joins * kv->kv_heads)), dim3(kJoinThreads), 0,
+                       stream, a);
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? ok() : hip_fail(e, "attention launch");

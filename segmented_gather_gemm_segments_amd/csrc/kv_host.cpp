@@ -54,10 +54,14 @@ namespace {
 
 // Items of one kind aim at this many (item, KV head) units, and at no range of fewer positions than
 // kMinRange: below that a range's own start and the join cost more than the
-// parallelism gives.  [0] row items, [1] tile items.
-constexpr int64_t kAimUnits[2] = {1024, 512};
-constexpr int64_t kMinRange[2] = {256, 1024};
-constexpr int64_t kTileMinRows = 33;  // requests of at least this many rows take tile items
+// parallelism gives.  [0] row items, [1] tile items.  Measured, 64 / 8 heads of 128: twice the units, 64 tokens over 512
+// positions each 41 us instead of 29.5, a chunk of 512 over 2048 61 instead of 48; half of them, a chunk of 128 over
+// 8192 93 instead of 63.  Row items of at least 128 positions, 4 tokens over 300 each: 12.6 us instead of 10.2, of
+// at least 512, one token over 2048: 16.1 instead of 13.6.  Tile items of at least 256, a chunk of 16 over 8192: 53
+// us instead of 43, of at least 1024, a chunk of 64 over 2048: 39 instead of 33.
+constexpr int64_t kAimUnits[2] = {512, 256};
+constexpr int64_t kMinRange[2] = {256, 512};
+constexpr int64_t kComputeUnits = 256;
 constexpr int32_t kTileKv = 64;  // range borders are multiples of this
 
 struct Tile {
@@ -95,10 +99,19 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
   }
   return guarded([&]() -> lora_status {
     std::vector<Tile> tiles[2];  // row items, tile items
+    int64_t medium = 0;          // (request, KV head) units whose rows two row items hold
+    for (int32_t r = 0; r < num_reqs; ++r) {
+      const int64_t rows = (q_starts[r + 1] - q_starts[r]) * group;
+      medium += rows > LORA_ATTN_ROWS && rows <= 2 * LORA_ATTN_ROWS ? kv_heads : 0;
+    }
+    // 17 to 32 rows: one tile item reads K and V once, two row items twice (64 requests of 24 rows over 2048
+    // positions, 8 KV heads: 96 us and 184); where units are few the row items' shorter steps count more (4
+    // requests: 35 us and 24).  33 rows and more: 64 requests 100 us as tile items, 268 as row items.
+    const int64_t tile_min_rows = (medium >= kComputeUnits ? 1 : 2) * LORA_ATTN_ROWS + 1;
     for (int32_t r = 0; r < num_reqs; ++r) {
       const int32_t qn = q_starts[r + 1] - q_starts[r];
       const int64_t rows = qn * group, pos0 = (int64_t)kv_len[r] - qn;
-      const int kind = rows >= kTileMinRows;
+      const int kind = rows >= tile_min_rows;
       const int64_t step = kind ? LORA_ATTN_TILE_ROWS : LORA_ATTN_ROWS;
       for (int64_t row0 = 0; row0 < rows; row0 += step) {
         const int64_t n = std::min(step, rows - row0);
@@ -116,10 +129,18 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
     std::vector<lora_attn_item> out[2], joins;
     int64_t part_rows = 0;
     for (int kind = 0; kind < 2; ++kind) {
-      int64_t work = 0;
-      for (const Tile &t : tiles[kind]) work += t.span * kv_heads;
+      int64_t work = 0, widest = 0;
+      for (const Tile &t : tiles[kind]) {
+        work += t.span * kv_heads;
+        widest = std::max(widest, t.span);
+      }
       // positions per range: an even share of the work for each unit aimed at
-      const int64_t share = std::max(kMinRange[kind], cdiv(cdiv(work, kAimUnits[kind]), kTileKv) * kTileKv);
+      auto even = [&](int64_t units) { return cdiv(cdiv(work, units), kTileKv) * kTileKv; };
+      int64_t share = even(kAimUnits[kind]);
+      // Row items of uneven spans aim at twice the units, which the device takes longest first (64 / 8 heads of 128, 64
+      // tokens over 256 to 8192 positions: 250 us, else 275).
+      if (kind == 0 && widest > share * 3 / 2) share = even(2 * kAimUnits[0]);
+      share = std::max(kMinRange[kind], share);
       std::vector<Tile> ranges;
       for (const Tile &t : tiles[kind]) {
         int64_t parts = max_parts == 1 ? 1 : std::max<int64_t>(1, (t.span + share / 2) / share);
