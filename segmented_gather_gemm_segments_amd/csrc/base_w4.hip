@@ -60,22 +60,21 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w) {
 // scales and x on their way while it works on this one; their fp32 sums are added in order through LDS.
 // x goes through two LDS stages of each group: read as operands straight from memory, every lane would
 // name a line of its own, and the address units, which take those one by one, would set the time
-// (16 tokens, 28672 x 8192: 33.4 us).
+// (16 tokens, 28672 x 8192: 33.4 us, with the stages 29.9; 64 tokens, 8192 x 8192: 38.2 and 28.6).
 template <int MT>
-struct Shape {
+struct Shape {  // 64 tokens: 8 waves and steps of 128 k take 26.7 us there, these 24.2
   static constexpr int kWaves = MT == 4 ? 16 : 8;
-  static constexpr int kRow = MT == 4 ? 2 : 1;    // R: so that two stages of each group fit the LDS
   static constexpr int kStep = MT == 4 ? 64 : 128;  // KC
 };
 
-template <int MT, int NT, int G, typename S, bool Z>
+template <int MT, int R, int NT, int G, typename S, bool Z>
 __global__ __launch_bounds__(64 * Shape<MT>::kWaves) void base_w4_kernel(int m, int n, int k, int row_tiles, int col_tiles,
                                                               const uint8_t *__restrict__ codes,
                                                               const S *__restrict__ scales,
                                                               const S *__restrict__ zeros,
                                                               const uint16_t *__restrict__ x, int64_t x_stride,
                                                               uint16_t *__restrict__ y, int64_t y_stride) {
-  constexpr int WAVES = Shape<MT>::kWaves, R = Shape<MT>::kRow, KC = Shape<MT>::kStep, W = WAVES / R;
+  constexpr int WAVES = Shape<MT>::kWaves, KC = Shape<MT>::kStep, W = WAVES / R;
   constexpr int WORDS = KC / 32;                 // words of codes per lane and step
   constexpr int GT = KC > G ? KC / G : 1;        // groups per step (a larger group is met in several)
   constexpr int GW = WORDS / GT;                 // words per group and step
@@ -137,7 +136,10 @@ __global__ __launch_bounds__(64 * Shape<MT>::kWaves) void base_w4_kernel(int m, 
     for (int a = 0; a < NT; ++a) {
       const int64_t at = (int64_t)(st * KC / kTileK) * kTileBytes + st * KC % kTileK / 8;
       const words_t *c = reinterpret_cast<const words_t *>(cp[a] + at + (uint32_t)lane * 16);
-      p.c[a] = MT < 4 ? __builtin_nontemporal_load(c) : *c;  // read once, for one token tile
+      // Up to 32 tokens the codes are read once, past the caches (16 tokens, 28672 x 8192: 28.8 us, else 30.9); above
+      // that, other token tiles may read them again (64 tokens, 8192 x 8192, codes that the last cache still holds: 24.2
+      // us, past the caches 28.1).
+      p.c[a] = MT < 4 ? __builtin_nontemporal_load(c) : *c;
 #pragma unroll
       for (int g = 0; g < GT; ++g) {
         const int64_t row = (int64_t)min(st * KC / G + g, groups - 1) * n;
@@ -250,24 +252,34 @@ struct W4Call {
   hipStream_t stream;
 };
 
-template <int MT, int NT, int G, typename S, bool Z>
+template <int MT, int R, int NT, int G, typename S, bool Z>
 void launch(const W4Call &c) {
+  constexpr int kRows = R * NT;
   const int row_tiles = (c.n + 15) / 16;
-  hipLaunchKernelGGL((base_w4_kernel<MT, NT, G, S, Z>), dim3((row_tiles + NT * Shape<MT>::kRow - 1) / (NT * Shape<MT>::kRow), (c.m + 16 * MT - 1) / (16 * MT)),
+  hipLaunchKernelGGL((base_w4_kernel<MT, R, NT, G, S, Z>), dim3((row_tiles + kRows - 1) / kRows, (c.m + 16 * MT - 1) / (16 * MT)),
                      dim3(64 * Shape<MT>::kWaves), 0, c.stream, c.m, c.n, c.k, row_tiles, c.col_tiles, (const uint8_t *)c.w->codes,
                      (const S *)c.w->scales, (const S *)c.w->zeros, c.x, c.xs, c.y, c.ys);
 }
-// Row tiles per workgroup: as many as still leave every compute unit a workgroup.  More tiles share the
-// reads of x, which for 16 tokens are four times those of one row tile's codes.  At most kMost, so that the
-// scales and zero points on their way (WORDS registers a tile) and the sums fit the registers.
+// Row tiles per workgroup: as many as still leave every compute unit a workgroup, since they share the
+// reads of x, which for 16 tokens are four times those of one row tile's codes.  Up to 32 tokens a wave takes
+// them, at most kMost, so that the scales and zero points on their way (kWords registers a tile) and the
+// sums fit the registers (16 tokens, 28672 x 8192: 30.2 us, with one row tile 42.8).  For
+// more tokens the waves of a group take one each, two of them, so that two stages of each group fit the LDS, or
+// four (64 tokens through 28672 x 8192: 78 us, with two 102; through 8192 x 8192, 128 workgroups of four: 38
+// and 30).
 template <int MT, int G, typename S, bool Z>
 void pick_tiles(const W4Call &c) {
-  constexpr int kWords = kTileK / G * (int)sizeof(S) * (Z ? 2 : 1);
-  constexpr int kMost = MT == 4 ? (kWords <= 8 ? 2 : 1) : 64 / MT / kWords;
-  const int row_tiles = (c.n + 15) / 16 / Shape<MT>::kRow;
-  if (kMost >= 4 && row_tiles >= 4 * kComputeUnits) launch<MT, kMost >= 4 ? 4 : 1, G, S, Z>(c);
-  else if (kMost >= 2 && row_tiles >= 2 * kComputeUnits) launch<MT, kMost >= 2 ? 2 : 1, G, S, Z>(c);
-  else launch<MT, 1, G, S, Z>(c);
+  const int64_t row_tiles = (c.n + 15) / 16;
+  if constexpr (MT == 4) {
+    if ((row_tiles + 3) / 4 * ((c.m + 63) / 64) >= kComputeUnits) launch<MT, 4, 1, G, S, Z>(c);
+    else launch<MT, 2, 1, G, S, Z>(c);
+  } else {
+    constexpr int kWords = kTileK / G * (int)sizeof(S) * (Z ? 2 : 1);
+    constexpr int kMost = 64 / MT / kWords;
+    if (kMost >= 4 && row_tiles >= 4 * kComputeUnits) launch<MT, 1, kMost >= 4 ? 4 : 1, G, S, Z>(c);
+    else if (kMost >= 2 && row_tiles >= 2 * kComputeUnits) launch<MT, 1, kMost >= 2 ? 2 : 1, G, S, Z>(c);
+    else launch<MT, 1, 1, G, S, Z>(c);
+  }
 }
 template <int MT, int G>
 void pick_scale(const W4Call &c) {
