@@ -926,8 +926,14 @@ class AttnPlan:
         self.items = self.workspace = None
 
     def to(self, device) -> "AttnPlan":
-        """Uploads the items and allocates a workspace (calls that share the plan must not overlap)."""
+        """Uploads the items and allocates a workspace (calls that share the plan must not overlap).  Both stay where
+        they are when they are on the device already: a captured graph may hold their addresses."""
         torch = _torch()
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        if self.items is not None and self.items.device == device:
+            return self
         self.items = torch.from_numpy(self.host_items).to(device)
         n = self.desc.workspace_bytes
         self.workspace = torch.empty(n // 4, dtype=torch.float32, device=device) if n else None

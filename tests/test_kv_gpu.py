@@ -343,6 +343,13 @@ def test_attention_repeats_and_graph():
         assert torch.equal(o2[:t], out[:t]) and torch.equal(l2[:t], lse[:t])
 
 
+def test_plan_stays_where_it_is():
+    plan = B.lora_kv_attn_plan([0, 1], [0], [5000], 2, 1, 64).to("cuda")
+    at = plan.items.data_ptr(), plan.workspace.data_ptr()
+    assert plan.to("cuda") is plan and plan.to(plan.items.device) is plan
+    assert (plan.items.data_ptr(), plan.workspace.data_ptr()) == at
+
+
 def test_bad_items_are_skipped():
     c = Paged([64], 1, 64, 16)
     plan = B.lora_kv_attn_plan([0, 1], [0], [64], 2, 1, 64).to("cuda")
