@@ -343,6 +343,37 @@ def test_attention_repeats_and_graph():
         assert torch.equal(o2[:t], out[:t]) and torch.equal(l2[:t], lse[:t])
 
 
+@pytest.mark.parametrize("reqs", [3, 36])
+@pytest.mark.parametrize("q_len", [17, 32])
+def test_medium_chunks(reqs, q_len):
+    """17 to 32 rows of a request: row items where requests are few, tile items where they are many."""
+    c = Paged([40 + 3 * i for i in range(reqs)], 8, 64, 16, seed=reqs)
+    plan = check_attention(c, [q_len] * reqs, 8, label="medium")[0]
+    assert (plan.desc.num_tile_items > 0) == (reqs * 8 >= 256)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_len", [2, 40])
+@pytest.mark.parametrize("max_parts", [2, 64])
+def test_bad_places_in_joined_ranges(bad, q_len, max_parts):
+    """A value that is not finite reaches the joined rows that keep it and leaves the others bit for bit."""
+    n = 3900
+    c = Paged([n], 2, 64, 16, seed=12)
+    plan, q, out, lse = check_attention(c, [q_len], 4, max_parts=max_parts, label="joined, clean")
+    assert plan.desc.num_joins > 0
+    at = n - q_len + 1  # not kept by the first token
+    page, slot = int(c.table[0, at // 16]), at % 16
+    for which in (0, 1):
+        keep = c.store[page, which, :, slot].clone()
+        c.store[page, which, :, slot] = bad
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        B.lora_kv_attn(c.view, plan, q, o2, lse=l2)
+        assert torch.equal(o2[:1], out[:1]) and torch.equal(l2[:1], lse[:1])
+        if which == 1 or math.isnan(bad):
+            assert not bool(torch.isfinite(o2[1:q_len]).any())
+        c.store[page, which, :, slot] = keep
+
+
 def test_plan_stays_where_it_is():
     plan = B.lora_kv_attn_plan([0, 1], [0], [5000], 2, 1, 64).to("cuda")
     at = plan.items.data_ptr(), plan.workspace.data_ptr()
