@@ -109,7 +109,7 @@ typedef struct {
   int32_t kv_end;
   int32_t part;      /* -1: the item's results are final; else its first row of partial
                         results.  Join items: the number of parts, each `rows` rows of
-                        partial results, the first at row kv_begin */
+                        partial results, the first at row kv_begin; kv_end as in the last part */
 } lora_attn_item;
 
 #define LORA_ATTN_ROWS 16
@@ -156,7 +156,9 @@ lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t *seq, const
  * are rounded to bf16 for their product with V (out is bf16), the sum is not;
  * out rounded once.  Bit-identical from run to run.  Device-side items are
  * checked against the plan and the view: a bad one is skipped (debug build:
- * LORA_DEBUG_BAD_ITEM).  Rows of out and lse beyond num_tokens are left as they are.
+ * LORA_DEBUG_BAD_ITEM), and the join of ranges that reach past the view with them, so
+ * that a plan made for a larger view leaves those rows of out and lse as they are.
+ * Rows of out and lse beyond num_tokens are left as they are.
  * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (dtype, head_dim), LORA_EHIP.      */
 lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, const lora_attn_item *items, const void *q,
                          int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,

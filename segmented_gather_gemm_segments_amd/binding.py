@@ -848,6 +848,7 @@ class KvView:
         self.desc = lora_kv_view(LORA_BF16, dim, heads, tokens, pages, int(page_table.shape[0]), int(page_table.shape[1]),
                                  0, _dptr(k), _dptr(v), ps, hs, ts, _dptr(page_table))
         self.ref, self.index, self.device = ctypes.byref(self.desc), k.get_device(), k.device
+        self.num_seqs, self.max_kv = self.desc.num_seqs, self.desc.max_pages * tokens
         self.bf16, self.int32, self.fp32 = torch.bfloat16, torch.int32, torch.float32
 
 
@@ -924,6 +925,9 @@ class AttnPlan:
     def __init__(self, desc: lora_attn_plan, items: np.ndarray):
         self.desc, self.host_items, self.ref = desc, items, ctypes.byref(desc)
         self.items = self.workspace = None
+        # what the items reach: sequences below num_seqs, positions below max_kv
+        self.num_seqs = int(items[:, 3].max()) + 1 if len(items) else 0
+        self.max_kv = int(items[:, 6].max()) if len(items) else 0
 
     def to(self, device) -> "AttnPlan":
         """Uploads the items and allocates a workspace (calls that share the plan must not overlap).  Both stay where
@@ -944,7 +948,7 @@ def lora_kv_attn_plan(q_starts, seqs, kv_lens, q_heads: int, kv_heads: int, head
                       window: int = 0, max_parts: int = 0, num_seqs: Optional[int] = None,
                       max_kv: int = 2**31 - 1) -> AttnPlan:
     """Plan of a batch: request r has tokens q_starts[r] .. q_starts[r + 1] of q, sequence seqs[r] of kv_lens[r]
-    positions.  num_seqs, max_kv: the bounds to check against (lora_kv_attn checks the view's on the device)."""
+    positions.  num_seqs, max_kv: the bounds to check against (lora_kv_attn checks the view's)."""
     starts, sq, kv = _i32(q_starts), _i32(seqs), _i32(kv_lens)
     if starts.size < 1 or sq.size != starts.size - 1 or kv.size != sq.size:
         _refuse(f"{starts.size} starts, {sq.size} sequences and {kv.size} lengths")
@@ -961,10 +965,14 @@ def lora_kv_attn_plan(q_starts, seqs, kv_lens, q_heads: int, kv_heads: int, head
 def lora_kv_attn(view: KvView, plan: AttnPlan, q, out, lse=None, scale: Optional[float] = None, workspace=None,
                  stream=None):
     """out [T, q_heads, head_dim] (and lse [T, q_heads] fp32) of q over the cache; scale defaults to
-    head_dim ** -0.5, workspace to the plan's own."""
+    head_dim ** -0.5, workspace to the plan's own.  A plan that reaches past the view is refused (LORA_ERANGE); the debug
+    library runs it, skips those items and records them."""
     items = plan.items
     if items is None:
         _refuse("the plan has not been uploaded: call plan.to(device)")
+    if (plan.num_seqs > view.num_seqs or plan.max_kv > view.max_kv) and not _debug:
+        raise LoraError(LORA_ERANGE, f"the plan reaches {plan.num_seqs} sequences of up to {plan.max_kv} positions, the "
+                                     f"view holds {view.num_seqs} of {view.max_kv}")
     p, index, bf16, fp32 = plan.desc, view.index, view.bf16, view.fp32
     ws = plan.workspace if workspace is None else workspace
     heads, dim, tokens = p.q_heads, p.head_dim, p.num_tokens

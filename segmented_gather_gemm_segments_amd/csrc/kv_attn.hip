@@ -740,7 +740,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(Args a) {
   lora_attn_item it = a.items[ii];
   const int parts = it.part, base = it.kv_begin;
   it.part = -1;
-  it.kv_begin = it.kv_end = 0;
+  it.kv_begin = 0;  // kv_end stays: a join past the view has parts that were skipped
   if (!good_item(a, it, LORA_ATTN_TILE_ROWS) || parts < 1 || parts > LORA_ATTN_MAX_PARTS || base < 0 ||
       base + (int64_t)parts * it.rows > a.num_part_rows) {
     KV_CHECK(threadIdx.x != 0, LORA_DEBUG_BAD_ITEM);

@@ -397,6 +397,30 @@ def test_bad_items_are_skipped():
         assert bool((out == 4).all())
 
 
+@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("seq,kv_len", [(0, 3000), (3, 900)])
+def test_joins_past_the_view_are_skipped(q_len, seq, kv_len):
+    """Ranges that reach past the view are skipped, and so is what joins them: out and lse keep what they hold, whatever
+    the workspace does."""
+    c = Paged([900], 1, 64, 16, seed=2)
+    plan = B.lora_kv_attn_plan([0, q_len], [seq], [kv_len], 2, 1, 64, max_parts=4).to("cuda")
+    assert plan.desc.num_joins > 0
+    plan.workspace.fill_(1.0)
+    q = torch.ones((q_len, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 4.0), torch.full((q_len, 2), 4.0, device="cuda")
+    with pytest.raises(B.LoraError) as e:
+        B.lora_kv_attn(c.view, plan, q, out, lse=lse)
+    assert e.value.status == B.LORA_ERANGE
+    # the library itself, which learns of it on the device
+    strides = q.stride(0), q.stride(1)
+    status = B.lib().lora_kv_attn(c.view.ref, plan.ref, plan.items.data_ptr(), q.data_ptr(), *strides, out.data_ptr(), *strides,
+                                  lse.data_ptr(), 0.125, plan.workspace.data_ptr(), plan.workspace.nbytes,
+                                  torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == B.LORA_OK
+    assert bool((out == 4).all()) and bool((lse == 4).all())
+
+
 # ---------------------------------------------------------------- append
 @pytest.mark.parametrize("dim,page,heads", [(64, 16, 2), (8, 1, 1), (128, 24, 8), (256, 33, 3), (80, 8, 5)])
 @pytest.mark.parametrize("layout", ["page", "token"])

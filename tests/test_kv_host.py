@@ -417,3 +417,15 @@ def test_binding_refuses_tensors_it_cannot_pass_on():
         refused(B.LORA_EINVAL, lambda: B.lora_kv_append(v, *a))
     refused(B.LORA_EINVAL, lambda: B.lora_pages_copy(k, ids, ids[:2]))
     refused(B.LORA_EINVAL, lambda: B.lora_page_table_remap(ids, table, ids))
+
+
+def test_a_plan_past_the_view_is_refused():
+    torch = pytest.importorskip("torch")
+    k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
+    v = B.KvView(k, k, torch.zeros((2, 3), dtype=torch.int32))  # 2 sequences of up to 48 positions
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    for seqs, lens, parts, status in (([0, 1], [48, 0], 0, B.LORA_EINVAL),  # fits: refused as a host tensor only
+                                      ([0, 2], [4, 4], 0, B.LORA_ERANGE), ([0, 1], [4, 49], 0, B.LORA_ERANGE),
+                                      ([0, 1], [4, 9000], 5, B.LORA_ERANGE), ([5, 0], [0, 4], 0, B.LORA_ERANGE)):
+        plan = B.lora_kv_attn_plan([0, 1, 2], seqs, lens, 4, 2, 64, max_parts=parts).to("cpu")
+        refused(status, lambda: B.lora_kv_attn(v, plan, q, q.clone()))
