@@ -40,9 +40,9 @@ typedef struct {
   int32_t num_seqs;     /* rows of page_table */
   int32_t max_pages;    /* row length of page_table */
   int32_t reserved;     /* 0 */
-  void *k, *v;          /* device, 16-byte aligned: position 0, head 0 of page 0 */
+  void *k, *v;          /* device, 16-byte aligned: position 0, head 0 of page 0 (NULL without pages) */
   int64_t page_stride, head_stride, token_stride; /* elements, multiples of 8, >= 0 */
-  const int32_t *page_table; /* device [num_seqs][max_pages] */
+  const int32_t *page_table; /* device [num_seqs][max_pages] (NULL only where that is empty) */
 } lora_kv_view;
 
 /* ------------------------------------------------------------------------ */

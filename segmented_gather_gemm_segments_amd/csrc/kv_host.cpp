@@ -40,8 +40,9 @@ lora_status lora::check_view(const lora_kv_view *kv) {
   if (kv->page_stride < 0 || kv->head_stride < 0 || kv->token_stride < 0 || kv->page_stride % 8 ||
       kv->head_stride % 8 || kv->token_stride % 8)
     return fail(LORA_EINVAL, "KV strides must be multiples of 8 elements, not negative");
-  const bool any = kv->num_pages > 0 && kv->num_seqs > 0 && kv->max_pages > 0;
-  if (any && (!kv->k || !kv->v || !kv->page_table)) return fail(LORA_EINVAL, "null KV pointer");
+  // attention reads the page table also where there are no pages for its entries to name
+  const bool table = kv->num_seqs > 0 && kv->max_pages > 0, rows = table && kv->num_pages > 0;
+  if ((table && !kv->page_table) || (rows && (!kv->k || !kv->v))) return fail(LORA_EINVAL, "null KV pointer");
   if (((uintptr_t)kv->k & 15) || ((uintptr_t)kv->v & 15) || ((uintptr_t)kv->page_table & 3))
     return fail(LORA_EINVAL, "k and v must be 16-byte aligned");
   return LORA_OK;

@@ -429,3 +429,15 @@ def test_a_plan_past_the_view_is_refused():
                                       ([0, 1], [4, 9000], 5, B.LORA_ERANGE), ([5, 0], [0, 4], 0, B.LORA_ERANGE)):
         plan = B.lora_kv_attn_plan([0, 1, 2], seqs, lens, 4, 2, 64, max_parts=parts).to("cpu")
         refused(status, lambda: B.lora_kv_attn(v, plan, q, q.clone()))
+
+
+def test_a_view_without_pages_still_needs_its_table():
+    """Attention looks positions up in the page table before it knows that no page exists."""
+    plan = B.lora_kv_attn_plan([0, 1], [0], [4], 4, 2, 64).desc
+    for v in (view(num_pages=0, page_table=None), view(num_pages=0, page_table=None, k=None, v=None)):
+        assert B.lib().lora_kv_attn(ctypes.byref(v), ctypes.byref(plan), 16, 16, 256, 64, 16, 256, 64, None, 0.1, None, 0,
+                                    None) == B.LORA_EINVAL
+        assert B.lib().lora_kv_append(ctypes.byref(v), 16, 16, 128, 64, 16, 16, 1, None) == B.LORA_EINVAL
+    for change in (dict(num_seqs=0), dict(max_pages=0)):  # nothing to look up
+        v = view(page_table=None, k=None, v=None, **change)
+        assert B.lib().lora_kv_append(ctypes.byref(v), 16, 16, 128, 64, 16, 16, 1, None) == B.LORA_OK
