@@ -179,7 +179,9 @@ lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, con
  * stream orders the two uses), and lora_kv_trim gives spares back to the
  * pool once that work is done.  A lora_kv and its pool are not thread-safe.
  *
- *   create    LORA_KV_HOST_ONLY: bookkeeping only, no device work (tests).  Errors: LORA_EINVAL,
+ *   create    fills the page table with -1, done on return, ordered behind no stream: nothing queued
+ *             may still use that memory, and no stream of the device may be in capture.
+ *             LORA_KV_HOST_ONLY: bookkeeping only, no device work (tests).  Errors: LORA_EINVAL,
  *             LORA_EUNSUPPORTED (a pool that is not plain bf16, head_dim, a page that
  *             holds no position or whose V is not 16-byte aligned)
  *   extend    sequence seqs[i] grows by new_tokens[i] >= 0 positions (a sequence not in use

@@ -1026,7 +1026,13 @@ class KvCache:
             return
         dev = pool.storage.device
         with _On(dev, None):
+            stream = torch.cuda.current_stream(dev)
+            if torch.cuda.is_current_stream_capturing():
+                _refuse("a KvCache cannot be made while its stream is being captured")
             self.page_table = torch.empty((max_seqs, max_pages), dtype=torch.int32, device=dev)
+            # the table may be memory that work still queued on this stream uses, and lora_kv_create, which fills it,
+            # knows nothing of the stream
+            stream.synchronize()
             _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, _dptr(self.page_table), 0,
                                         ctypes.byref(h)))
         self._own(h)

@@ -590,3 +590,39 @@ def test_bookkeeping_is_refused_under_capture():
     g.replay()
     torch.cuda.synchronize()
     assert kv.length(0) == 3 and float(x[0]) == 1
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_a_new_cache_waits_for_the_memory_of_its_table(side):
+    """The page table may be a block that work queued on the current stream still writes: it holds -1 all the same."""
+    pool = B.Pool(torch.zeros((8, 16, 64), dtype=torch.bfloat16, device="cuda"), 16)
+    stream = torch.cuda.Stream() if side else torch.cuda.current_stream()
+    big = torch.zeros(1 << 28, dtype=torch.float32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        old = torch.empty((40, 3000), dtype=torch.int32, device="cuda")
+        at = old.data_ptr()
+        for _ in range(20):  # about 10 ms of work before the write
+            big.add_(1)
+        old.fill_(7)
+        del old
+        kv = B.KvCache(pool, 2, 32, 40, 3000)
+        assert kv.page_table.data_ptr() == at, "the allocator gave other memory: the case is not the one meant"
+    torch.cuda.synchronize()
+    assert bool((kv.page_table == -1).all())
+    kv.extend([3], [20])
+    assert kv.page_table[3, :3].tolist() == kv.pages(3).tolist()
+
+
+def test_a_cache_is_not_made_under_capture():
+    pool = B.Pool(torch.zeros((8, 16, 64), dtype=torch.bfloat16, device="cuda"), 16)
+    g, x = torch.cuda.CUDAGraph(), torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        x.add_(1)
+        with pytest.raises(B.LoraError) as e:
+            B.KvCache(pool, 2, 32, 2, 4)
+        assert e.value.status == B.LORA_EINVAL
+    g.replay()
+    torch.cuda.synchronize()
+    assert float(x[0]) == 1 and pool.num_free() == 8
