@@ -776,13 +776,13 @@ def lora_w4_bytes(n: int, k: int) -> int:
 
 def lora_w4_pack(rows, twos_complement: bool = False, stream=None):
     """Tiled codes [ceil(n/16), ceil(k/128), 64, 16] of row-major ones: rows uint8 [n, k/2] on the
-    device, element 2i in the low nibble."""
+    device, element 2i in the low nibble.  The codes are memory of the stream that writes them."""
     torch = _torch()
     _tensors(rows.device, ("rows", rows, torch.uint8))
     _flat("rows", rows)
     n, k = int(rows.shape[0]), int(rows.shape[1]) * 2
     lora_w4_bytes(n, k)
-    with _On(rows.device, stream) as s:
+    with _On(rows.device, stream) as s, torch.cuda.stream(stream):
         codes = torch.empty((-(-n // 16), -(-k // 128), 64, 16), dtype=torch.uint8, device=rows.device)
         _check(lib().lora_w4_pack(n, k, int(bool(twos_complement)), _dptr(rows), _dptr(codes), s))
     return codes

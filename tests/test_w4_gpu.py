@@ -175,3 +175,21 @@ def test_empty_call_streams_and_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y.cpu(), want)
+
+
+def test_packing_on_another_stream():
+    """Codes packed on a stream of their own are not memory that work queued on the current one still writes."""
+    n, k = 512, 4096
+    u, s, z, rows = make(n, k, 32, False, torch.float32, 6, True)
+    rows = rows.cuda()
+    want = B.lora_w4_pack(rows)
+    big = torch.zeros(1 << 28, dtype=torch.float32, device="cuda")
+    old, st = torch.empty_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):  # about 10 ms of work before the write
+        big.add_(1)
+    old.fill_(0x77)
+    del old
+    codes = B.lora_w4_pack(rows, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(codes, want)
