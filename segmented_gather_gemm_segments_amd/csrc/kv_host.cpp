@@ -205,13 +205,15 @@ struct Seq {
 
 struct Spare {
   int32_t page;
-  std::shared_ptr<void> mark;  // the work that may still read it
+  bool marked;                 // false: the mark could not be made yet
+  std::shared_ptr<void> mark;  // the work that may still read it (null: none, host only)
 };
 
 struct lora_kv {
   lora_pool *pool;
   int32_t kv_heads, head_dim, page_tokens, max_pages, flags;
   int32_t *table;
+  hipStream_t stream = nullptr;  // of the last call with device steps
   std::vector<Seq> seqs;
   std::vector<int32_t> refs;   // per page of the pool: sequences that hold it
   std::vector<Spare> spares;
@@ -240,8 +242,20 @@ lora_status check_ids(const lora_kv *kv, const int32_t *ids, int32_t n) {
   return LORA_OK;
 }
 
-lora_status begin_device(const lora_kv *kv, hipStream_t stream) {
-  return kv->host_only() ? LORA_OK : kv_not_capturing(stream);
+lora_status begin_device(lora_kv *kv, hipStream_t stream) {
+  if (kv->host_only()) return LORA_OK;
+  const lora_status st = kv_not_capturing(stream);
+  if (st == LORA_OK) kv->stream = stream;
+  return st;
+}
+
+// A mark behind everything queued on the cache's stream; false where it cannot be made.
+bool try_mark(const lora_kv *kv, std::shared_ptr<void> *mark) {
+  try {
+    return kv_mark(kv->stream, mark) == LORA_OK;
+  } catch (const std::bad_alloc &) {
+    return false;
+  }
 }
 
 // The device steps of one call, in order: page copies, then table entries.
@@ -259,13 +273,14 @@ lora_status run_steps(lora_kv *kv, const Steps &s, hipStream_t stream) {
   return st;
 }
 
-// Pages that nothing holds any more become spares, marked behind everything queued on the stream.
-lora_status make_spares(lora_kv *kv, const std::vector<int32_t> &dropped, hipStream_t stream) {
-  if (dropped.empty()) return LORA_OK;
+// Pages that nothing holds any more become spares, marked behind everything queued on the stream.  Nothing here
+// fails, since the sequences have changed already (the caller has reserved the room): a mark that cannot be made is
+// made by a later trim, whose place in the stream is a later one.
+void make_spares(lora_kv *kv, const std::vector<int32_t> &dropped) {
+  if (dropped.empty()) return;
   std::shared_ptr<void> mark;
-  lora_status st = kv->host_only() ? LORA_OK : kv_mark(stream, &mark);
-  for (int32_t p : dropped) kv->spares.push_back({p, mark});
-  return st;
+  const bool marked = kv->host_only() || try_mark(kv, &mark);
+  for (int32_t p : dropped) kv->spares.push_back({p, marked, mark});
 }
 
 int64_t entry(const lora_kv *kv, int32_t seq, size_t i) { return (int64_t)seq * kv->max_pages + (int64_t)i; }
@@ -446,9 +461,9 @@ static lora_status shorten(lora_kv *kv, const int32_t *seqs, int32_t n, int32_t 
     }
     s.len = new_len;
   }
-  lora_status marked = make_spares(kv, dropped, stream);
+  make_spares(kv, dropped);
   if ((st = run_steps(kv, steps, stream)) != LORA_OK) return st;
-  return marked != LORA_OK ? marked : ok();
+  return ok();
 }
 
 extern "C" lora_status lora_kv_truncate(lora_kv *kv, int32_t seq, int32_t new_len, hipStream_t stream) {
@@ -522,10 +537,9 @@ extern "C" lora_status lora_kv_compact(lora_kv *kv, int32_t *moved, hipStream_t 
       for (int32_t &page : s.pages)
         if (to[(size_t)page] >= 0) page = to[(size_t)page];
     st = run_steps(kv, steps, stream);
-    const lora_status marked = make_spares(kv, dropped, stream);
+    make_spares(kv, dropped);
     *moved = (int32_t)steps.moves.size();
-    if (st != LORA_OK) return st;
-    return marked != LORA_OK ? marked : ok();
+    return st != LORA_OK ? st : ok();
   });
 }
 
@@ -534,8 +548,15 @@ extern "C" lora_status lora_kv_trim(lora_kv *kv, int32_t wait, int32_t *left) {
   return guarded([&]() -> lora_status {
     std::vector<int32_t> back;
     std::vector<Spare> kept;
+    const auto unmarked = [](const Spare &s) { return !s.marked; };
+    if (std::any_of(kv->spares.begin(), kv->spares.end(), unmarked)) {
+      std::shared_ptr<void> mark;
+      if (kv_not_capturing(kv->stream) == LORA_OK && try_mark(kv, &mark))
+        for (Spare &s : kv->spares)
+          if (!s.marked) s = {s.page, true, mark};
+    }
     for (const Spare &s : kv->spares) {
-      if (!s.mark || kv_mark_done(s.mark, wait != 0)) back.push_back(s.page);
+      if (s.marked && (!s.mark || kv_mark_done(s.mark, wait != 0))) back.push_back(s.page);
       else kept.push_back(s);
     }
     lora_status st = lora_pool_free(kv->pool, back.data(), (int32_t)back.size());
