@@ -222,8 +222,10 @@ lora_status lora_kv_seq(const lora_kv *kv, int32_t seq, int32_t *length, int32_t
 lora_status lora_kv_get_stats(const lora_kv *kv, lora_kv_stats *stats);
 /* The descriptor that append and attention take. */
 lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view);
-/* Waits for the work on its spares, gives every page back to the pool (which
- * must still exist) and frees the object. */
+/* Waits for the work that its stream (that of its last call, which must still
+ * exist) holds by now, gives every page back to the pool (which must still exist too) and
+ * frees the object.  Pages whose work cannot be waited for -- the stream is in capture, or another
+ * device than the pool's is current -- stay taken for good. */
 void lora_kv_destroy(lora_kv *kv);
 
 /* ------------------------------------------------------------------------ */

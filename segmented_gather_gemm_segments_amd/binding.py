@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from dataclasses import dataclass
 from typing import Optional
 
@@ -523,18 +524,19 @@ class Pool:
                                           _dptr(src_scales), _stream(stream)))
 
     def close(self):
-        """Destroys the pool, and before it every KvCache over it."""
+        """Destroys the pool, and before it every KvCache over it (which waits for the device, so that it is refused
+        while the current stream is being captured)."""
         if self._h:
-            for box in self.__dict__.pop("_kv_handles", []):
+            boxes = self.__dict__.get("_kv_handles", [])
+            if any(box[0] and box[1] is not None for box in boxes):
+                _not_capturing("a pool with KV caches cannot be closed")
+            for box in boxes:
                 _kv_destroy(box)
             lib().lora_pool_destroy(self._h)
             self._h = None
 
     def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
+        _close_later(self)
 
 
 class Cache:
@@ -1004,10 +1006,52 @@ def lora_kv_attn(view: KvView, plan: AttnPlan, q, out, lse=None, scale: Optional
             lse_ptr, dim ** -0.5 if scale is None else scale, wp, wb)
 
 
+def _capturing() -> bool:
+    torch = sys.modules.get("torch")
+    return torch is not None and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+def _not_capturing(what: str):
+    if _capturing():
+        _refuse(f"{what} while the current stream is being captured")
+
+
 def _kv_destroy(box: list):
-    if box[0]:
-        lib().lora_kv_destroy(box[0])
-        box[0] = None
+    """box: the handle (None once it is gone) and the device whose work it waits for (None: host only)."""
+    handle, device = box
+    if not handle:
+        return
+    if device is not None:
+        cuda = _torch().cuda
+        cuda.synchronize(device)
+        with cuda.device(device):
+            lib().lora_kv_destroy(handle)
+    else:
+        lib().lora_kv_destroy(handle)
+    box[0] = None
+
+
+_waiting = []  # closes of objects that were collected during a capture
+
+
+def _close_later(owner):
+    """What __del__ does: closes, or under capture, which a wait for the device would end, leaves it to the next call that
+    makes, changes or closes a KvCache."""
+    try:
+        try:
+            owner.close()
+        except LoraError:
+            if _capturing():
+                _waiting.append(owner.close)
+    except Exception:
+        pass
+
+
+def _close_waiting():
+    if _waiting and not _capturing():
+        todo, _waiting[:] = _waiting[:], []
+        for close in todo:
+            close()
 
 
 class KvCache:
@@ -1016,13 +1060,14 @@ class KvCache:
 
     def __init__(self, pool: Pool, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int, host_only: bool = False):
         torch = _torch()
+        _close_waiting()
         self.pool, self.max_pages, self._host_only = pool, max_pages, host_only
         self.page_table = None
         h = ctypes.c_void_p()
         if host_only:
             _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, None, LORA_KV_HOST_ONLY,
                                         ctypes.byref(h)))
-            self._own(h)
+            self._own(h, None)
             return
         dev = pool.storage.device
         with _On(dev, None):
@@ -1035,15 +1080,15 @@ class KvCache:
             stream.synchronize()
             _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, _dptr(self.page_table), 0,
                                         ctypes.byref(h)))
-        self._own(h)
+        self._own(h, dev)
         tokens, size = self.stats()["page_tokens"], kv_heads * head_dim
         flat = pool.storage.view(pool.storage.shape[0], -1)
         part = lambda i: flat[:, i * size * tokens:(i + 1) * size * tokens].view(-1, kv_heads, tokens, head_dim)
         self.view = KvView(part(0), part(1), self.page_table)
 
-    def _own(self, handle):
+    def _own(self, handle, device):
         """The handle in a box that the pool knows too: whichever goes first, the cache is destroyed before the pool."""
-        self._box = [handle]
+        self._box = [handle, device]
         self.pool.__dict__.setdefault("_kv_handles", []).append(self._box)
 
     @property
@@ -1051,6 +1096,7 @@ class KvCache:
         return self._box[0]
 
     def _call(self, name, *args, stream=None):
+        _close_waiting()
         if self._host_only:
             _check(getattr(lib(), name)(self._h, *args, None))
             return
@@ -1080,7 +1126,11 @@ class KvCache:
         return n.value
 
     def trim(self, wait: bool = False) -> int:
+        """Pages still spare afterwards; refused under capture, where the marks of their readers cannot be asked."""
         n = ctypes.c_int32(0)
+        if not self._host_only:
+            _not_capturing("spares cannot be given back")
+        _close_waiting()
         _check(lib().lora_kv_trim(self._h, int(wait), ctypes.byref(n)))
         return n.value
 
@@ -1100,14 +1150,14 @@ class KvCache:
         return {f: getattr(st, f) for f, _ in lora_kv_stats._fields_}
 
     def close(self):
+        """Waits for the device and gives the pages back to the pool; refused under capture."""
         box = getattr(self, "_box", None)
         if box is not None:
+            if box[0] and box[1] is not None:
+                _not_capturing("a KvCache cannot be closed")
             _kv_destroy(box)
             boxes = self.pool.__dict__.get("_kv_handles", [])
             boxes[:] = [b for b in boxes if b is not box]
 
     def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
+        _close_later(self)

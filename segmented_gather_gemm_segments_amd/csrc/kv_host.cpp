@@ -619,16 +619,22 @@ extern "C" lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view) {
 
 extern "C" void lora_kv_destroy(lora_kv *kv) {
   if (!kv) return;
-  bool any = !kv->spares.empty();
-  for (int32_t r : kv->refs) any = any || r > 0;
-  if (any && !kv->host_only()) kv_device_wait();
   try {
+    // A page goes back only once its readers are known to be done: behind a mark of the cache's stream for what
+    // sequences hold, behind its own for a spare.  Where a wait fails, or memory for it, the page stays taken.
     std::vector<int32_t> back;
-    for (const Spare &s : kv->spares) back.push_back(s.page);
+    bool any = false;
+    for (int32_t r : kv->refs) any = any || r > 0;
+    for (const Spare &s : kv->spares) any = any || !s.marked;
+    std::shared_ptr<void> mark;
+    const bool idle = kv->host_only() || (any && kv_not_capturing(kv->stream) == LORA_OK && try_mark(kv, &mark) &&
+                                          kv_mark_done(mark, true));
+    for (const Spare &s : kv->spares)
+      if (s.marked ? !s.mark || kv_mark_done(s.mark, true) : idle) back.push_back(s.page);
     for (size_t p = 0; p < kv->refs.size(); ++p)
-      if (kv->refs[p] > 0) back.push_back((int32_t)p);
+      if (kv->refs[p] > 0 && idle) back.push_back((int32_t)p);
     (void)lora_pool_free(kv->pool, back.data(), (int32_t)back.size());
-  } catch (...) {  // out of host memory: the pages stay taken
+  } catch (...) {
   }
   delete kv;
 }

@@ -25,7 +25,6 @@ lora_status kv_clear_table(int32_t *table, int64_t count);  // -1 everywhere, do
 lora_status kv_mark(hipStream_t stream, std::shared_ptr<void> *mark);
 bool kv_mark_done(const std::shared_ptr<void> &mark, bool wait);
 lora_status kv_not_capturing(hipStream_t stream);
-void kv_device_wait();
 
 // The debug word of kv_attn.hip (lora_kv_debug_flags adds that of kv_pages.hip; 0 in release builds).
 lora_status kv_attn_debug(uint32_t *flags, int32_t clear);

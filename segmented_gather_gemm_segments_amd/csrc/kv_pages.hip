@@ -178,8 +178,6 @@ lora_status lora::kv_not_capturing(hipStream_t stream) {
   return LORA_OK;
 }
 
-void lora::kv_device_wait() { (void)hipDeviceSynchronize(); }
-
 extern "C" lora_status lora_kv_debug_flags(uint32_t *flags, int32_t clear) {
   if (!flags) return fail(LORA_EINVAL, "null flags");
   *flags = 0;

@@ -136,7 +136,29 @@ static void taken_again() {
   CHECK(lora_kv_extend(c.kv, &first, &n, 1, kStream) == LORA_OK && c.spares() == 0 && c.free_pages() == before);
 }
 
+// A cache that goes gives back what it knows to be done, and keeps the rest from the pool.
+static void destroyed(Way mark, bool wait_works, bool capturing, bool spare) {
+  Cache c;
+  const int32_t first = 0;
+  if (spare) CHECK(lora_kv_free(c.kv, &first, 1, kStream) == LORA_OK);
+  const bool works = mark == kWorks && wait_works && !capturing;
+  g_mark = mark;
+  g_wait_works = wait_works;
+  g_capturing = capturing;
+  lora_kv_destroy(c.kv);
+  c.kv = nullptr;
+  // the spares' own mark was made before, and is waited for whatever becomes of the others'
+  CHECK(c.free_pages() == (works ? kPages : kPages - 7 + (spare && wait_works ? 2 : 0)));
+}
+
 int main() {
+  for (bool spare : {false, true}) {
+    destroyed(kWorks, true, false, spare);
+    destroyed(kFails, true, false, spare);
+    destroyed(kThrows, true, false, spare);
+    destroyed(kWorks, false, false, spare);
+    destroyed(kWorks, true, true, spare);
+  }
   for (int op = 0; op < 3; ++op)
     for (Way way : {kFails, kThrows}) dropped_pages(op, way);
   taken_again();

@@ -626,3 +626,35 @@ def test_a_cache_is_not_made_under_capture():
     g.replay()
     torch.cuda.synchronize()
     assert float(x[0]) == 1 and pool.num_free() == 8
+
+
+def test_caches_that_go_during_a_capture():
+    """A KvCache (and a pool with one) collected while a graph is captured leaves the capture whole and gives its pages
+    back at the next call; closing one there is refused."""
+    storage = torch.zeros((8, 16, 64), dtype=torch.bfloat16, device="cuda")
+    pool, lost = B.Pool(storage, 16), B.Pool(storage.clone(), 16)
+    kept, gone, orphan = B.KvCache(pool, 2, 32, 2, 4), B.KvCache(pool, 2, 32, 2, 4), B.KvCache(lost, 2, 32, 2, 4)
+    kept.extend([0], [3])
+    gone.extend([0, 1], [9, 3])
+    gone.free([1])
+    orphan.extend([0], [1])
+    torch.cuda.synchronize()
+    g, x = torch.cuda.CUDAGraph(), torch.zeros(4, device="cuda")
+    with torch.cuda.graph(g):
+        x.add_(1)
+        for call in (kept.close, kept.trim, pool.close):
+            with pytest.raises(B.LoraError) as e:
+                call()
+            assert e.value.status == B.LORA_EINVAL
+        del gone, orphan, lost
+        x.add_(1)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert float(x[0]) == 4 and kept.length(0) == 3
+    assert pool.num_free() == 8 - 1 - 2 - 1
+    kept.extend([0], [1])
+    assert pool.num_free() == 8 - 1 and not B._waiting
+    kept.close()
+    assert pool.num_free() == 8
+    pool.close()
