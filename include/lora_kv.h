@@ -52,13 +52,13 @@ typedef struct {
  *   src, dst   device int32 [n]; a pair with an id outside [0, num_pages) is
  *              skipped (debug build: LORA_DEBUG_BAD_PAGE).  No page may be written
  *              twice or both read and written, except src[i] == dst[i], which changes nothing.
- * Errors: LORA_EINVAL, LORA_EHIP.                                           */
+ * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (64 GiB and more to copy), LORA_EHIP. */
 lora_status lora_pages_copy(void *storage, int64_t page_bytes, int32_t num_pages, const int32_t *src,
                             const int32_t *dst, int32_t n, hipStream_t stream);
 /* table_out[i] = remap[table_in[i]] for entries in [0, num_pages); other entries
  * (such as -1) are copied as they are.  remap device int32 [num_pages]; table_in and
  * table_out device int32 [count], the same array or not overlapping.
- * Errors: LORA_EINVAL, LORA_EHIP.                                           */
+ * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (2^32 entries and more), LORA_EHIP. */
 lora_status lora_page_table_remap(const int32_t *remap, int32_t num_pages, const int32_t *table_in,
                                   int32_t *table_out, int64_t count, hipStream_t stream);
 
@@ -73,7 +73,7 @@ lora_status lora_page_table_remap(const int32_t *remap, int32_t num_pages, const
  *                 [0, max_pages * page_tokens) it is skipped (LORA_DEBUG_BAD_TOKEN)
  * No two tokens may name the same place (a page held by two sequences is
  * written by neither: extend copies it first).  Errors: LORA_EINVAL,
- * LORA_EUNSUPPORTED, LORA_EHIP.                                             */
+ * LORA_EUNSUPPORTED (view; 64 GiB and more of new K rows), LORA_EHIP.       */
 lora_status lora_kv_append(const lora_kv_view *kv, const void *k_new, const void *v_new, int64_t new_token_stride,
                            int64_t new_head_stride, const int32_t *token_seq, const int32_t *token_pos,
                            int32_t num_tokens, hipStream_t stream);
@@ -159,7 +159,8 @@ lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t *seq, const
  * LORA_DEBUG_BAD_ITEM), and the join of ranges that reach past the view with them, so
  * that a plan made for a larger view leaves those rows of out and lse as they are.
  * Rows of out and lse beyond num_tokens are left as they are.
- * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (dtype, head_dim), LORA_EHIP.      */
+ * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (dtype, head_dim, strides of 2^35 elements,
+ * 2^24 items of all KV heads and more), LORA_EHIP.                          */
 lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, const lora_attn_item *items, const void *q,
                          int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,
                          int64_t out_head_stride, float *lse, float scale, void *workspace, int64_t workspace_bytes,

@@ -868,6 +868,10 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
                 (long long)workspace_bytes);
   const int64_t all = (int64_t)plan->num_row_items + plan->num_tile_items + plan->num_joins;
   if (all * kv->kv_heads > INT32_MAX) return fail(LORA_EINVAL, "not a plan");
+  // row and tile items have at most 256 threads where their grid is large
+  if (too_many((int64_t)plan->num_row_items * kv->kv_heads, 256) || too_many((int64_t)plan->num_tile_items * kv->kv_heads, 256) ||
+      too_many((int64_t)plan->num_joins * kv->kv_heads, kJoinThreads))
+    return fail(LORA_EUNSUPPORTED, "too many items for one launch");
   if (plan->num_tokens == 0 || all == 0) return ok();
   if (!items || !q || !out) return fail(LORA_EINVAL, "null pointer");
   if (!aligned16(items) || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3))

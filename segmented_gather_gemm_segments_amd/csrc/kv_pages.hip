@@ -108,16 +108,18 @@ lora_status launched(const char *what) {
 
 lora_status lora::kv_move_pages(void *storage, int64_t page_bytes, const std::vector<std::pair<int32_t, int32_t>> &moves,
                                 hipStream_t stream) {
-  const int slices = (int)((page_bytes + kSliceBytes - 1) / kSliceBytes);
-  for (size_t i0 = 0; i0 < moves.size(); i0 += kListMoves) {
+  const int64_t slices = (page_bytes + kSliceBytes - 1) / kSliceBytes;
+  if (too_many(slices, kThreads)) return fail(LORA_EUNSUPPORTED, "pages of %lld bytes", (long long)page_bytes);
+  const size_t most = (size_t)std::min<int64_t>(kListMoves, (int64_t)UINT32_MAX / kThreads / slices);  // of one launch
+  for (size_t i0 = 0; i0 < moves.size(); i0 += most) {
     MoveList list{};
-    const int n = (int)std::min<size_t>(kListMoves, moves.size() - i0);
+    const int n = (int)std::min<size_t>(most, moves.size() - i0);
     for (int i = 0; i < n; ++i) {
       list.from[i] = moves[i0 + (size_t)i].first;
       list.to[i] = moves[i0 + (size_t)i].second;
     }
-    hipLaunchKernelGGL(list_copy_kernel, dim3(n * slices), dim3(kThreads), 0, stream, (char *)storage, page_bytes, list,
-                       slices);
+    hipLaunchKernelGGL(list_copy_kernel, dim3((unsigned)(n * slices)), dim3(kThreads), 0, stream, (char *)storage, page_bytes,
+                       list, (int)slices);
   }
   return launched("page move launch");
 }
@@ -201,7 +203,7 @@ extern "C" lora_status lora_pages_copy(void *storage, int64_t page_bytes, int32_
   if (!aligned(storage, 16) || !aligned(src, 4) || !aligned(dst, 4))
     return fail(LORA_EINVAL, "page storage must be 16-byte aligned");
   const int64_t slices = (page_bytes + kSliceBytes - 1) / kSliceBytes;
-  if (slices * n > INT32_MAX) return fail(LORA_EUNSUPPORTED, "page copy too large");
+  if (too_many(slices, (int64_t)kThreads * n)) return fail(LORA_EUNSUPPORTED, "page copy too large");
   hipLaunchKernelGGL(pages_copy_kernel, dim3((unsigned)(slices * n)), dim3(kThreads), 0, stream, (char *)storage,
                      page_bytes, num_pages, src, dst, (int)slices);
   return launched("page copy launch");
@@ -215,7 +217,7 @@ extern "C" lora_status lora_page_table_remap(const int32_t *remap, int32_t num_p
   if (!aligned(table_in, 4) || !aligned(table_out, 4) || !aligned(remap, 4))
     return fail(LORA_EINVAL, "page tables must be 4-byte aligned");
   const int64_t blocks = (count + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX) return fail(LORA_EUNSUPPORTED, "page table too large");
+  if (too_many(blocks, kThreads)) return fail(LORA_EUNSUPPORTED, "page table too large");
   hipLaunchKernelGGL(table_remap_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, remap, num_pages, table_in,
                      table_out, count);
   return launched("page-table remap launch");
@@ -235,7 +237,7 @@ extern "C" lora_status lora_kv_append(const lora_kv_view *kv, const void *k_new,
     return fail(LORA_EINVAL, "new rows must be 16-byte aligned");
   const int64_t units = (int64_t)num_tokens * kv->kv_heads * (kv->head_dim / 8);
   const int64_t blocks = (units + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX) return fail(LORA_EUNSUPPORTED, "append too large");
+  if (too_many(blocks, kThreads)) return fail(LORA_EUNSUPPORTED, "append too large");
   hipLaunchKernelGGL(append_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, *kv, (const uint16_t *)k_new,
                      (const uint16_t *)v_new, new_token_stride, new_head_stride, token_seq, token_pos, units);
   return launched("append launch");

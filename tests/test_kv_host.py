@@ -441,3 +441,20 @@ def test_a_view_without_pages_still_needs_its_table():
     for change in (dict(num_seqs=0), dict(max_pages=0)):  # nothing to look up
         v = view(page_table=None, k=None, v=None, **change)
         assert B.lib().lora_kv_append(ctypes.byref(v), 16, 16, 128, 64, 16, 16, 1, None) == B.LORA_OK
+
+
+def test_calls_too_large_for_a_launch():
+    """A launch has fewer than 2^32 threads: what needs more is refused before it fails on the device."""
+    f, g = B.lib().lora_pages_copy, B.lib().lora_page_table_remap
+    for args in ((16, 16, 4, 16, 16, 2**24), (16, 2**20, 4, 16, 16, 2**16), (16, 2**36, 4, 16, 16, 1)):
+        assert f(*args, None) == B.LORA_EUNSUPPORTED, args
+    assert g(16, 4, 16, 16, 2**32, None) == B.LORA_EUNSUPPORTED
+    v = view()  # 16 units of 16 bytes a token
+    assert B.lib().lora_kv_append(ctypes.byref(v), 16, 16, 128, 64, 16, 16, 2**28, None) == B.LORA_EUNSUPPORTED
+    plan = B.lora_kv_attn_plan([0, 1], [0], [4], 4, 2, 64).desc
+    for field, n in (("num_row_items", 2**23), ("num_tile_items", 2**23), ("num_joins", 2**21)):
+        bad = B.lora_attn_plan()
+        ctypes.memmove(ctypes.byref(bad), ctypes.byref(plan), ctypes.sizeof(plan))
+        setattr(bad, field, n)
+        assert B.lib().lora_kv_attn(ctypes.byref(v), ctypes.byref(bad), 16, 16, 256, 64, 16, 256, 64, None, 0.1, None, 0,
+                                    None) == B.LORA_EUNSUPPORTED, field
