@@ -29,7 +29,7 @@ extern "C" {
 #endif
 
 typedef struct {
-  int32_t n, k;        /* W is n x k; n a multiple of 8, k of group */
+  int32_t n, k;        /* W is n x k; n a multiple of 8, at most 2^26, k of group, at most 2^24 */
   int32_t group;       /* 32, 64 or 128 */
   int32_t scale_dtype; /* LORA_F32 or LORA_BF16: element type of scales and zeros */
   const void *codes;   /* device, lora_w4_bytes(n, k) bytes */
@@ -45,7 +45,7 @@ lora_status lora_w4_bytes(int32_t n, int32_t k, int64_t *bytes);
  * codes a byte, element 2i in the low nibble (the LORA_WFMT_INT4 order).
  * twos_complement 1: the nibbles are -8 .. 7 and u = value + 8; 0: they are u
  * itself.  Padding gets u = 8.  rows and codes 16-byte aligned; n a multiple of
- * 8, k of 32.  Done once when weights are loaded.  Errors: LORA_EINVAL,
+ * 8, k of 32, below the limits above and 16 GiB of codes.  Done once when weights are loaded.  Errors: LORA_EINVAL,
  * LORA_EUNSUPPORTED, LORA_EHIP. */
 lora_status lora_w4_pack(int32_t n, int32_t k, int32_t twos_complement, const void *rows, void *codes,
                          hipStream_t stream);

@@ -33,6 +33,8 @@ constexpr int kTileBytes = 1024;   // codes of 16 rows x 128 k
 constexpr int kTileK = 128;
 __device__ const uint4 g_zeros = {0, 0, 0, 0};  // x behind the last k
 constexpr int kComputeUnits = 256;
+// The kernels count rows, columns and bytes of one row in 32 bits.
+constexpr int kMaxN = 1 << 26, kMaxK = 1 << 24;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));  // nearest even
@@ -313,11 +315,12 @@ extern "C" lora_status lora_w4_pack(int32_t n, int32_t k, int32_t twos_complemen
   lora_status st = lora_w4_bytes(n, k, &bytes);
   if (st != LORA_OK) return st;
   if (n % 8 || k % 32) return fail(LORA_EUNSUPPORTED, "4-bit weights need n a multiple of 8 and k of 32");
+  if (n > kMaxN || k > kMaxK) return fail(LORA_EUNSUPPORTED, "4-bit weights of n=%d k=%d", n, k);
   if (twos_complement != 0 && twos_complement != 1) return fail(LORA_EINVAL, "twos_complement is 0 or 1");
   if (!rows || !codes) return fail(LORA_EINVAL, "null pointer");
   if (!aligned16(rows) || !aligned16(codes)) return fail(LORA_EINVAL, "device arrays must be 16-byte aligned");
   const int64_t words = bytes / 4, blocks = (words + 255) / 256;
-  if (blocks > INT32_MAX) return fail(LORA_EUNSUPPORTED, "4-bit weights too large");
+  if (blocks > UINT32_MAX / 256) return fail(LORA_EUNSUPPORTED, "4-bit weights too large");
   hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, n, k, (k + kTileK - 1) / kTileK,
                      words, twos_complement ? 0x88888888u : 0u, (const uint32_t *)rows, (uint32_t *)codes);
   hipError_t e = hipGetLastError();
@@ -336,10 +339,11 @@ extern "C" lora_status lora_base_w4(int32_t dtype, int32_t m, const lora_w4_weig
     return fail(LORA_EUNSUPPORTED, "4-bit base projection needs n a multiple of 8 and k of the group");
   if (w->scale_dtype != LORA_F32 && w->scale_dtype != LORA_BF16)
     return fail(LORA_EUNSUPPORTED, "scale dtype %d", w->scale_dtype);
+  if (w->n > kMaxN || w->k > kMaxK) return fail(LORA_EUNSUPPORTED, "4-bit weights of n=%d k=%d", w->n, w->k);
   if (x_stride < w->k || y_stride < w->n || x_stride % 8 || y_stride % 8)
     return fail(LORA_EINVAL, "row strides must be multiples of 8 of at least k and n (got %lld and %lld)",
                 (long long)x_stride, (long long)y_stride);
-  if (x_stride > (1 << 24)) return fail(LORA_EUNSUPPORTED, "an x row stride above 2^24");
+  if (x_stride > kMaxK) return fail(LORA_EUNSUPPORTED, "an x row stride above 2^24");
   if (m == 0) return ok();
   if (!w->codes || !w->scales || !x || !y) return fail(LORA_EINVAL, "null pointer");
   if (!aligned16(w->codes) || !aligned16(w->scales) || !aligned16(w->zeros) || !aligned16(x) || !aligned16(y))

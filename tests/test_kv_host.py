@@ -458,3 +458,14 @@ def test_calls_too_large_for_a_launch():
         setattr(bad, field, n)
         assert B.lib().lora_kv_attn(ctypes.byref(v), ctypes.byref(bad), 16, 16, 256, 64, 16, 256, 64, None, 0.1, None, 0,
                                     None) == B.LORA_EUNSUPPORTED, field
+
+
+def test_w4_sizes_that_the_kernels_cannot_count():
+    """Row and column counts near 2^31 would wrap in the kernels' 32-bit indexes."""
+    def base(n, k, group=32):
+        w = B.lora_w4_weights(n, k, group, B.LORA_BF16, 16, 16, None)
+        return B.lib().lora_base_w4(B.LORA_BF16, 1, ctypes.byref(w), 16, k, 16, n, None)
+    for n, k in ((2**31 - 8, 32), (2**26 + 8, 32), (8, 2**31 - 32), (8, 2**24 + 32)):
+        assert base(n, k) == B.LORA_EUNSUPPORTED, (n, k)
+        assert B.lib().lora_w4_pack(n, k, 0, 16, 16, None) == B.LORA_EUNSUPPORTED, (n, k)
+    assert B.lib().lora_w4_pack(2**26, 512, 0, 16, 16, None) == B.LORA_EUNSUPPORTED  # codes of 2^32 words
