@@ -58,10 +58,13 @@ lora_status lora_w4_pack(int32_t n, int32_t k, int32_t twos_complement, const vo
  *              wider array (the q, k and v projections of a layer side by side)
  * bf16 products and fp32 sums (matrix cores), the group's scale and zero point applied in
  * fp32, y rounded once to nearest even.  The codes enter as 128 + u, which
- * bf16 holds exactly; 128 + z times the group's sum of x is taken off in fp32, so a
- * group's sum is off by about 2^-17 of sum |x| at most before scaling.  A
- * non-finite x, or one above 2^118 in magnitude, gives a non-finite or
- * unspecified y in its own row only.  Nothing is allocated, no workspace is
+ * bf16 holds exactly; 128 + z times the group's sum of x is taken off in fp32.  With
+ * zero points in 0..15 both sums have terms of at most 143 |x| and at most group + 4
+ * roundings, so before scaling a group's sum is off by at most
+ * 2^-24 (group + 4) 288 sum |x|: 2^-8.8 of sum |x| for groups of 128 if every rounding
+ * went one way, 2^-15.5 in a model with random x.  143 group |x| < 2^128 keeps both sums
+ * finite (|x| below 2^113.8 for groups of 128); a larger or non-finite x gives a
+ * non-finite or unspecified y in its own row only.  Nothing is allocated, no workspace is
  * used, and results are bit-identical from run to run; a token's bits do not
  * depend on the other tokens of the call except through m's tile choice.
  * m == 0 is a no-op.  x and y must not overlap.

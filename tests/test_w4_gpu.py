@@ -193,3 +193,21 @@ def test_packing_on_another_stream():
     codes = B.lora_w4_pack(rows, stream=st)
     torch.cuda.synchronize()
     assert torch.equal(codes, want)
+
+
+@pytest.mark.parametrize("m", [1, 17, 40])
+@pytest.mark.parametrize("group,power", [(128, 113), (64, 114), (32, 115)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_largest_activations(m, group, power, zeros):
+    """143 group |x| just below 2^128 (2^127.75): every sum is finite, and exact since x is 1.5 times one power of two."""
+    n, k = 48, 2 * group
+    assert 2.0 ** 127.5 < 143 * group * 1.5 * 2.0 ** power < 2.0 ** 128
+    u, s, z, rows = make(n, k, group, zeros, torch.float32, m + group, True)
+    s = s * 2.0 ** -10
+    x = torch.full((m, k), 1.5 * 2.0 ** power).bfloat16()
+    x[m // 2:] *= -1
+    want = (x.double() @ dense(u, s, z, group).t()).bfloat16()
+    assert bool(torch.isfinite(want).all())
+    y = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    B.lora_base_w4(x.cuda(), device(u, s, z, rows, n, k, group), y)
+    assert torch.equal(y.cpu(), want)
