@@ -322,55 +322,83 @@ class ServingBlock:
     def __init__(self, d_model: int, q_heads: int, kv_heads: int, head_dim: int, num_adapters: int, rank: int,
                  max_seqs: int, max_pages: int, pool_pages: int, group: int = 128, seed: int = 0, device="cuda"):
         torch = _torch()
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         gen = torch.Generator(device=device).manual_seed(seed)
-        self.device, self.d_model, self.head_dim = torch.device(device), d_model, head_dim
+        self.device, self.d_model, self.head_dim = device, d_model, head_dim
         self.q_heads, self.kv_heads = q_heads, kv_heads
         self.widths = {"q": (d_model, q_heads * head_dim), "k": (d_model, kv_heads * head_dim),
                        "v": (d_model, kv_heads * head_dim), "o": (q_heads * head_dim, d_model)}
         if q_heads * head_dim != d_model:
             raise ValueError("the pool's rows are as long as the hidden state: q_heads * head_dim == d_model")
-        rows = 16
-        storage = torch.zeros((pool_pages, rows, d_model), dtype=torch.bfloat16, device=device)
-        self.pool = B.Pool(storage, rows, shuffle_seed=seed + 1)
-        # adapters of q and o (square) share the pool with the KV pages; those of k and v have B^T rows of another width
-        # and keep them in stacks of their own
-        self.base, self.delta, self.rows16, self.scales = {}, {}, {}, {}
-        rank_dev = torch.full((num_adapters,), rank, dtype=torch.int32, device=device)
-        ranks = np.full(num_adapters, rank, np.int32)
-        pages = -(-rank // rows)
+        with torch.cuda.device(self.device):
+            rows = 16
+            storage = torch.zeros((pool_pages, rows, d_model), dtype=torch.bfloat16, device=device)
+            self.pool = B.Pool(storage, rows, shuffle_seed=seed + 1)
+            # adapters of q and o (square) share the pool with the KV pages; those of k and v have B^T rows of another width
+            # and keep them in stacks of their own
+            self.base, self.delta, self.rows16, self.scales = {}, {}, {}, {}
+            rank_dev = torch.full((num_adapters,), rank, dtype=torch.int32, device=device)
+            ranks = np.full(num_adapters, rank, np.int32)
+            pages = -(-rank // rows)
 
-        def paged(d):
-            table = np.zeros((num_adapters, pages), np.int32)
-            for a in range(num_adapters):
-                table[a] = self.pool.alloc(rank)
-                r = (torch.randn((rank, d), generator=gen, device=device) * d ** -0.5).bfloat16()
-                self.pool.write_rows(table[a], r)
-            return torch.from_numpy(table).to(device)
+            def paged(d):
+                table = np.zeros((num_adapters, pages), np.int32)
+                for a in range(num_adapters):
+                    table[a] = self.pool.alloc(rank)
+                    r = (torch.randn((rank, d), generator=gen, device=device) * d ** -0.5).bfloat16()
+                    self.pool.write_rows(table[a], r)
+                return torch.from_numpy(table).to(device)
 
-        for name, (k, n) in self.widths.items():
-            codes = torch.randint(0, 256, (n, k // 2), generator=gen, device=device, dtype=torch.uint8)
-            scales = ((0.5 + torch.rand((k // group, n), generator=gen, device=device)) / (4.6 * k ** 0.5)).bfloat16()
-            self.rows16[name], self.scales[name] = codes, scales
-            self.base[name] = B.W4Weights(n, k, group, B.lora_w4_pack(codes), scales)
-            if n == k == d_model:
-                a_pt, b_pt = paged(k), paged(n)
-                self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rows, storage, storage, rank_dev, ranks, a_pt, b_pt,
-                                             pages)
-            else:
-                a = (torch.randn((num_adapters, rank, k), generator=gen, device=device) * k ** -0.5).bfloat16()
-                b = (torch.randn((num_adapters, rank, n), generator=gen, device=device) * rank ** -0.5).bfloat16()
-                self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rank, a, b, rank_dev, ranks)
-        self.kv = B.KvCache(self.pool, kv_heads, head_dim, max_seqs, max_pages)
+            for name, (k, n) in self.widths.items():
+                codes = torch.randint(0, 256, (n, k // 2), generator=gen, device=device, dtype=torch.uint8)
+                scales = ((0.5 + torch.rand((k // group, n), generator=gen, device=device)) / (4.6 * k ** 0.5)).bfloat16()
+                self.rows16[name], self.scales[name] = codes, scales
+                self.base[name] = B.W4Weights(n, k, group, B.lora_w4_pack(codes), scales)
+                if n == k == d_model:
+                    a_pt, b_pt = paged(k), paged(n)
+                    self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rows, storage, storage, rank_dev, ranks, a_pt, b_pt,
+                                                 pages)
+                else:
+                    a = (torch.randn((num_adapters, rank, k), generator=gen, device=device) * k ** -0.5).bfloat16()
+                    b = (torch.randn((num_adapters, rank, n), generator=gen, device=device) * rank ** -0.5).bfloat16()
+                    self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rank, a, b, rank_dev, ranks)
+            self.kv = B.KvCache(self.pool, kv_heads, head_dim, max_seqs, max_pages)
 
     def project(self, name, x, y, token_adapter):
-        """y = W x + B (A x), the base from 4-bit codes, the delta of each token's adapter."""
+        """y = W x + B (A x), the base from 4-bit codes, the delta of each token's adapter.  x and y are contiguous, and
+        token_adapter names an adapter (or -1) for each of their rows: the delta takes bare addresses."""
+        k, n = self.widths[name]
+        self._rows(token_adapter, ("x", x, k), ("y", y, n))
         B.lora_base_w4(x, self.base[name], y)
-        B.lora_bgmv_fused(self.delta[name], token_adapter, x, y)
+        with B._On(self.device, None):
+            B.lora_bgmv_fused(self.delta[name], token_adapter, x, y)
+
+    def _rows(self, token_adapter, *named):
+        """Checks (name, tensor, width) triples of rows and the adapter ids that go with them; returns their number."""
+        torch = _torch()
+        t = token_adapter.numel()
+        B._tensors(self.device, ("token_adapter", token_adapter, torch.int32),
+                   *((name, rows, torch.bfloat16) for name, rows, _ in named))
+        B._flat("token_adapter", token_adapter)
+        for name, rows, width in named:
+            B._flat(name, rows)
+            if tuple(rows.shape) != (t, width):
+                B._refuse(f"{name} {tuple(rows.shape)}: {(t, width)} wanted for {t} adapter ids")
+        return t
 
     def step(self, hidden, seqs, new_tokens, token_adapter):
-        """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device."""
+        """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device.  A call that
+        is refused leaves the cache as it is."""
         torch = _torch()
+        seqs, new_tokens = [int(s) for s in seqs], [int(n) for n in new_tokens]
+        t = self._rows(token_adapter, ("hidden", hidden, self.d_model))
+        if len(seqs) != len(new_tokens) or any(n < 0 for n in new_tokens) or sum(new_tokens) != t:
+            B._refuse(f"{len(seqs)} sequences grow by {new_tokens}, hidden has {t} tokens")
         self.kv.extend(seqs, new_tokens)
+        if t == 0:
+            return torch.empty_like(hidden)
         lens = [self.kv.length(s) for s in seqs]
         starts = np.concatenate([[0], np.cumsum(new_tokens)]).astype(np.int32)
         seq = np.repeat(np.asarray(seqs, np.int32), new_tokens)
