@@ -658,3 +658,77 @@ def test_caches_that_go_during_a_capture():
     kept.close()
     assert pool.num_free() == 8
     pool.close()
+
+
+# ---------------------------------------------------------------- head dims between the usual ones
+@pytest.mark.parametrize("dim", [40, 80, 96, 104, 120, 136, 160, 192, 200, 248])
+def test_chunks_of_other_head_dims(dim):
+    """Heads that fill none of the kernels' widths, or 96 and 192 whole: few requests and many, single tokens and chunks."""
+    c = Paged([150, 64, 65, 1], 2, dim, 24, seed=dim)
+    check_attention(c, [70, 64, 2, 1], 4, label="few")
+    check_attention(c, [70, 33, 40, 1], 2, False, 30, label="few, windowed", kv_lens=[150, 64, 65, 1])
+    check_masks(c, [70, 33, 65, 1], 4, True, 5)
+    kv_lens = [1 + (37 * i) % 90 for i in range(36)]
+    c = Paged(kv_lens, 8, dim, 16, seed=dim + 1)
+    q_lens = [min(40, n) for n in kv_lens]
+    check_attention(c, q_lens, 8, label="many")
+    check_attention(c, [1] * 36, 24, window=50, label="many, single tokens")
+    check_masks(c, q_lens, 8, True, 50)
+
+
+@pytest.mark.parametrize("dim", [40, 96, 104, 192, 248, 256])
+@pytest.mark.parametrize("reqs", [1, 34])
+@pytest.mark.parametrize("q_len", [3, 70])
+def test_bad_places_with_other_head_dims(dim, reqs, q_len):
+    """A position that is not finite reaches the tokens that keep it and no others."""
+    n, at = 150, 150 - q_len + 1  # not kept by a chunk's first token
+    c = Paged([n], 8, dim, 16, seed=dim)
+    plan, q, out, lse = check_attention(c, [q_len] * reqs, 8, seqs=[0] * reqs, label="clean")
+    t = q_len * reqs
+    first = torch.arange(0, t, q_len, device="cuda")
+    others = torch.ones(t, dtype=torch.bool, device="cuda")
+    others[first] = False
+    page, slot = int(c.table[0, at // 16]), at % 16
+    for which, bad in ((0, float("nan")), (0, float("inf")), (1, float("nan")), (1, -float("inf"))):
+        keep = c.store[page, which, :, slot].clone()
+        c.store[page, which, :, slot] = bad
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        B.lora_kv_attn(c.view, plan, q, o2, lse=l2)
+        assert torch.equal(o2[first], out[first]) and torch.equal(l2[first], lse[first])
+        if which == 1 or math.isnan(bad):
+            assert not bool(torch.isfinite(o2[:t][others]).any())
+        c.store[page, which, :, slot] = keep
+
+
+@pytest.mark.parametrize("dim,max_parts", [(104, 3), (192, 5), (248, 2)])
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_joined_ranges_of_other_head_dims(dim, max_parts, q_len):
+    c = Paged([1300], 2, dim, 16, seed=dim)
+    plan = check_attention(c, [q_len], 8, max_parts=max_parts, label="joined")[0]
+    assert plan.desc.num_joins > 0
+
+
+# ---------------------------------------------------------------- a cache above 4 GiB
+def test_offsets_past_32_bits():
+    """Pages whose byte and element offsets pass 2^32 and 2^31: attention, append and copies reach them."""
+    total, heads, page, dim = 20000, 8, 64, 128  # 256 KiB a page, 4.9 GiB
+    small = Paged([300, 130], heads, dim, page, seed=31)
+    far = torch.tensor([19999, 16383, 16384, 3, 18001, 8191, 8192, 17000, 19000, 12345, 12346], dtype=torch.int32)
+    far = far[: small.store.shape[0]]
+    assert far.numel() == small.store.shape[0] and total * 2 * heads * page * dim > 2**31
+    store = torch.full((total, 2, heads, page, dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+    store[far.long().cuda()] = small.store
+    small.table = torch.where(small.table < 0, small.table, far[small.table.clamp(min=0).long()])
+    small.store = store
+    small.view = B.KvView(store[:, 0], store[:, 1], small.table.cuda())
+    check_attention(small, [1, 1], 64, label="far pages")
+    check_attention(small, [70, 40], 16, label="far pages, chunks")
+    new = torch.randn((2, 2, heads, dim), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    B.lora_kv_append(small.view, new[:, 0], new[:, 1], torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                     torch.tensor([299, 129], dtype=torch.int32, device="cuda"))
+    for i, (s, p) in enumerate(((0, 299), (1, 129))):
+        assert torch.equal(store[int(small.table[s, p // page]), :, :, p % page], new[i])
+    ids = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    B.lora_pages_copy(store, ids(19999, 5), ids(19998, 16385))
+    same = lambda a, b: torch.equal(store[a].view(torch.int16), store[b].view(torch.int16))
+    assert same(19998, 19999) and same(16385, 5)
