@@ -536,7 +536,10 @@ class Pool:
             self._h = None
 
     def __del__(self):
-        _close_later(self)
+        try:
+            _close_later(self)
+        except Exception:  # at the interpreter's end the module's names may be gone
+            pass
 
 
 class Cache:
@@ -1160,4 +1163,7 @@ class KvCache:
             boxes[:] = [b for b in boxes if b is not box]
 
     def __del__(self):
-        _close_later(self)
+        try:
+            _close_later(self)
+        except Exception:  # at the interpreter's end the module's names may be gone
+            pass

@@ -3,6 +3,9 @@ projection, without a GPU: the attention planner's coverage, the sequence bookke
 model, refusals."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -469,3 +472,18 @@ def test_w4_sizes_that_the_kernels_cannot_count():
         assert base(n, k) == B.LORA_EUNSUPPORTED, (n, k)
         assert B.lib().lora_w4_pack(n, k, 0, 16, 16, None) == B.LORA_EUNSUPPORTED, (n, k)
     assert B.lib().lora_w4_pack(2**26, 512, 0, 16, 16, None) == B.LORA_EUNSUPPORTED  # codes of 2^32 words
+
+
+def test_objects_left_at_the_end_of_the_program_go_quietly():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = f"""
+import sys
+sys.path[:0] = [{root!r}, {os.path.join(root, "tests")!r}]
+import test_kv_host as T
+pool = T.HostPool(8)
+kv = T.cache(pool)
+kv.extend([0], [9])
+sys.late = [T.B, kv, pool]  # goes after the names of the binding
+"""
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert got.returncode == 0 and got.stderr == "", got.stderr
