@@ -3,9 +3,6 @@ projection, without a GPU: the attention planner's coverage, the sequence bookke
 model, refusals."""
 import ctypes
 import math
-import os
-import subprocess
-import sys
 
 import numpy as np
 import pytest
@@ -474,16 +471,13 @@ def test_w4_sizes_that_the_kernels_cannot_count():
     assert B.lib().lora_w4_pack(2**26, 512, 0, 16, 16, None) == B.LORA_EUNSUPPORTED  # codes of 2^32 words
 
 
-def test_objects_left_at_the_end_of_the_program_go_quietly():
-    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    code = f"""
-import sys
-sys.path[:0] = [{root!r}, {os.path.join(root, "tests")!r}]
-import test_kv_host as T
-pool = T.HostPool(8)
-kv = T.cache(pool)
-kv.extend([0], [9])
-sys.late = [T.B, kv, pool]  # goes after the names of the binding
-"""
-    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
-    assert got.returncode == 0 and got.stderr == "", got.stderr
+def test_objects_left_at_the_interpreters_end(monkeypatch):
+    """By then a module's names may be None: what is left of its objects goes without an error."""
+    pool = HostPool(8)
+    kv = cache(pool)
+    for name in ("_close_later", "LoraError", "_capturing", "_kv_destroy"):
+        with monkeypatch.context() as m:
+            m.setattr(B, name, None)
+            kv.__del__()
+            pool.__del__()
+    kv.close()
