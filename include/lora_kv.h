@@ -184,7 +184,7 @@ lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, con
  *             may still use that memory, and no stream of the device may be in capture.
  *             LORA_KV_HOST_ONLY: bookkeeping only, no device work (tests).  Errors: LORA_EINVAL,
  *             LORA_EUNSUPPORTED (a pool that is not plain bf16, head_dim, a page that
- *             holds no position or whose V is not 16-byte aligned)
+ *             holds no position, whose V is not 16-byte aligned or that exceeds 32 GiB)
  *   extend    sequence seqs[i] grows by new_tokens[i] >= 0 positions (a sequence not in use
  *             starts at 0): pages are taken, and a shared page that the growth
  *             writes into is replaced by a copy.  All or nothing.  Errors: LORA_ERANGE (a sequence id),

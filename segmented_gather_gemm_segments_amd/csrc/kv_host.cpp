@@ -305,6 +305,7 @@ extern "C" lora_status lora_kv_create(lora_pool *pool, int32_t kv_heads, int32_t
   const int64_t tokens = elems / (2 * (int64_t)kv_heads * head_dim);
   if (tokens < 1 || elems % 8)
     return fail(LORA_EUNSUPPORTED, "a page of %lld elements for %d KV heads of %d", (long long)elems, kv_heads, head_dim);
+  if (elems > kKvMaxPageBytes / 2) return fail(LORA_EUNSUPPORTED, "a page of %lld elements", (long long)elems);
   if (tokens * max_pages > INT32_MAX) return fail(LORA_EUNSUPPORTED, "a sequence of more than 2^31 - 1 positions");
   const bool host_only = flags & LORA_KV_HOST_ONLY;
   if (!host_only && !device_page_table) return fail(LORA_EINVAL, "null page table");

@@ -14,6 +14,9 @@ namespace lora {
 // Whether a launch of this many workgroups goes past the 2^32 - 1 threads that one may have.
 inline bool too_many(int64_t workgroups, int64_t threads) { return workgroups > (int64_t)UINT32_MAX / threads; }
 
+// A page that one launch can copy.
+constexpr int64_t kKvMaxPageBytes = (int64_t)1 << 35;
+
 // Checks a descriptor's geometry and pointers (LORA_OK, or an error with its message).
 lora_status check_view(const lora_kv_view *kv);
 

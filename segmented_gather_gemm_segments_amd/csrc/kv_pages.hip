@@ -20,6 +20,7 @@ constexpr int kThreads = 256;
 // stores past the caches 170 us there, but 24 us for 1024 pages of 64 KiB, which the last cache holds, and
 // these 17.6 us.
 constexpr int kSliceBytes = 16 * kThreads;  // of a page, per workgroup
+static_assert(kKvMaxPageBytes / kSliceBytes <= UINT32_MAX / kThreads);
 
 // Copies bytes [slice * kSliceBytes, ..) of one page.
 __device__ __forceinline__ void copy_slice(char *storage, int64_t page_bytes, int from, int to, int slice) {
@@ -108,8 +109,7 @@ lora_status launched(const char *what) {
 
 lora_status lora::kv_move_pages(void *storage, int64_t page_bytes, const std::vector<std::pair<int32_t, int32_t>> &moves,
                                 hipStream_t stream) {
-  const int64_t slices = (page_bytes + kSliceBytes - 1) / kSliceBytes;
-  if (too_many(slices, kThreads)) return fail(LORA_EUNSUPPORTED, "pages of %lld bytes", (long long)page_bytes);
+  const int64_t slices = (page_bytes + kSliceBytes - 1) / kSliceBytes;  // lora_kv_create bounds page_bytes
   const size_t most = (size_t)std::min<int64_t>(kListMoves, (int64_t)UINT32_MAX / kThreads / slices);  // of one launch
   for (size_t i0 = 0; i0 < moves.size(); i0 += most) {
     MoveList list{};

@@ -451,6 +451,9 @@ def test_calls_too_large_for_a_launch():
     assert g(16, 4, 16, 16, 2**32, None) == B.LORA_EUNSUPPORTED
     v = view()  # 16 units of 16 bytes a token
     assert B.lib().lora_kv_append(ctypes.byref(v), 16, 16, 128, 64, 16, 16, 2**28, None) == B.LORA_EUNSUPPORTED
+    # a page that no launch could copy when a shared one is written
+    refused(B.LORA_EUNSUPPORTED, lambda: B.KvCache(HostPool(2, rows=2**20, width=2**15), 256, 256, 1, 1, host_only=True))
+    B.KvCache(HostPool(2, rows=2**20, width=2**14), 256, 256, 1, 1, host_only=True).close()
     plan = B.lora_kv_attn_plan([0, 1], [0], [4], 4, 2, 64).desc
     for field, n in (("num_row_items", 2**23), ("num_tile_items", 2**23), ("num_joins", 2**21)):
         bad = B.lora_attn_plan()
