@@ -170,7 +170,10 @@ lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, con
 /* Sequences over a pool's pages (host bookkeeping).  The pool's pages of page_rows x
  * row_width elements hold page_tokens = page_rows * row_width / (2 kv_heads head_dim)
  * positions each: first K [kv_heads][page_tokens][head_dim], then V.  The pool may hold adapters
- * too (lora_cache): each page belongs to whoever took it.
+ * too (lora_cache): each page belongs to whoever took it.  A page that an eviction of a lora_cache
+ * gave back may still be read on that cache's compute stream, and extend and compact take it
+ * without asking: a pool's lora_cache and lora_kv use one stream, the cache's compute stream.
+ * Pages freed by hand (lora_pool_free) are those that no queued work reads any more.
  *
  * A lora_kv owns the contents of the caller's device page table [max_seqs][max_pages] (-1
  * where there is no page).  Every device step goes on the `stream` of the call; use one

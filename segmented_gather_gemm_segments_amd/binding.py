@@ -936,7 +936,8 @@ class AttnPlan:
 
     def to(self, device) -> "AttnPlan":
         """Uploads the items and allocates a workspace (calls that share the plan must not overlap).  Both stay where
-        they are when they are on the device already: a captured graph may hold their addresses."""
+        they are when they are on the device already: a captured graph may hold their addresses.  They are memory of the
+        current stream: a call on another one comes behind it, and before the plan goes, as with any tensor."""
         torch = _torch()
         device = torch.device(device)
         if device.type == "cuda" and device.index is None:
@@ -1059,7 +1060,8 @@ def _close_waiting():
 
 class KvCache:
     """lora_kv: sequences over the pages of a Pool (which may hold adapters too).  The pool's storage is a
-    bf16 tensor [num_pages, page_rows, row_width]; the cache owns a device page table it makes itself."""
+    bf16 tensor [num_pages, page_rows, row_width]; the cache owns a device page table it makes itself.  All calls and the
+    kernels that read the pages use one stream, which is the compute stream of a Cache over the same pool."""
 
     def __init__(self, pool: Pool, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int, host_only: bool = False):
         torch = _torch()
