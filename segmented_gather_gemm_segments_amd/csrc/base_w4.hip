@@ -8,9 +8,11 @@
 // comes from the same x fragments against a constant operand of ones.
 //
 // Bound by HBM while the tokens of a decode batch are few, since at 4 bits a weight the codes are nearly all
-// the bytes (16 tokens, 28672 x 8192: 28.8 us, 4.3 TB/s), and for 64 tokens by x, which every
-// workgroup reads through L2 and LDS (8192 x 8192: 24.2 us, 355 TFLOP/s).  Small calls are a launch and one chain of loads
-// (one token, 4096 x 4096: 4.6 us in the kernel).
+// the bytes (16 tokens, 28672 x 8192: 28.9 us, 4.2 TB/s).  From 33 tokens on by the latency of a step: one step is in
+// flight, behind a wait for all its loads and a barrier, and waves wait for 42 % of their time (8192 x 8192, groups of 64 with
+// zero points: 24.6 us, 349 TFLOP/s, with the codes in the last cache, 30.2 from HBM).  The matrix cores are busy for 31 %
+// of it, half of that for the sums of x, which each wave forms anew; the LDS for 17 %.  Small calls are a launch and one
+// chain of loads (one token, 4096 x 4096: 4.6 us in the kernel).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -64,9 +66,9 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t w) {
 // scales and x on their way while it works on this one; their fp32 sums are added in order through LDS.
 // x goes through two LDS stages of each group: read as operands straight from memory, every lane would
 // name a line of its own, and the address units, which take those one by one, would set the time
-// (16 tokens, 28672 x 8192: 33.4 us, with the stages 29.9; 64 tokens, 8192 x 8192: 38.2 and 28.6).
+// (when the stages came, 16 tokens through 28672 x 8192 went from 33.4 to 29.9 us, 64 through 8192 x 8192 from 38.2 to 28.6).
 template <int MT>
-struct Shape {  // 64 tokens: 8 waves and steps of 128 k take 26.7 us there, these 24.2
+struct Shape {  // 64 tokens: 8 waves and steps of 128 k take 26.5 us there from the last cache, 29.7 from HBM, these 24.6 and 30.2
   static constexpr int kWaves = MT == 4 ? 16 : 8;
   static constexpr int kStep = MT == 4 ? 64 : 128;  // KC
 };
@@ -140,9 +142,9 @@ __global__ __launch_bounds__(64 * Shape<MT>::kWaves) void base_w4_kernel(int m, 
     for (int a = 0; a < NT; ++a) {
       const int64_t at = (int64_t)(st * KC / kTileK) * kTileBytes + st * KC % kTileK / 8;
       const words_t *c = reinterpret_cast<const words_t *>(cp[a] + at + (uint32_t)lane * 16);
-      // Up to 32 tokens the codes are read once, past the caches (16 tokens, 28672 x 8192: 28.8 us, else 30.9); above
-      // that, other token tiles may read them again (64 tokens, 8192 x 8192, codes that the last cache still holds: 24.2
-      // us, past the caches 28.1).
+      // Up to 32 tokens the codes are read once, past the caches (16 tokens, 28672 x 8192: 28.9 us, else 31.3); above
+      // that, other token tiles may read them again (64 tokens, 8192 x 8192, codes that the last cache still holds: 24.6
+      // us, past the caches 28.2; codes from HBM 30.2 and 29.0).
       p.c[a] = MT < 4 ? __builtin_nontemporal_load(c) : *c;
 #pragma unroll
       for (int g = 0; g < GT; ++g) {
@@ -267,10 +269,10 @@ void launch(const W4Call &c) {
 // Row tiles per workgroup: as many as still leave every compute unit a workgroup, since they share the
 // reads of x, which for 16 tokens are four times those of one row tile's codes.  Up to 32 tokens a wave takes
 // them, at most kMost, so that the scales and zero points on their way (kWords registers a tile) and the
-// sums fit the registers (16 tokens, 28672 x 8192: 30.2 us, with one row tile 42.8).  For
+// sums fit the registers (16 tokens, 28672 x 8192: 28.9 us, with one row tile 42.0).  For
 // more tokens the waves of a group take one each, two of them, so that two stages of each group fit the LDS, or
-// four (64 tokens through 28672 x 8192: 78 us, with two 102; through 8192 x 8192, 128 workgroups of four: 38
-// and 30).
+// four (64 tokens, codes from HBM: through 28672 x 8192 77 us, with two 102; through 8192 x 8192, 128 workgroups of
+// four, 42 and 30).
 template <int MT, int G, typename S, bool Z>
 void pick_tiles(const W4Call &c) {
   const int64_t row_tiles = (c.n + 15) / 16;

@@ -56,7 +56,7 @@ struct Args {
   int64_t q_ts, q_hs, o_ts, o_hs;
   float scale2;     // |scale| log2(e), 1 for a scale of 0
   uint32_t q_and, q_xor;  // see query()
-  int32_t num_items, q_heads, group, causal, window, num_tokens, num_part_rows;
+  int32_t q_heads, group, causal, window, num_tokens, num_part_rows;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -322,6 +322,7 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
         __builtin_amdgcn_wave_barrier();
       }
     }
+    // rounded for the product only, as in the tile items
     const bf16x8_t pf = __builtin_bit_cast(
         bf16x8_t, make_uint4(pack_bf16(p8[0], p8[1]), pack_bf16(p8[2], p8[3]), pack_bf16(p8[4], p8[5]), pack_bf16(p8[6], p8[7])));
     const int vr = 4 * fg + (fr >> 2);
@@ -410,10 +411,11 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(Args a) {
 // 64 positions, which go from the pages straight into LDS (16 bytes a lane, any page
 // per lane) while the tile before is multiplied.
 //
-// Bound by instruction issue: the matrix cores are busy for 40 % of the time and the vector units for 45 %, most of it
-// exponentials and the rounding of the weights.  A chunk of 4096 tokens over 16384 positions, 64 / 8 heads of
-// 128: 2.07 ms, 930 TFLOP/s; in items of 16 rows, each reading K and V for itself, 22.1 ms.  Heads
-// of 168 to 256 keep their sums in twice the registers, some of which spill.
+// The matrix cores are busy for 43 % of the time and the vector units for 46 %, most of it exponentials and the rounding of
+// the weights, and nearly in turn: two waves share a SIMD, and those of a workgroup leave every barrier in the same phase.
+// A chunk of 4096 tokens over 16384 positions, 64 / 8 heads of 128: 2.02 to 2.07 ms, 930 to 950 TFLOP/s; in items of 16
+// rows, each reading K and V for itself, 22.1 ms.  Heads above 128 leave a SIMD one wave, and those above 192 spill 78
+// registers a lane (2048 tokens over 8192, 32 / 8 heads: of 128 0.29 ms, of 192 0.54, of 256 0.70).
 constexpr int kTileWaves = 4;
 constexpr int kTilePos = 64;
 template <int DP>
@@ -616,6 +618,9 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
       }
     }
     if (active) {
+      // The weights are rounded to bf16 for this product, the sum takes them unrounded: out is 1.3 times as far from 64 bits
+      // as its own rounding alone leaves it (0.0023 and 0.0017 of it).  A second product with what the rounding leaves off
+      // would take as many matrix instructions again, and 0 * inf would make NaN of a kept infinite V.
       // O^T += V^T P^T: k-step ks holds positions 16 ks ..; this lane's half of P has 4 hf .. + 3 and 8 + 4 hf .. + 3
       const int li = lane & 15, vr = 4 * hf + (li >> 2);
       // The second block's weights are computed between the first block's products, which leave the vector
@@ -902,7 +907,6 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   const int dp = (kv->head_dim + 31) / 32 * 32;
   if (plan->num_row_items) {
     a.items = items;
-    a.num_items = plan->num_row_items;
     const unsigned grid = (unsigned)(plan->num_row_items * kv->kv_heads);
     if (dp <= 64) launch_rows<64>(a, grid, stream);
     else if (dp <= 96) launch_rows<96>(a, grid, stream);
@@ -912,7 +916,6 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   }
   if (plan->num_tile_items) {
     a.items = items + plan->num_row_items;
-    a.num_items = plan->num_tile_items;
     const unsigned grid = (unsigned)(plan->num_tile_items * kv->kv_heads);
     if (dp <= 64) launch_tiles<64>(a, grid, stream);
     else if (dp <= 96) launch_tiles<96>(a, grid, stream);
@@ -922,7 +925,6 @@ extern "C" lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan
   }
   if (plan->num_joins) {
     a.items = items + plan->num_row_items + plan->num_tile_items;
-    a.num_items = plan->num_joins;
     hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)(plan->num_joins * kv->kv_heads)), dim3(kJoinThreads), 0,
                        stream, a);
   }
