@@ -371,9 +371,12 @@ class ServingBlock:
         token_adapter names an adapter (or -1) for each of their rows: the delta takes bare addresses."""
         k, n = self.widths[name]
         self._rows(token_adapter, ("x", x, k), ("y", y, n))
-        B.lora_base_w4(x, self.base[name], y)
         with B._On(self.device, None):
-            B.lora_bgmv_fused(self.delta[name], token_adapter, x, y)
+            self._project(name, x, y, token_adapter)
+
+    def _project(self, name, x, y, token_adapter):
+        B.lora_base_w4(x, self.base[name], y)
+        B.lora_bgmv_fused(self.delta[name], token_adapter, x, y)
 
     def _rows(self, token_adapter, *named):
         """Checks (name, tensor, width) triples of rows and the adapter ids that go with them; returns their number."""
@@ -408,17 +411,19 @@ class ServingBlock:
         return self.run(hidden, plan, to(seq), to(pos), token_adapter)
 
     def run(self, hidden, plan, token_seq, token_pos, token_adapter):
-        """The device work of a step, launches only (every buffer is new; the plan and indices may serve many layers)."""
+        """The device work of a step, launches only (every buffer is new; the plan and indices may serve many layers).
+        Rows behind the plan's tokens are padding (token_seq -1, token_adapter -1): what stands in their y is unspecified."""
         torch = _torch()
-        t = hidden.shape[0]
+        t = self._rows(token_adapter, ("hidden", hidden, self.d_model))
         new = lambda n: torch.empty((t, n), dtype=torch.bfloat16, device=self.device)
-        q, k, v = (new(self.widths[n][1]) for n in "qkv")
-        for name, y in (("q", q), ("k", k), ("v", v)):
-            self.project(name, hidden, y, token_adapter)
         heads = lambda y, h: y.view(t, h, self.head_dim)
-        B.lora_kv_append(self.kv.view, heads(k, self.kv_heads), heads(v, self.kv_heads), token_seq, token_pos)
-        out = new(self.q_heads * self.head_dim)
-        B.lora_kv_attn(self.kv.view, plan, heads(q, self.q_heads), heads(out, self.q_heads))
-        y = new(self.d_model)
-        self.project("o", out, y, token_adapter)
+        with B._On(self.device, None):
+            q, k, v = (new(self.widths[n][1]) for n in "qkv")
+            for name, y in (("q", q), ("k", k), ("v", v)):
+                self._project(name, hidden, y, token_adapter)
+            B.lora_kv_append(self.kv.view, heads(k, self.kv_heads), heads(v, self.kv_heads), token_seq, token_pos)
+            out = new(self.q_heads * self.head_dim)
+            B.lora_kv_attn(self.kv.view, plan, heads(q, self.q_heads), heads(out, self.q_heads))
+            y = new(self.d_model)
+            self._project("o", out, y, token_adapter)
         return y

@@ -69,3 +69,11 @@ def test_a_step_of_no_tokens(block):
     y = block.step(rows(0), [0, 1], [0, 0], ids(0))
     assert y.shape == (0, 128) and block.calls == ["extend"]
     assert block.step(rows(0), [], [], ids(0)).shape == (0, 128)
+
+
+@pytest.mark.parametrize("hidden,adapters", [(rows(3), ids(4)), (rows(3), ids(3).long()), (rows(3).float(), ids(3)),
+                                             (rows(3, 256)[:, :128], ids(3)), (rows(3, 64), ids(3))])
+def test_a_refused_run_launches_nothing(block, hidden, adapters):
+    with pytest.raises(B.LoraError) as e:
+        block.run(hidden, None, ids(3), ids(3), adapters)
+    assert e.value.status == B.LORA_EINVAL and block.calls == []
