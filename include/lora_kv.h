@@ -228,8 +228,8 @@ lora_status lora_kv_get_stats(const lora_kv *kv, lora_kv_stats *stats);
 lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view);
 /* Waits for the work that its stream (that of its last call, which must still
  * exist) holds by now, gives every page back to the pool (which must still exist too) and
- * frees the object.  Pages whose work cannot be waited for -- the stream is in capture, or another
- * device than the pool's is current -- stay taken for good. */
+ * frees the object.  Pages whose work cannot be waited for (the stream is in capture, an
+ * error) stay taken for good.  The pool's device is current, as for every call here. */
 void lora_kv_destroy(lora_kv *kv);
 
 /* ------------------------------------------------------------------------ */

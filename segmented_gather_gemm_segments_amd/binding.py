@@ -1026,8 +1026,10 @@ def _kv_destroy(box: list):
     if not handle:
         return
     if device is not None:
-        cuda = _torch().cuda
-        cuda.synchronize(device)
+        cuda, st = _torch().cuda, lora_kv_stats()
+        _check(lib().lora_kv_get_stats(handle, ctypes.byref(st)))
+        if st.pages or st.spare:
+            cuda.synchronize(device)
         with cuda.device(device):
             lib().lora_kv_destroy(handle)
     else:
@@ -1052,10 +1054,8 @@ def _close_later(owner):
 
 
 def _close_waiting():
-    if _waiting and not _capturing():
-        todo, _waiting[:] = _waiting[:], []
-        for close in todo:
-            close()
+    while _waiting and not _capturing():
+        _waiting.pop()()
 
 
 class KvCache:
