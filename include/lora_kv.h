@@ -148,7 +148,8 @@ lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t *seq, const
  *   q, out     device bf16 [num_tokens][q_heads] rows of head_dim elements; token and head
  *              strides in elements, multiples of 8, >= 0 (out: rows must not overlap)
  *   lse        device fp32 [num_tokens][q_heads], or NULL
- *   scale      factor of the products, finite (the usual one is head_dim^-1/2)
+ *   scale      factor of the products, finite (the usual one is head_dim^-1/2); a row whose scores pass
+ *              2^127 in magnitude has unspecified results
  *   workspace  device, 16-byte aligned, at least plan->workspace_bytes (NULL with 0);
  *              contents on entry do not matter.  Calls that share it must not
  *              overlap, in graphs too.
