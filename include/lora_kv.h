@@ -6,7 +6,8 @@
  * intro paragraph).  Four parts, from the device up:
  *
  *   pages      lora_pages_copy, lora_page_table_remap: pages moved in one launch
- *   append     lora_kv_append: new tokens' K and V rows written through the page table
+ *   append     lora_kv_append: new tokens' K and V rows written through the page table, in 8 bits where
+ *              the cache holds those; lora_kv_read: rows read back
  *   attention  lora_kv_attn_plan, lora_kv_attn: new tokens (a prompt's chunk, or single decode
  *              tokens) attend to everything cached of their sequence
  *   sequences  lora_kv_*: host bookkeeping of which pages a sequence holds -- extend, fork
@@ -32,7 +33,7 @@ extern "C" {
  * them (the debug build records LORA_DEBUG_BAD_PAGE).  Any order of page,
  * head and token is described by the strides; rows must not overlap.        */
 typedef struct {
-  int32_t dtype;        /* LORA_BF16 */
+  int32_t dtype;        /* LORA_BF16, or LORA_FP8_E4M3 (lora_kv8_view below) */
   int32_t head_dim;     /* a multiple of 8, 8..256 */
   int32_t kv_heads;     /* >= 1 */
   int32_t page_tokens;  /* positions per page, >= 1 */
@@ -44,6 +45,26 @@ typedef struct {
   int64_t page_stride, head_stride, token_stride; /* elements, multiples of 8, >= 0 */
   const int32_t *page_table; /* device [num_seqs][max_pages] (NULL only where that is empty) */
 } lora_kv_view;
+
+/* A cache of 8-bit rows: half the bytes of a cache for twice the positions ("Multi-LoRA Inference Serving", the paragraphs
+ * on quantization, for the adapters' rows).  Every call that takes a lora_kv_view takes the
+ * first member of this one too: dtype LORA_FP8_E4M3 says that the rest follows it.
+ * A row x of head_dim elements, of one position, head and of K or V, is stored as codes c and an exponent e:
+ *     e = max(-117, the least e with max |x_i| <= 448 2^e),   c_i = x_i 2^-e rounded to nearest even in E4M3,
+ * and stands for c_i 2^e.  The maximum is over finite elements (e = -117 where it is 0); one that is not
+ * finite is stored as E4M3's NaN; magnitudes above 1.875 2^127 count as that, since 2^128 would not be finite.  A power
+ * of two costs no precision over any other factor but where codes are subnormal (below 2^-13
+ * of the row's largest), makes both directions exact, and every c 2^e a normal bf16 number or 0.
+ * In the view: head_dim a multiple of 16; k and v hold bytes, their strides (in elements, which are
+ * bytes) multiples of 16.  e + 127 of position p, head h is the byte at
+ *     k_scales + page * scale_page_stride + h * scale_head_stride + (p % page_tokens) * scale_token_stride
+ * and likewise in v_scales.                                                 */
+#define LORA_FP8_E4M3 2
+typedef struct {
+  lora_kv_view kv;      /* dtype LORA_FP8_E4M3 */
+  uint8_t *k_scales, *v_scales; /* device (NULL without pages) */
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride; /* bytes, >= 0 */
+} lora_kv8_view;
 
 /* ------------------------------------------------------------------------ */
 /* Copies page src[i] to page dst[i] of one storage, i < n, in one launch: the move
@@ -77,6 +98,13 @@ lora_status lora_page_table_remap(const int32_t *remap, int32_t num_pages, const
 lora_status lora_kv_append(const lora_kv_view *kv, const void *k_new, const void *v_new, int64_t new_token_stride,
                            int64_t new_head_stride, const int32_t *token_seq, const int32_t *token_pos,
                            int32_t num_tokens, hipStream_t stream);
+/* The other way: rows of listed positions copied out of the cache in bf16 (those of an 8-bit cache are exact),
+ * to hand a sequence over or to keep it elsewhere.  Arguments as for lora_kv_append, k_out and v_out
+ * written where it reads k_new and v_new (their rows must not overlap); a position may be listed twice.
+ * Where append would skip a token, and on an absent page, the rows of k_out and v_out are left as they are. */
+lora_status lora_kv_read(const lora_kv_view *kv, void *k_out, void *v_out, int64_t out_token_stride,
+                         int64_t out_head_stride, const int32_t *token_seq, const int32_t *token_pos, int32_t num_tokens,
+                         hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Attention of new tokens over the cache.  Request r of a batch has q_len[r] new
@@ -116,10 +144,12 @@ typedef struct {
 #define LORA_ATTN_TILE_ROWS 128
 #define LORA_ATTN_MAX_PARTS 64
 #define LORA_ATTN_CAUSAL 1
+#define LORA_ATTN_TREE 8     /* the plan is for lora_kv_attn_tree (lora_tree.h) */
+#define LORA_ATTN_BLOCKS 16  /* the plan is for lora_kv_attn_blocks (lora_blocks.h) */
 
 typedef struct {
   int32_t q_heads, kv_heads, head_dim;
-  int32_t flags;        /* LORA_ATTN_CAUSAL or 0 */
+  int32_t flags;        /* of LORA_ATTN_*; lora_kv_attn takes LORA_ATTN_CAUSAL or 0 */
   int32_t window;       /* 0: none */
   int32_t num_tokens;   /* new tokens of the batch (the last of q_starts) */
   int32_t num_row_items, num_tile_items, num_joins; /* items: row items, tile items, joins, in this order */
@@ -153,7 +183,7 @@ lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t *seq, const
  *   workspace  device, 16-byte aligned, at least plan->workspace_bytes (NULL with 0);
  *              contents on entry do not matter.  Calls that share it must not
  *              overlap, in graphs too.
- * Products of bf16 in fp32; maximum and sum of the softmax in fp32; its weights
+ * Products of bf16 in fp32 (an 8-bit cache's rows enter them exactly); maximum and sum of the softmax in fp32; its weights
  * are rounded to bf16 for their product with V (out is bf16), the sum is not;
  * out rounded once.  Bit-identical from run to run.  Device-side items are
  * checked against the plan and the view: a bad one is skipped (debug build:
@@ -170,7 +200,7 @@ lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, con
 /* ------------------------------------------------------------------------ */
 /* Sequences over a pool's pages (host bookkeeping).  The pool's pages of page_rows x
  * row_width elements hold page_tokens = page_rows * row_width / (2 kv_heads head_dim)
- * positions each: first K [kv_heads][page_tokens][head_dim], then V.  The pool may hold adapters
+ * positions each: first K [kv_heads][page_tokens][head_dim], then V (the flags below change both).  The pool may hold adapters
  * too (lora_cache): each page belongs to whoever took it.  A page that an eviction of a lora_cache
  * gave back may still be read on that cache's compute stream, and extend and compact take it
  * without asking: a pool's lora_cache and lora_kv use one stream, the cache's compute stream.
@@ -205,6 +235,10 @@ lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, con
  * On an error nothing is changed, except that LORA_EHIP leaves the device
  * contents unspecified.                                                     */
 #define LORA_KV_HOST_ONLY 1
+#define LORA_KV_FP8 4     /* flag: 8-bit rows.  A page holds K codes [kv_heads][page_tokens][head_dim], V codes, then the
+                             scale bytes of K [kv_heads][page_tokens] and of V; head_dim a multiple of 16 */
+#define LORA_KV_BOUNDS 8  /* flag: each page ends in the bounds of its keys (lora_blocks.h), which copies and moves of
+                             the page take along */
 typedef struct lora_kv lora_kv;
 typedef struct {
   int32_t seqs;        /* sequences in use */
@@ -225,8 +259,9 @@ lora_status lora_kv_trim(lora_kv *kv, int32_t wait, int32_t *left);
 /* *length = -1 for a sequence not in use; page_ids: capacity max_pages, or NULL. */
 lora_status lora_kv_seq(const lora_kv *kv, int32_t seq, int32_t *length, int32_t *page_ids, int32_t *num_pages);
 lora_status lora_kv_get_stats(const lora_kv *kv, lora_kv_stats *stats);
-/* The descriptor that append and attention take. */
+/* The descriptor that append and attention take (a cache made with LORA_KV_FP8: lora_kv_get_view8, else LORA_EINVAL). */
 lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view);
+lora_status lora_kv_get_view8(const lora_kv *kv, lora_kv8_view *view);
 /* Waits for the work that its stream (that of its last call, which must still
  * exist) holds by now, gives every page back to the pool (which must still exist too) and
  * frees the object.  Pages whose work cannot be waited for (the stream is in capture, an

@@ -9,6 +9,7 @@ module raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import sys
 from dataclasses import dataclass
@@ -19,7 +20,7 @@ import numpy as np
 from . import build as _build
 
 LORA_OK, LORA_EINVAL, LORA_ERANGE, LORA_EUNSUPPORTED, LORA_ENOMEM, LORA_EHIP = 0, -1, -2, -3, -4, -5
-LORA_F32, LORA_BF16 = 0, 1
+LORA_F32, LORA_BF16, LORA_FP8_E4M3 = 0, 1, 2
 LORA_WFMT_PLAIN, LORA_WFMT_FP8_E4M3, LORA_WFMT_INT4 = 0, 1, 2
 LORA_CACHE_HOST_ONLY = 1
 LORA_NO_ADAPTER = -1
@@ -37,7 +38,9 @@ LORA_SHRINK_TILE_TOKENS, LORA_SHRINK_TILE_K, LORA_SHRINK_TILE_ITEM_BYTES = 64, 6
 LORA_DEFAULT_TILE_MIN_TOKENS, LORA_TILE_MIN_RANK_SHORT, LORA_MAX_K_SPLITS = 16, 32, 64
 LORA_TILE_PAYS_BYTES = 24 << 20
 LORA_ATTN_ROWS, LORA_ATTN_TILE_ROWS, LORA_ATTN_MAX_PARTS, LORA_ATTN_CAUSAL = 16, 128, 64, 1
-LORA_KV_HOST_ONLY = 1
+LORA_ATTN_TREE, LORA_ATTN_BLOCKS = 8, 16
+LORA_KV_HOST_ONLY, LORA_KV_FP8, LORA_KV_BOUNDS = 1, 4, 8
+LORA_TREE_MAX_NODES, LORA_BLOCKS_MAX_PAGES, LORA_BLOCKS_MAX_COUNT = 4096, 32768, 4096
 
 
 class LoraError(RuntimeError):
@@ -81,6 +84,21 @@ class lora_kv_view(ctypes.Structure):
                                               "num_seqs", "max_pages", "reserved")] + \
                [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p)]
+
+
+class lora_kv8_view(ctypes.Structure):
+    _fields_ = [("kv", lora_kv_view), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64)]
+
+
+class lora_tree(ctypes.Structure):
+    _fields_ = [("mask", ctypes.c_void_p), ("depth", ctypes.c_void_p), ("words", ctypes.c_int32),
+                ("num_tokens", ctypes.c_int32)]
+
+
+class lora_kv_bounds(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class lora_attn_plan(ctypes.Structure):
@@ -139,8 +157,17 @@ EXPORTS = {
     "lora_pages_copy": ([_P, _I64, _I32, _P, _P, _I32, _P], _I32),
     "lora_page_table_remap": ([_P, _I32, _P, _P, _I64, _P], _I32),
     "lora_kv_append": ([_P, _P, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
+    "lora_kv_read": ([_P, _P, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
     "lora_kv_attn_plan": ([_P, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32], _I32),
     "lora_kv_attn": ([_P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P], _I32),
+    "lora_tree_mask": ([_P, _I32, _P, _I32, _P, _P], _I32),
+    "lora_kv_attn_tree": ([_P, _P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P], _I32),
+    "lora_kv_keep_path": ([_P, _P, _P, _P, _I32, _I32, _P], _I32),
+    "lora_kv_bounds_row_bytes": ([_I32, _P], _I32),
+    "lora_kv_bounds_update": ([_P, _P, _P, _P, _P, _I32, _I32, _P], _I32),
+    "lora_kv_block_select": ([_P, _P, _P, _P, _I32, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P], _I32),
+    "lora_kv_attn_blocks": ([_P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P],
+                            _I32),
     "lora_kv_create": ([_P, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "lora_kv_extend": ([_P, _P, _P, _I32, _P], _I32),
     "lora_kv_fork": ([_P, _I32, _P, _I32, _P], _I32),
@@ -151,6 +178,8 @@ EXPORTS = {
     "lora_kv_seq": ([_P, _I32, _P, _P, _P], _I32),
     "lora_kv_get_stats": ([_P, _P], _I32),
     "lora_kv_get_view": ([_P, _P], _I32),
+    "lora_kv_get_view8": ([_P, _P], _I32),
+    "lora_kv_get_bounds": ([_P, _P], _I32),
     "lora_kv_destroy": ([_P], None),
     "lora_kv_debug_flags": ([_P, _I32], _I32),
 }
@@ -836,23 +865,39 @@ def lora_base_w4(x, w: W4Weights, y, stream=None):
 
 
 class KvView:
-    """A paged KV cache as the kernels read it: k and v [num_pages, kv_heads, page_tokens, head_dim] bf16
-    tensors of the same strides (views of one storage, usually), page_table int32 [num_seqs, max_pages]."""
+    """A paged KV cache as the kernels read it: k and v [num_pages, kv_heads, page_tokens, head_dim] tensors of the same
+    strides (views of one storage, usually), page_table int32 [num_seqs, max_pages].  bf16, or of 8-bit rows:
+    float8_e4m3fn with k_scales and v_scales, uint8 [num_pages, kv_heads, page_tokens], the rows' exponents plus 127."""
 
-    def __init__(self, k, v, page_table):
+    def __init__(self, k, v, page_table, k_scales=None, v_scales=None):
         torch = _torch()
-        _tensors(k.device, ("k", k, torch.bfloat16), ("v", v, torch.bfloat16), ("page_table", page_table, torch.int32))
+        dtype = torch.bfloat16 if k_scales is None and v_scales is None else torch.float8_e4m3fn
+        _tensors(k.device, ("k", k, dtype), ("v", v, dtype), ("page_table", page_table, torch.int32))
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
             _refuse(f"k {tuple(k.shape)} {k.stride()} and v {tuple(v.shape)} {v.stride()} differ or are not 4-d")
         if page_table.dim() != 2:
             _refuse("page_table is [num_seqs, max_pages]")
         _flat("page_table", page_table)
         self.k, self.v, self.page_table = k, v, page_table
+        self.k_scales, self.v_scales = k_scales, v_scales
         pages, heads, tokens, dim = (int(n) for n in k.shape)
-        ps, hs, ts = (st if n > 1 else 0 for n, st in zip(k.shape[:3], k.stride()))
-        self.desc = lora_kv_view(LORA_BF16, dim, heads, tokens, pages, int(page_table.shape[0]), int(page_table.shape[1]),
-                                 0, _dptr(k), _dptr(v), ps, hs, ts, _dptr(page_table))
-        self.ref, self.index, self.device = ctypes.byref(self.desc), k.get_device(), k.device
+        strides = lambda t: (st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()))
+        fields = (dim, heads, tokens, pages, int(page_table.shape[0]), int(page_table.shape[1]), 0, _dptr(k), _dptr(v),
+                  *strides(k), _dptr(page_table))
+        if dtype is torch.bfloat16:
+            self.desc = lora_kv_view(LORA_BF16, *fields)
+            self.ref = ctypes.byref(self.desc)
+        else:
+            if k_scales is None or v_scales is None:
+                _refuse("8-bit rows need the scales of both k and v")
+            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                if t.dtype != torch.uint8 or t.device != k.device or t.shape != k.shape[:3]:
+                    _refuse(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}: uint8 {tuple(k.shape[:3])} on {k.device} wanted")
+            if k_scales.stride() != v_scales.stride():
+                _refuse(f"k_scales and v_scales have strides {k_scales.stride()} and {v_scales.stride()}")
+            self.desc8 = lora_kv8_view(lora_kv_view(LORA_FP8_E4M3, *fields), _dptr(k_scales), _dptr(v_scales), *strides(k_scales))
+            self.desc, self.ref = self.desc8.kv, ctypes.byref(self.desc8)
+        self.index, self.device = k.get_device(), k.device
         self.num_seqs, self.max_kv = self.desc.num_seqs, self.desc.max_pages * tokens
         self.bf16, self.int32, self.fp32 = torch.bfloat16, torch.int32, torch.float32
 
@@ -898,8 +943,10 @@ def _row_strides(t):
     return (a if n > 1 else 0, b if h > 1 else 0) if n else (0, 0)
 
 
-def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None):
-    """Writes k_new, v_new [T, kv_heads, head_dim] at positions token_pos [T] of sequences token_seq [T]."""
+def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None, *, _call="lora_kv_append",
+                   _names=("k_new", "v_new")):
+    """Writes k_new, v_new [T, kv_heads, head_dim] bf16 at positions token_pos [T] of sequences token_seq [T], quantised where
+    the cache holds 8-bit rows."""
     d, index, bf16, i32 = view.desc, view.index, view.bf16, view.int32
     n = k_new.shape[0]
     shape = (n, d.kv_heads, d.head_dim)
@@ -908,10 +955,10 @@ def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None
             token_pos.get_device() == index and k_new.shape == shape and v_new.shape == shape and
             token_seq.numel() == n and token_pos.numel() == n and token_seq.is_contiguous() and
             token_pos.is_contiguous() and (n == 0 or (k_new.stride(2) == 1 and v_new.stride(2) == 1))):
-        _tensors(view.device, ("k_new", k_new, bf16), ("v_new", v_new, bf16), ("token_seq", token_seq, i32),
+        _tensors(view.device, (_names[0], k_new, bf16), (_names[1], v_new, bf16), ("token_seq", token_seq, i32),
                  ("token_pos", token_pos, i32))
         if tuple(k_new.shape) != shape or tuple(v_new.shape) != shape or token_seq.numel() != n or token_pos.numel() != n:
-            _refuse(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}, {token_seq.numel()} sequences and "
+            _refuse(f"{_names[0]} {tuple(k_new.shape)}, {_names[1]} {tuple(v_new.shape)}, {token_seq.numel()} sequences and "
                     f"{token_pos.numel()} positions: {shape} wanted")
         _flat("token_seq", token_seq)
         _flat("token_pos", token_pos)
@@ -919,9 +966,13 @@ def lora_kv_append(view: KvView, k_new, v_new, token_seq, token_pos, stream=None
         _gpu(view.device)
     ts, hs = _row_strides(k_new)
     if _row_strides(v_new) != (ts, hs):
-        _refuse(f"k_new and v_new have strides {k_new.stride()} and {v_new.stride()}")
-    _launch("lora_kv_append", index, stream, view.ref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, token_seq.data_ptr(),
-            token_pos.data_ptr(), n)
+        _refuse(f"{_names[0]} and {_names[1]} have strides {k_new.stride()} and {v_new.stride()}")
+    _launch(_call, index, stream, view.ref, k_new.data_ptr(), v_new.data_ptr(), ts, hs, token_seq.data_ptr(), token_pos.data_ptr(), n)
+
+
+def lora_kv_read(view: KvView, token_seq, token_pos, k_out, v_out, stream=None):
+    """The rows of those positions in k_out, v_out [T, kv_heads, head_dim] bf16; rows of absent ones are left as they are."""
+    lora_kv_append(view, k_out, v_out, token_seq, token_pos, stream, _call="lora_kv_read", _names=("k_out", "v_out"))
 
 
 class AttnPlan:
@@ -952,15 +1003,19 @@ class AttnPlan:
 
 def lora_kv_attn_plan(q_starts, seqs, kv_lens, q_heads: int, kv_heads: int, head_dim: int, causal: bool = True,
                       window: int = 0, max_parts: int = 0, num_seqs: Optional[int] = None,
-                      max_kv: int = 2**31 - 1) -> AttnPlan:
+                      max_kv: int = 2**31 - 1, tree: bool = False, blocks: bool = False) -> AttnPlan:
     """Plan of a batch: request r has tokens q_starts[r] .. q_starts[r + 1] of q, sequence seqs[r] of kv_lens[r]
-    positions.  num_seqs, max_kv: the bounds to check against (lora_kv_attn checks the view's)."""
+    positions.  num_seqs, max_kv: the bounds to check against (lora_kv_attn checks the view's).  tree: for
+    lora_kv_attn_tree.  blocks: for lora_kv_attn_blocks, a request for each token, kv_lens of its list's pages (there is
+    no other mask then, `causal` says nothing)."""
     starts, sq, kv = _i32(q_starts), _i32(seqs), _i32(kv_lens)
     if starts.size < 1 or sq.size != starts.size - 1 or kv.size != sq.size:
         _refuse(f"{starts.size} starts, {sq.size} sequences and {kv.size} lengths")
     plan = lora_attn_plan()
     args = (_np_ptr(starts), _np_ptr(sq), _np_ptr(kv), sq.size, 2**31 - 1 if num_seqs is None else num_seqs, max_kv,
-            q_heads, kv_heads, head_dim, LORA_ATTN_CAUSAL if causal else 0, window, max_parts, ctypes.byref(plan))
+            q_heads, kv_heads, head_dim,
+            LORA_ATTN_BLOCKS | (LORA_ATTN_TREE if tree else 0) if blocks else
+            (LORA_ATTN_CAUSAL if causal else 0) | (LORA_ATTN_TREE if tree else 0), window, max_parts, ctypes.byref(plan))
     _check(lib().lora_kv_attn_plan(*args, None, 0))
     n = plan.num_row_items + plan.num_tile_items + plan.num_joins
     items = np.zeros((max(n, 1), 8), np.int32)
@@ -969,16 +1024,17 @@ def lora_kv_attn_plan(q_starts, seqs, kv_lens, q_heads: int, kv_heads: int, head
 
 
 def lora_kv_attn(view: KvView, plan: AttnPlan, q, out, lse=None, scale: Optional[float] = None, workspace=None,
-                 stream=None):
+                 stream=None, *, _call="lora_kv_attn", _mask=(), _max_kv=None):
     """out [T, q_heads, head_dim] (and lse [T, q_heads] fp32) of q over the cache; scale defaults to
     head_dim ** -0.5, workspace to the plan's own.  A plan that reaches past the view is refused (LORA_ERANGE); the debug
     library runs it, skips those items and records them."""
     items = plan.items
     if items is None:
         _refuse("the plan has not been uploaded: call plan.to(device)")
-    if (plan.num_seqs > view.num_seqs or plan.max_kv > view.max_kv) and not _debug:
+    max_kv = view.max_kv if _max_kv is None else _max_kv  # _mask: what another kind of mask has behind the items
+    if (plan.num_seqs > view.num_seqs or plan.max_kv > max_kv) and not _debug:
         raise LoraError(LORA_ERANGE, f"the plan reaches {plan.num_seqs} sequences of up to {plan.max_kv} positions, the "
-                                     f"view holds {view.num_seqs} of {view.max_kv}")
+                                     f"view holds {view.num_seqs} of {max_kv}")
     p, index, bf16, fp32 = plan.desc, view.index, view.bf16, view.fp32
     ws = plan.workspace if workspace is None else workspace
     heads, dim, tokens = p.q_heads, p.head_dim, p.num_tokens
@@ -1006,8 +1062,130 @@ def lora_kv_attn(view: KvView, plan: AttnPlan, q, out, lse=None, scale: Optional
     if index < 0:
         _gpu(view.device)
     qs, os_ = _row_strides(q), _row_strides(out)
-    _launch("lora_kv_attn", index, stream, view.ref, plan.ref, items.data_ptr(), q.data_ptr(), *qs, out.data_ptr(), *os_,
+    _launch(_call, index, stream, view.ref, plan.ref, items.data_ptr(), *_mask, q.data_ptr(), *qs, out.data_ptr(), *os_,
             lse_ptr, dim ** -0.5 if scale is None else scale, wp, wb)
+
+
+class Tree:
+    """What a tree's attention reads of the nodes of a batch: mask int64 [num_tokens, words], depth int32 [num_tokens].
+    max_nodes: the most that a request has."""
+
+    def __init__(self, num_tokens: int, max_nodes: int, device):
+        torch = _torch()
+        if not 0 <= max_nodes <= LORA_TREE_MAX_NODES:
+            raise LoraError(LORA_EUNSUPPORTED, f"a tree of {max_nodes} nodes, not up to {LORA_TREE_MAX_NODES}")
+        words = max(1, -(-max_nodes // 64))
+        self.mask = torch.empty((num_tokens, words), dtype=torch.int64, device=device)
+        self.depth = torch.empty(num_tokens, dtype=torch.int32, device=device)
+        self.desc = lora_tree(_dptr(self.mask), _dptr(self.depth), words, num_tokens)
+        self.ref, self.index, self.device = ctypes.byref(self.desc), self.mask.get_device(), self.mask.device
+
+
+def _i32s(device, *named):
+    """Checks (name, tensor) pairs: int32, contiguous, on the device."""
+    i32 = _torch().int32
+    for name, t in named:
+        if t.dtype is not i32 or t.device != device or not t.is_contiguous():
+            _tensors(device, (name, t, i32))
+            _flat(name, t)
+
+
+def lora_tree_mask(q_starts, parent, tree: Tree, window: int = 0, stream=None):
+    """Masks and depths of a batch's trees: q_starts int32 [num_reqs + 1] and parent int32 [num_tokens] on the device (a
+    parent's number within its request, -1 for the context)."""
+    _i32s(tree.device, ("q_starts", q_starts), ("parent", parent))
+    if q_starts.numel() < 1 or parent.numel() != tree.desc.num_tokens:
+        _refuse(f"{q_starts.numel()} starts and {parent.numel()} parents for a tree of {tree.desc.num_tokens} tokens")
+    if tree.index < 0:
+        _gpu(tree.device)
+    _launch("lora_tree_mask", tree.index, stream, q_starts.data_ptr(), q_starts.numel() - 1, parent.data_ptr(), window, tree.ref)
+
+
+def lora_kv_attn_tree(view: KvView, plan: AttnPlan, tree: Tree, q, out, lse=None, scale: Optional[float] = None,
+                      workspace=None, stream=None):
+    """lora_kv_attn for nodes of trees, with a plan made with tree=True."""
+    if tree.device != view.device:
+        _refuse(f"the tree is on {tree.device}, not {view.device}")
+    lora_kv_attn(view, plan, q, out, lse, scale, workspace, stream, _call="lora_kv_attn_tree", _mask=(tree.ref,))
+
+
+def lora_kv_keep_path(view: KvView, seq, base, path, stream=None):
+    """Moves the rows of accepted paths: path int32 [num_reqs, max_path] of ascending nodes, -1 behind the last, of trees
+    whose node 0 stands at position base [num_reqs] of sequence seq [num_reqs]."""
+    _i32s(view.device, ("seq", seq), ("base", base), ("path", path))
+    n = seq.numel()
+    if path.dim() != 2 or path.shape[0] != n or base.numel() != n:
+        _refuse(f"{n} sequences, {base.numel()} positions and paths {tuple(path.shape)}")
+    if view.index < 0:
+        _gpu(view.device)
+    _launch("lora_kv_keep_path", view.index, stream, view.ref, seq.data_ptr(), base.data_ptr(), path.data_ptr(), n, path.shape[1])
+
+
+def lora_kv_bounds_row_bytes(head_dim: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().lora_kv_bounds_row_bytes(head_dim, ctypes.byref(out)))
+    return int(out.value)
+
+
+class KvBounds:
+    """Bounds of the keys of a cache's pages: rows uint8 [num_pages, kv_heads, lora_kv_bounds_row_bytes(head_dim)]."""
+
+    def __init__(self, view: KvView, rows):
+        torch, d = _torch(), view.desc
+        _tensors(view.device, ("rows", rows, torch.uint8))
+        shape = (d.num_pages, d.kv_heads, lora_kv_bounds_row_bytes(d.head_dim))
+        if tuple(rows.shape) != shape:
+            _refuse(f"rows {tuple(rows.shape)}: {shape} wanted")
+        ps, hs = (st if n > 1 else 0 for n, st in zip(rows.shape[:2], rows.stride()))
+        self.rows, self.desc = rows, lora_kv_bounds(_dptr(rows), ps, hs)
+        self.ref, self.index = ctypes.byref(self.desc), rows.get_device()
+
+
+def lora_kv_bounds_update(view: KvView, bounds: KvBounds, seq, begin, end, max_tokens: int, stream=None):
+    """Bounds of the pages that hold positions begin[r] .. end[r] of sequence seq[r] (int32 [n]); max_tokens: the most
+    positions of a range."""
+    _i32s(view.device, ("seq", seq), ("begin", begin), ("end", end))
+    n = seq.numel()
+    if begin.numel() != n or end.numel() != n:
+        _refuse(f"{n} sequences, {begin.numel()} first and {end.numel()} last positions")
+    if bounds.index != view.index:
+        _refuse(f"bounds are on {bounds.rows.device}, not {view.device}")
+    if view.index < 0:
+        _gpu(view.device)
+    _launch("lora_kv_bounds_update", view.index, stream, view.ref, bounds.ref, seq.data_ptr(), begin.data_ptr(), end.data_ptr(), n,
+            max_tokens)
+
+
+def lora_kv_block_select(view: KvView, bounds: KvBounds, token_seq, token_pos, q, blocks, sink: int = 1, recent: int = 1,
+                         stream=None):
+    """The pages that token t, at position token_pos[t] of sequence token_seq[t] (int32 [T]), attends to, for each KV
+    head: blocks int32 [T, kv_heads, count], ascending, -1 behind the last.  q [T or more, q_heads, head_dim] bf16."""
+    d, n = view.desc, token_seq.numel()
+    _i32s(view.device, ("token_seq", token_seq), ("token_pos", token_pos), ("blocks", blocks))
+    _tensors(view.device, ("q", q, view.bf16))
+    if (token_pos.numel() != n or q.dim() != 3 or q.shape[0] < n or q.shape[2] != d.head_dim or blocks.dim() != 3 or
+            blocks.shape[0] < n or blocks.shape[1] != d.kv_heads):
+        _refuse(f"{n} sequences, {token_pos.numel()} positions, q {tuple(q.shape)} and blocks {tuple(blocks.shape)} for "
+                f"{d.kv_heads} KV heads of {d.head_dim}")
+    if bounds.index != view.index:
+        _refuse(f"bounds are on {bounds.rows.device}, not {view.device}")
+    if view.index < 0:
+        _gpu(view.device)
+    _launch("lora_kv_block_select", view.index, stream, view.ref, bounds.ref, token_seq.data_ptr(), token_pos.data_ptr(), n,
+            q.data_ptr(), *_row_strides(q), q.shape[1], blocks.shape[2], sink, recent, blocks.data_ptr())
+
+
+def lora_kv_attn_blocks(view: KvView, plan: AttnPlan, blocks, token_pos, q, out, lse=None, scale: Optional[float] = None,
+                        workspace=None, stream=None):
+    """lora_kv_attn over the pages that blocks [T, kv_heads, count] lists, up to token_pos [T], with a plan made with
+    blocks=True."""
+    d, n = view.desc, plan.desc.num_tokens
+    _i32s(view.device, ("blocks", blocks), ("token_pos", token_pos))
+    if blocks.dim() != 3 or blocks.shape[0] < n or blocks.shape[1] != d.kv_heads or token_pos.numel() < n:
+        _refuse(f"blocks {tuple(blocks.shape)} and {token_pos.numel()} positions: [{n} or more, {d.kv_heads}, pages] wanted")
+    count = blocks.shape[2]
+    lora_kv_attn(view, plan, q, out, lse, scale, workspace, stream, _call="lora_kv_attn_blocks",
+                 _mask=(blocks.data_ptr(), count, token_pos.data_ptr()), _max_kv=count * d.page_tokens)
 
 
 def _capturing() -> bool:
@@ -1061,16 +1239,19 @@ def _close_waiting():
 class KvCache:
     """lora_kv: sequences over the pages of a Pool (which may hold adapters too).  The pool's storage is a
     bf16 tensor [num_pages, page_rows, row_width]; the cache owns a device page table it makes itself.  All calls and the
-    kernels that read the pages use one stream, which is the compute stream of a Cache over the same pool."""
+    kernels that read the pages use one stream, which is the compute stream of a Cache over the same pool.  fp8: 8-bit rows;
+    bounds: each page holds the bounds of its keys too (`self.bounds`, a KvBounds)."""
 
-    def __init__(self, pool: Pool, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int, host_only: bool = False):
+    def __init__(self, pool: Pool, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int, host_only: bool = False,
+                 fp8: bool = False, bounds: bool = False):
         torch = _torch()
         _close_waiting()
         self.pool, self.max_pages, self._host_only = pool, max_pages, host_only
-        self.page_table = None
+        self.page_table = self.bounds = None
+        flags = (LORA_KV_FP8 if fp8 else 0) | (LORA_KV_BOUNDS if bounds else 0)
         h = ctypes.c_void_p()
         if host_only:
-            _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, None, LORA_KV_HOST_ONLY,
+            _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, None, LORA_KV_HOST_ONLY | flags,
                                         ctypes.byref(h)))
             self._own(h, None)
             return
@@ -1083,13 +1264,25 @@ class KvCache:
             # the table may be memory that work still queued on this stream uses, and lora_kv_create, which fills it,
             # knows nothing of the stream
             stream.synchronize()
-            _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, _dptr(self.page_table), 0,
+            _check(lib().lora_kv_create(pool._h, kv_heads, head_dim, max_seqs, max_pages, _dptr(self.page_table), flags,
                                         ctypes.byref(h)))
         self._own(h, dev)
         tokens, size = self.stats()["page_tokens"], kv_heads * head_dim
         flat = pool.storage.view(pool.storage.shape[0], -1)
-        part = lambda i: flat[:, i * size * tokens:(i + 1) * size * tokens].view(-1, kv_heads, tokens, head_dim)
-        self.view = KvView(part(0), part(1), self.page_table)
+        if fp8 or bounds:
+            bytes8 = flat.view(torch.uint8)
+        if fp8:
+            codes = bytes8.view(torch.float8_e4m3fn)
+            part = lambda t, i, *shape: t[:, i:i + math.prod(shape)].view(-1, *shape)
+            rows, n = (kv_heads, tokens, head_dim), kv_heads * tokens
+            self.view = KvView(part(codes, 0, *rows), part(codes, size * tokens, *rows), self.page_table,
+                               part(bytes8, 2 * size * tokens, kv_heads, tokens), part(bytes8, 2 * size * tokens + n, kv_heads, tokens))
+        else:
+            part = lambda i: flat[:, i * size * tokens:(i + 1) * size * tokens].view(-1, kv_heads, tokens, head_dim)
+            self.view = KvView(part(0), part(1), self.page_table)
+        if bounds:
+            row = lora_kv_bounds_row_bytes(head_dim)
+            self.bounds = KvBounds(self.view, bytes8[:, bytes8.shape[1] - kv_heads * row:].view(-1, kv_heads, row))
 
     def _own(self, handle, device):
         """The handle in a box that the pool knows too: whichever goes first, the cache is destroyed before the pool."""

@@ -23,11 +23,15 @@ SOURCES = [os.path.join(HERE, "csrc", "host.cpp"), os.path.join(HERE, "csrc", "k
            os.path.join(HERE, "csrc", "base_gemm.hip"), os.path.join(HERE, "csrc", "residency.hip"),
            os.path.join(HERE, "csrc", "probe.hip"), os.path.join(HERE, "csrc", "base_w4.hip"),
            os.path.join(HERE, "csrc", "kv_host.cpp"), os.path.join(HERE, "csrc", "kv_pages.hip"),
-           os.path.join(HERE, "csrc", "kv_attn.hip")]
+           *(os.path.join(HERE, "csrc", f"{n}.hip") for n in (
+               "kv_attn", "kv_attn_tree", "kv_attn_blocks", "kv_attn8", "kv_attn8_tree", "kv_attn8_blocks", "kv_tree",
+               "kv_blocks"))]
 HEADERS = [os.path.join(ROOT, "include", "lora_sgmv.h"), os.path.join(ROOT, "include", "lora_probe.h"),
            os.path.join(ROOT, "include", "lora_w4.h"), os.path.join(ROOT, "include", "lora_kv.h"),
+           os.path.join(ROOT, "include", "lora_tree.h"), os.path.join(ROOT, "include", "lora_blocks.h"),
            os.path.join(HERE, "csrc", "lora_internal.h"), os.path.join(HERE, "csrc", "kv_internal.h"),
-           os.path.join(HERE, "csrc", "kv_debug.h"), os.path.join(HERE, "csrc", "lds_load.h")]
+           os.path.join(HERE, "csrc", "kv_debug.h"), os.path.join(HERE, "csrc", "lds_load.h"),
+           *(os.path.join(HERE, "csrc", f"{n}.h") for n in ("kv_attn", "kv8", "kv_rows"))]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",

@@ -1,0 +1,7 @@
+// Attention's kernels for listed pages of 8-bit rows (kv_attn.h).
+#include "kv_attn.h"
+
+void lora::attn8_items_blocks(const AttnMoreArgs &a, const lora_attn_plan &plan, hipStream_t stream) {
+  launch_items<true, Mask::kBlocks>(a, plan, stream);
+}
+lora_status lora::kv_attn8_blocks_debug(uint32_t *flags, int32_t clear) { return kv_debug_word(flags, clear); }

@@ -29,7 +29,8 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 lora_status lora::check_view(const lora_kv_view *kv) {
   if (!kv) return fail(LORA_EINVAL, "null view");
-  if (kv->dtype != LORA_BF16) return fail(LORA_EUNSUPPORTED, "a KV cache holds bf16 (got dtype %d)", kv->dtype);
+  const bool f8 = kv->dtype == LORA_FP8_E4M3;
+  if (kv->dtype != LORA_BF16 && !f8) return fail(LORA_EUNSUPPORTED, "a KV cache holds bf16 or FP8 E4M3 (got dtype %d)", kv->dtype);
   if (kv->head_dim < 8 || kv->head_dim > 256 || kv->head_dim % 8)
     return fail(LORA_EUNSUPPORTED, "head_dim must be a multiple of 8 in 8..256 (got %d)", kv->head_dim);
   if (kv->kv_heads < 1 || kv->page_tokens < 1 || kv->num_pages < 0 || kv->num_seqs < 0 || kv->max_pages < 0)
@@ -45,6 +46,15 @@ lora_status lora::check_view(const lora_kv_view *kv) {
   if ((table && !kv->page_table) || (rows && (!kv->k || !kv->v))) return fail(LORA_EINVAL, "null KV pointer");
   if (((uintptr_t)kv->k & 15) || ((uintptr_t)kv->v & 15) || ((uintptr_t)kv->page_table & 3))
     return fail(LORA_EINVAL, "k and v must be 16-byte aligned");
+  if (f8) {
+    const lora_kv8_view *v = reinterpret_cast<const lora_kv8_view *>(kv);
+    if (kv->head_dim % 16) return fail(LORA_EUNSUPPORTED, "8-bit rows need a head_dim that is a multiple of 16 (got %d)", kv->head_dim);
+    if (kv->page_stride % 16 || kv->head_stride % 16 || kv->token_stride % 16)
+      return fail(LORA_EINVAL, "strides of 8-bit rows must be multiples of 16");
+    if (v->scale_page_stride < 0 || v->scale_head_stride < 0 || v->scale_token_stride < 0)
+      return fail(LORA_EINVAL, "negative stride of scales");
+    if (rows && (!v->k_scales || !v->v_scales)) return fail(LORA_EINVAL, "null scales");
+  }
   return LORA_OK;
 }
 
@@ -84,8 +94,10 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
     return fail(LORA_EINVAL, "%d query heads over %d KV heads", q_heads, kv_heads);
   if (head_dim < 8 || head_dim > 256 || head_dim % 8)
     return fail(LORA_EUNSUPPORTED, "head_dim must be a multiple of 8 in 8..256 (got %d)", head_dim);
-  if (flags & ~LORA_ATTN_CAUSAL) return fail(LORA_EINVAL, "unknown flags 0x%x", flags);
+  if (flags & ~(LORA_ATTN_CAUSAL | LORA_ATTN_TREE | LORA_ATTN_BLOCKS)) return fail(LORA_EINVAL, "unknown flags 0x%x", flags);
   if (window < 0) return fail(LORA_EINVAL, "negative window");
+  const bool listed = flags & LORA_ATTN_BLOCKS, tree = flags & LORA_ATTN_TREE;
+  if (listed && (flags != LORA_ATTN_BLOCKS || window)) return fail(LORA_EINVAL, "listed pages go with no other flag and no window");
   if (max_parts < 0 || max_parts > LORA_ATTN_MAX_PARTS)
     return fail(LORA_EINVAL, "max_parts %d outside 0..%d", max_parts, LORA_ATTN_MAX_PARTS);
   if (q_starts[0] != 0) return fail(LORA_EINVAL, "q_starts begins at %d", q_starts[0]);
@@ -97,6 +109,10 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
       return fail(LORA_ERANGE, "request %d has %d positions, its sequence holds %lld", r, kv_len[r], (long long)max_kv);
     if ((q_starts[r + 1] - q_starts[r]) * group > INT32_MAX)
       return fail(LORA_EUNSUPPORTED, "request %d has too many rows", r);
+    if (listed && q_starts[r + 1] - q_starts[r] > 1)
+      return fail(LORA_EINVAL, "request %d has %d tokens, listed pages go with one", r, q_starts[r + 1] - q_starts[r]);
+    if (tree && q_starts[r + 1] - q_starts[r] > LORA_TREE_MAX_NODES)
+      return fail(LORA_EUNSUPPORTED, "a tree of %d nodes", q_starts[r + 1] - q_starts[r]);
   }
   return guarded([&]() -> lora_status {
     std::vector<Tile> tiles[2];  // row items, tile items
@@ -112,13 +128,14 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
     for (int32_t r = 0; r < num_reqs; ++r) {
       const int32_t qn = q_starts[r + 1] - q_starts[r];
       const int64_t rows = qn * group, pos0 = (int64_t)kv_len[r] - qn;
-      const int kind = rows >= tile_min_rows;
+      const int kind = rows >= tile_min_rows && !listed;  // the query heads of one token: few rows
       const int64_t step = kind ? LORA_ATTN_TILE_ROWS : LORA_ATTN_ROWS;
       for (int64_t row0 = 0; row0 < rows; row0 += step) {
         const int64_t n = std::min(step, rows - row0);
         const int64_t first = pos0 + row0 / group, last = pos0 + (row0 + n - 1) / group;
         const int64_t end = (flags & LORA_ATTN_CAUSAL) ? std::min<int64_t>(kv_len[r], last + 1) : kv_len[r];
-        const int64_t begin = window > 0 ? std::max<int64_t>(0, first - window + 1) : 0;
+        // a node of a tree may be as low as the context's first successor
+        const int64_t begin = window > 0 ? std::max<int64_t>(0, (tree ? pos0 : first) - window + 1) : 0;
         Tile t{};
         t.it = {q_starts[r], (int32_t)row0, (int32_t)n, seq[r], (int32_t)pos0, (int32_t)begin,
                 (int32_t)std::max(begin, end), -1};
@@ -212,6 +229,7 @@ struct Spare {
 struct lora_kv {
   lora_pool *pool;
   int32_t kv_heads, head_dim, page_tokens, max_pages, flags;
+  int64_t bounds_at, bounds_row;  // with LORA_KV_BOUNDS: bytes from a page's start to its bounds, and of a head's
   int32_t *table;
   hipStream_t stream = nullptr;  // of the last call with device steps
   std::vector<Seq> seqs;
@@ -294,15 +312,21 @@ void drop(lora_kv *kv, int32_t page, std::vector<int32_t> &dropped) {
 extern "C" lora_status lora_kv_create(lora_pool *pool, int32_t kv_heads, int32_t head_dim, int32_t max_seqs,
                                       int32_t max_pages, int32_t *device_page_table, int32_t flags, lora_kv **out) {
   if (!pool || !out) return fail(LORA_EINVAL, "null argument");
-  if (flags & ~LORA_KV_HOST_ONLY) return fail(LORA_EINVAL, "unknown flags 0x%x", flags);
+  if (flags & ~(LORA_KV_HOST_ONLY | LORA_KV_FP8 | LORA_KV_BOUNDS)) return fail(LORA_EINVAL, "unknown flags 0x%x", flags);
   if (kv_heads < 1 || max_seqs < 1 || max_pages < 1)
     return fail(LORA_EINVAL, "%d KV heads, %d sequences of %d pages", kv_heads, max_seqs, max_pages);
   if (head_dim < 8 || head_dim > 256 || head_dim % 8)
     return fail(LORA_EUNSUPPORTED, "head_dim must be a multiple of 8 in 8..256 (got %d)", head_dim);
   if (pool->dtype != LORA_BF16 || pool->weight_format != LORA_WFMT_PLAIN)
     return fail(LORA_EUNSUPPORTED, "a KV cache needs a plain bf16 pool");
+  const bool f8 = flags & LORA_KV_FP8;
+  if (f8 && head_dim % 16) return fail(LORA_EUNSUPPORTED, "8-bit rows need a head_dim that is a multiple of 16 (got %d)", head_dim);
   const int64_t elems = (int64_t)pool->page_rows * pool->row_width;
-  const int64_t tokens = elems / (2 * (int64_t)kv_heads * head_dim);
+  int64_t bounds_row = 0;
+  if (flags & LORA_KV_BOUNDS) lora_kv_bounds_row_bytes(head_dim, &bounds_row);
+  const int64_t bounds_at = 2 * elems - kv_heads * bounds_row;
+  const int64_t position = 2 * (int64_t)kv_heads * (f8 ? head_dim + 1 : 2 * head_dim);  // bytes
+  const int64_t tokens = bounds_at < 0 ? 0 : bounds_at / position;
   if (tokens < 1 || elems % 8)
     return fail(LORA_EUNSUPPORTED, "a page of %lld elements for %d KV heads of %d", (long long)elems, kv_heads, head_dim);
   if (elems > kKvMaxPageBytes / 2) return fail(LORA_EUNSUPPORTED, "a page of %lld elements", (long long)elems);
@@ -318,6 +342,8 @@ extern "C" lora_status lora_kv_create(lora_pool *pool, int32_t kv_heads, int32_t
     kv->page_tokens = (int32_t)tokens;
     kv->max_pages = max_pages;
     kv->flags = flags;
+    kv->bounds_at = bounds_at;
+    kv->bounds_row = bounds_row;
     kv->table = device_page_table;
     kv->seqs.resize((size_t)max_seqs);
     kv->refs.assign((size_t)pool->num_pages, 0);
@@ -597,11 +623,11 @@ extern "C" lora_status lora_kv_get_stats(const lora_kv *kv, lora_kv_stats *out) 
   return ok();
 }
 
-extern "C" lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view) {
-  if (!kv || !view) return fail(LORA_EINVAL, "null argument");
-  if (kv->host_only()) return fail(LORA_EINVAL, "a host-only cache has no device view");
+// The view's part that 8-bit and bf16 caches have in common.
+static lora_kv_view view_of(const lora_kv *kv, bool f8) {
   lora_kv_view v{};
-  v.dtype = LORA_BF16;
+  const int64_t size = f8 ? 1 : 2;
+  v.dtype = f8 ? LORA_FP8_E4M3 : LORA_BF16;
   v.head_dim = kv->head_dim;
   v.kv_heads = kv->kv_heads;
   v.page_tokens = kv->page_tokens;
@@ -609,12 +635,53 @@ extern "C" lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view) {
   v.num_seqs = (int32_t)kv->seqs.size();
   v.max_pages = kv->max_pages;
   v.k = kv->pool->storage;
-  v.v = kv->pool->storage + (int64_t)kv->kv_heads * kv->page_tokens * kv->head_dim * 2;
-  v.page_stride = (int64_t)kv->pool->page_rows * kv->pool->row_width;
+  v.v = kv->pool->storage + (int64_t)kv->kv_heads * kv->page_tokens * kv->head_dim * size;
+  v.page_stride = (int64_t)kv->pool->page_rows * kv->pool->row_width * 2 / size;
   v.head_stride = (int64_t)kv->page_tokens * kv->head_dim;
   v.token_stride = kv->head_dim;
   v.page_table = kv->table;
+  return v;
+}
+
+extern "C" lora_status lora_kv_get_view(const lora_kv *kv, lora_kv_view *view) {
+  if (!kv || !view) return fail(LORA_EINVAL, "null argument");
+  if (kv->host_only()) return fail(LORA_EINVAL, "a host-only cache has no device view");
+  if (kv->flags & LORA_KV_FP8) return fail(LORA_EINVAL, "a cache of 8-bit rows has a lora_kv8_view");
+  *view = view_of(kv, false);
+  return ok();
+}
+
+extern "C" lora_status lora_kv_get_view8(const lora_kv *kv, lora_kv8_view *view) {
+  if (!kv || !view) return fail(LORA_EINVAL, "null argument");
+  if (kv->host_only()) return fail(LORA_EINVAL, "a host-only cache has no device view");
+  if (!(kv->flags & LORA_KV_FP8)) return fail(LORA_EINVAL, "a cache of bf16 rows has a lora_kv_view");
+  lora_kv8_view v{};
+  v.kv = view_of(kv, true);
+  const int64_t scales = (int64_t)kv->kv_heads * kv->page_tokens;
+  v.k_scales = (uint8_t *)kv->pool->storage + 2 * scales * kv->head_dim;
+  v.v_scales = v.k_scales + scales;
+  v.scale_page_stride = v.kv.page_stride;
+  v.scale_head_stride = kv->page_tokens;
+  v.scale_token_stride = 1;
   *view = v;
+  return ok();
+}
+
+extern "C" lora_status lora_kv_bounds_row_bytes(int32_t head_dim, int64_t *bytes) {
+  if (!bytes) return fail(LORA_EINVAL, "null argument");
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8)
+    return fail(LORA_EUNSUPPORTED, "head_dim must be a multiple of 8 in 8..256 (got %d)", head_dim);
+  *bytes = cdiv(2 * head_dim, 64) * 64 + 16;
+  return ok();
+}
+
+extern "C" lora_status lora_kv_get_bounds(const lora_kv *kv, lora_kv_bounds *bounds) {
+  if (!kv || !bounds) return fail(LORA_EINVAL, "null argument");
+  if (kv->host_only()) return fail(LORA_EINVAL, "a host-only cache has no device view");
+  if (!(kv->flags & LORA_KV_BOUNDS)) return fail(LORA_EINVAL, "a cache made without LORA_KV_BOUNDS");
+  bounds->rows = kv->pool->storage + kv->bounds_at;
+  bounds->page_stride = (int64_t)kv->pool->page_rows * kv->pool->row_width * 2;
+  bounds->head_stride = kv->bounds_row;
   return ok();
 }
 

@@ -1,5 +1,5 @@
 // Declarations shared by the files of the paged KV cache (kv_host.cpp,
-// kv_pages.hip, kv_attn.hip).  Not part of the public ABI.
+// kv_pages.hip, kv_tree.hip, kv_blocks.hip, kv_attn*.hip).  Not part of the public ABI.
 #pragma once
 
 #include <memory>
@@ -7,7 +7,9 @@
 #include <vector>
 
 #include "lora_internal.h"
+#include "lora_blocks.h"
 #include "lora_kv.h"
+#include "lora_tree.h"
 
 namespace lora {
 
@@ -32,7 +34,17 @@ lora_status kv_mark(hipStream_t stream, std::shared_ptr<void> *mark);
 bool kv_mark_done(const std::shared_ptr<void> &mark, bool wait);
 lora_status kv_not_capturing(hipStream_t stream);
 
-// The debug word of kv_attn.hip (lora_kv_debug_flags adds that of kv_pages.hip; 0 in release builds).
+// Checks a tree's sizes and pointers.
+lora_status check_tree(const lora_tree *tree);
+
+// The debug words of the other files (lora_kv_debug_flags adds that of kv_pages.hip; 0 in release builds).
 lora_status kv_attn_debug(uint32_t *flags, int32_t clear);
+lora_status kv_attn_tree_debug(uint32_t *flags, int32_t clear);
+lora_status kv_attn_blocks_debug(uint32_t *flags, int32_t clear);
+lora_status kv_attn8_debug(uint32_t *flags, int32_t clear);
+lora_status kv_attn8_tree_debug(uint32_t *flags, int32_t clear);
+lora_status kv_attn8_blocks_debug(uint32_t *flags, int32_t clear);
+lora_status kv_tree_debug(uint32_t *flags, int32_t clear);
+lora_status kv_blocks_debug(uint32_t *flags, int32_t clear);
 
 }  // namespace lora

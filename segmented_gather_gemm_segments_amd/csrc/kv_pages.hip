@@ -1,5 +1,5 @@
-// Paged KV cache: page copies, page-table rewrites and the append of new tokens'
-// rows (lora_kv.h), and the device steps of the sequence bookkeeping.
+// Paged KV cache: page copies, page-table rewrites, the append of new tokens'
+// rows and their way back (lora_kv.h), and the device steps of the sequence bookkeeping.
 //
 // All of it moves bytes, each read once and written once, in 16-byte units; HBM bounds
 // the large calls, the launch the small ones.
@@ -10,6 +10,8 @@
 
 #include "kv_internal.h"
 #include "kv_debug.h"
+#include "kv8.h"
+#include "kv_rows.h"
 
 using namespace lora;
 
@@ -81,19 +83,80 @@ __global__ __launch_bounds__(kThreads) void append_kernel(lora_kv_view kv, const
   const int chunks = kv.head_dim >> 3, per = chunks * kv.kv_heads;
   const int t = (int)(i / per), u = (int)(i % per);
   const int h = u / chunks, c = u % chunks;
-  const int s = token_seq[t], p = token_pos[t];
-  const bool in = s < kv.num_seqs && p >= 0 && p < kv.max_pages * kv.page_tokens;
-  KV_CHECK(in || s < 0, LORA_DEBUG_BAD_TOKEN);
-  if (s < 0 || !in) return;
-  const int page = kv.page_table[(int64_t)s * kv.max_pages + p / kv.page_tokens];
-  KV_CHECK((unsigned)page < (unsigned)kv.num_pages, LORA_DEBUG_BAD_PAGE);
-  if ((unsigned)page >= (unsigned)kv.num_pages) return;
-  const int64_t from = t * token_stride + h * head_stride + c * 8;
-  const int64_t to = page * kv.page_stride + h * kv.head_stride + (p % kv.page_tokens) * kv.token_stride + c * 8;
+  const Place place = place_of(kv, token_seq[t], token_pos[t]);
+  if (place.page < 0) return;
+  const int64_t from = t * token_stride + h * head_stride + c * 8, to = row_at(kv, place, h) + c * 8;
   const uint4 a = *reinterpret_cast<const uint4 *>(k_new + from);
   const uint4 b = *reinterpret_cast<const uint4 *>(v_new + from);
   *reinterpret_cast<uint4 *>((uint16_t *)kv.k + to) = a;
   *reinterpret_cast<uint4 *>((uint16_t *)kv.v + to) = b;
+}
+
+// Append to an 8-bit cache: P lanes, a power of two, per row (8 elements of K and of V each, those past head_dim idle), so
+// that the row's largest magnitude is an exchange between lanes and each row is read once.
+template <int P>
+__global__ __launch_bounds__(kThreads) void append8_kernel(lora_kv8_view v, const uint16_t *__restrict__ k_new,
+                                                           const uint16_t *__restrict__ v_new, int64_t token_stride,
+                                                           int64_t head_stride, const int32_t *__restrict__ token_seq,
+                                                           const int32_t *__restrict__ token_pos, uint32_t rows) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x, row = i / P, c = i % P;
+  if (row >= rows) return;  // whole groups of P lanes
+  const lora_kv_view &kv = v.kv;
+  const int t = (int)(row / (uint32_t)kv.kv_heads), h = (int)(row % (uint32_t)kv.kv_heads);
+  const Place to = place_of(kv, token_seq[t], token_pos[t]);
+  if (to.page < 0) return;  // all lanes of the row
+  const bool mine = c < (uint32_t)kv.head_dim / 8;
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (mine) {
+    const int64_t from = t * token_stride + h * head_stride + c * 8;
+    a = *reinterpret_cast<const uint4 *>(k_new + from);
+    b = *reinterpret_cast<const uint4 *>(v_new + from);
+  }
+  float ka = top8(a), va = top8(b);
+#pragma unroll
+  for (int x = 1; x < P; x <<= 1) {
+    ka = fmaxf(ka, __shfl_xor(ka, x));
+    va = fmaxf(va, __shfl_xor(va, x));
+  }
+  const int ke = row_exponent(ka), ve = row_exponent(va);
+  const int64_t at = row_at(kv, to, h) + c * 8;
+  if (mine) {
+    *reinterpret_cast<uint2 *>((uint8_t *)kv.k + at) = narrow8(a, exponent((uint32_t)(127 - ke)));
+    *reinterpret_cast<uint2 *>((uint8_t *)kv.v + at) = narrow8(b, exponent((uint32_t)(127 - ve)));
+  }
+  if (c == 0) {
+    const int64_t s = scale_at(v, to, h);
+    v.k_scales[s] = (uint8_t)(ke + 127);
+    v.v_scales[s] = (uint8_t)(ve + 127);
+  }
+}
+
+// Rows read back: a thread takes 8 elements of a K row and of the V row beside it.
+template <bool F8>
+__global__ __launch_bounds__(kThreads) void read_kernel(lora_kv8_view v, uint16_t *__restrict__ k_out,
+                                                        uint16_t *__restrict__ v_out, int64_t token_stride,
+                                                        int64_t head_stride, const int32_t *__restrict__ token_seq,
+                                                        const int32_t *__restrict__ token_pos, uint32_t units) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= units) return;
+  const lora_kv_view &kv = v.kv;
+  const uint32_t chunks = (uint32_t)kv.head_dim >> 3, row = i / chunks, c = i % chunks;
+  const int t = (int)(row / (uint32_t)kv.kv_heads), h = (int)(row % (uint32_t)kv.kv_heads);
+  const Place from = place_of(kv, token_seq[t], token_pos[t]);
+  if (from.page < 0) return;
+  const int64_t at = row_at(kv, from, h) + c * 8, to = t * token_stride + h * head_stride + c * 8;
+  uint4 a, b;
+  if constexpr (F8) {
+    const uint2 k = *reinterpret_cast<const uint2 *>((const uint8_t *)kv.k + at), w = *reinterpret_cast<const uint2 *>((const uint8_t *)kv.v + at);
+    const int64_t s = scale_at(v, from, h);
+    a = __builtin_bit_cast(uint4, widen8(k.x, k.y, exponent(v.k_scales[s])));
+    b = __builtin_bit_cast(uint4, widen8(w.x, w.y, exponent(v.v_scales[s])));
+  } else {
+    a = *reinterpret_cast<const uint4 *>((const uint16_t *)kv.k + at);
+    b = *reinterpret_cast<const uint4 *>((const uint16_t *)kv.v + at);
+  }
+  *reinterpret_cast<uint4 *>(k_out + to) = a;
+  *reinterpret_cast<uint4 *>(v_out + to) = b;
 }
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -185,7 +248,9 @@ extern "C" lora_status lora_kv_debug_flags(uint32_t *flags, int32_t clear) {
   *flags = 0;
 #if LORA_DEBUG
   lora_status st = kv_debug_word(flags, clear);
-  if (st == LORA_OK) st = kv_attn_debug(flags, clear);
+  for (const auto word : {kv_attn_debug, kv_attn_tree_debug, kv_attn_blocks_debug, kv_attn8_debug, kv_attn8_tree_debug,
+                          kv_attn8_blocks_debug, kv_tree_debug, kv_blocks_debug})
+    if (st == LORA_OK) st = word(flags, clear);
   return st == LORA_OK ? ok() : st;
 #else
   return fail(LORA_EUNSUPPORTED, "library built without LORA_DEBUG (load liblora_sgmv_debug.so)");
@@ -223,22 +288,62 @@ extern "C" lora_status lora_page_table_remap(const int32_t *remap, int32_t num_p
   return launched("page-table remap launch");
 }
 
-extern "C" lora_status lora_kv_append(const lora_kv_view *kv, const void *k_new, const void *v_new,
-                                      int64_t new_token_stride, int64_t new_head_stride, const int32_t *token_seq,
-                                      const int32_t *token_pos, int32_t num_tokens, hipStream_t stream) {
+// Checks the arguments of append and read; *none: there is nothing to do.
+static lora_status check_rows(const lora_kv_view *kv, const void *k_rows, const void *v_rows, int64_t token_stride,
+                              int64_t head_stride, const int32_t *token_seq, const int32_t *token_pos, int32_t num_tokens,
+                              bool *none) {
   lora_status st = check_view(kv);
   if (st != LORA_OK) return st;
   if (num_tokens < 0) return fail(LORA_EINVAL, "negative token count");
-  if (new_token_stride < 0 || new_head_stride < 0 || new_token_stride % 8 || new_head_stride % 8)
+  if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8)
     return fail(LORA_EINVAL, "strides of new rows must be multiples of 8 elements, not negative");
-  if (num_tokens == 0 || kv->num_pages == 0 || kv->num_seqs == 0 || kv->max_pages == 0) return ok();
-  if (!k_new || !v_new || !token_seq || !token_pos) return fail(LORA_EINVAL, "null pointer");
-  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(token_seq, 4) || !aligned(token_pos, 4))
+  if (num_tokens == 0 || kv->num_pages == 0 || kv->num_seqs == 0 || kv->max_pages == 0) {
+    *none = true;
+    return ok();
+  }
+  if (!k_rows || !v_rows || !token_seq || !token_pos) return fail(LORA_EINVAL, "null pointer");
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(token_seq, 4) || !aligned(token_pos, 4))
     return fail(LORA_EINVAL, "new rows must be 16-byte aligned");
+  *none = false;
+  return LORA_OK;
+}
+
+extern "C" lora_status lora_kv_append(const lora_kv_view *kv, const void *k_new, const void *v_new,
+                                      int64_t new_token_stride, int64_t new_head_stride, const int32_t *token_seq,
+                                      const int32_t *token_pos, int32_t num_tokens, hipStream_t stream) {
+  bool none;
+  lora_status st = check_rows(kv, k_new, v_new, new_token_stride, new_head_stride, token_seq, token_pos, num_tokens, &none);
+  if (st != LORA_OK || none) return st;
+  if (kv->dtype == LORA_FP8_E4M3) {
+    int lanes = 2;
+    while (lanes * 8 < kv->head_dim) lanes *= 2;
+    const int64_t rows = (int64_t)num_tokens * kv->kv_heads, groups = (rows * lanes + kThreads - 1) / kThreads;
+    if (rows > UINT32_MAX || too_many(groups, kThreads)) return fail(LORA_EUNSUPPORTED, "append too large");
+    const auto kernel = lanes == 2 ? append8_kernel<2> : lanes == 4 ? append8_kernel<4> : lanes == 8 ? append8_kernel<8>
+                        : lanes == 16 ? append8_kernel<16> : append8_kernel<32>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, view8(kv), (const uint16_t *)k_new,
+                       (const uint16_t *)v_new, new_token_stride, new_head_stride, token_seq, token_pos, (uint32_t)rows);
+    return launched("append launch");
+  }
   const int64_t units = (int64_t)num_tokens * kv->kv_heads * (kv->head_dim / 8);
   const int64_t blocks = (units + kThreads - 1) / kThreads;
   if (too_many(blocks, kThreads)) return fail(LORA_EUNSUPPORTED, "append too large");
   hipLaunchKernelGGL(append_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, *kv, (const uint16_t *)k_new,
                      (const uint16_t *)v_new, new_token_stride, new_head_stride, token_seq, token_pos, units);
   return launched("append launch");
+}
+
+extern "C" lora_status lora_kv_read(const lora_kv_view *kv, void *k_out, void *v_out, int64_t out_token_stride,
+                                    int64_t out_head_stride, const int32_t *token_seq, const int32_t *token_pos,
+                                    int32_t num_tokens, hipStream_t stream) {
+  bool none;
+  lora_status st = check_rows(kv, k_out, v_out, out_token_stride, out_head_stride, token_seq, token_pos, num_tokens, &none);
+  if (st != LORA_OK || none) return st;
+  const int64_t units = (int64_t)num_tokens * kv->kv_heads * (kv->head_dim / 8);
+  const int64_t groups = (units + kThreads - 1) / kThreads;
+  if (too_many(groups, kThreads)) return fail(LORA_EUNSUPPORTED, "read too large");
+  const auto kernel = kv->dtype == LORA_FP8_E4M3 ? read_kernel<true> : read_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, view8(kv), (uint16_t *)k_out,
+                     (uint16_t *)v_out, out_token_stride, out_head_stride, token_seq, token_pos, (uint32_t)units);
+  return launched("read launch");
 }

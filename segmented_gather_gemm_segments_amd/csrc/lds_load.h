@@ -37,8 +37,16 @@ __device__ __forceinline__ void load_lds16(const void *base, uint32_t off, uint3
                : "s"(to), "v"(off), "s"(base)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds_offset(const uint16_t *p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t *)p;
+// One byte a lane, lane l's to the 32 bits at byte `to` + 4 l.
+__device__ __forceinline__ void load_lds1(const void *from, uint32_t to) {
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %2, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(to), "v"(from)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_offset(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
 
 }  // namespace
