@@ -74,6 +74,7 @@ constexpr int64_t kAimUnits[2] = {512, 256};
 constexpr int64_t kMinRange[2] = {256, 512};
 constexpr int64_t kComputeUnits = 256;
 constexpr int32_t kTileKv = 64;  // range borders are multiples of this
+constexpr int64_t kTreeRowWork = 1 << 18;
 
 struct Tile {
   lora_attn_item it;
@@ -124,11 +125,22 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
     // 17 to 32 rows: one tile item reads K and V once, two row items twice (64 requests of 24 rows over 2048
     // positions, 8 KV heads: 96 us and 184); where units are few the row items' shorter steps count more (4
     // requests: 35 us and 24).  33 rows and more: 64 requests 100 us as tile items, 268 as row items.
+    // A tree of a few requests has few rows, but more than two row items' worth.  Row items read K and V for every 16 rows
+    // and come sooner to their end: they are taken while there are two for each compute unit at most that read no more
+    // than kTreeRowWork positions in all (a tree of 26 over 700, 32 / 8 heads of 128: 16.5 us, as tile items 24; of 61 over
+    // 700, 64 / 8 heads: 20 and 28; of 130 over 3000, 32 / 8: 86 and 40; 32 of 26 over 100: 35 and 16).
+    int64_t row_units = 0, row_work = 0;
+    for (int32_t r = 0; tree && r < num_reqs; ++r) {
+      const int64_t n = q_starts[r + 1] - q_starts[r], units = cdiv(n * group, LORA_ATTN_ROWS) * kv_heads;
+      row_units += units;
+      row_work += units * (window > 0 ? std::min<int64_t>(kv_len[r], window + n) : kv_len[r]);
+    }
+    const bool few = tree && row_units <= 2 * kComputeUnits && row_work <= kTreeRowWork;
     const int64_t tile_min_rows = (medium >= kComputeUnits ? 1 : 2) * LORA_ATTN_ROWS + 1;
     for (int32_t r = 0; r < num_reqs; ++r) {
       const int32_t qn = q_starts[r + 1] - q_starts[r];
       const int64_t rows = qn * group, pos0 = (int64_t)kv_len[r] - qn;
-      const int kind = rows >= tile_min_rows && !listed;  // the query heads of one token: few rows
+      const int kind = rows >= tile_min_rows && !few && !listed;  // listed pages: the query heads of one token, few rows
       const int64_t step = kind ? LORA_ATTN_TILE_ROWS : LORA_ATTN_ROWS;
       for (int64_t row0 = 0; row0 < rows; row0 += step) {
         const int64_t n = std::min(step, rows - row0);
@@ -152,12 +164,17 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
         work += t.span * kv_heads;
         widest = std::max(widest, t.span);
       }
+      // Tile items of trees whose contexts differ aim at twice the units too (16 trees of 26 over 2000 to 8000, 64 / 8
+      // heads: 140 us, else 217; one of 61 over 8000: 47, with twice the units 52).
+      const bool uneven = tree && widest * (int64_t)tiles[kind].size() * kv_heads > work * 3 / 2;
       // positions per range: an even share of the work for each unit aimed at
       auto even = [&](int64_t units) { return cdiv(cdiv(work, units), kTileKv) * kTileKv; };
-      int64_t share = even(kAimUnits[kind]);
+      int64_t share = even(kind == 1 && uneven ? 2 * kAimUnits[1] : kAimUnits[kind]);
       // Row items of uneven spans aim at twice the units, which the device takes longest first (64 / 8 heads of 128, 64
       // tokens over 256 to 8192 positions: 250 us, else 275).
-      if (kind == 0 && widest > share * 3 / 2) share = even(2 * kAimUnits[0]);
+      if (kind == 0 && !few && widest > share * 3 / 2) share = even(2 * kAimUnits[0]);
+      // those are cut while that leaves each compute unit one at most (4 trees of 26 over 175 to 700: 20 us uncut, 30 cut)
+      if (kind == 0 && few) share = 2 * (int64_t)tiles[0].size() * kv_heads > kComputeUnits ? widest : even(kComputeUnits);
       share = std::max(kMinRange[kind], share);
       std::vector<Tile> ranges;
       for (const Tile &t : tiles[kind]) {
