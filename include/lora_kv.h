@@ -190,7 +190,7 @@ lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t *seq, const
  * LORA_DEBUG_BAD_ITEM), and the join of ranges that reach past the view with them, so
  * that a plan made for a larger view leaves those rows of out and lse as they are.
  * Rows of out and lse beyond num_tokens are left as they are.
- * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (dtype, head_dim, strides of 2^35 elements,
+ * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (dtype, head_dim, strides of 2^35 elements, of scales 2^32,
  * 2^24 items of all KV heads and more), LORA_EHIP.                          */
 lora_status lora_kv_attn(const lora_kv_view *kv, const lora_attn_plan *plan, const lora_attn_item *items, const void *q,
                          int64_t q_token_stride, int64_t q_head_stride, void *out, int64_t out_token_stride,

@@ -57,7 +57,8 @@ struct AttnArgs {
 // What 8-bit rows and the other masks add; kernels that need none of it are not handed it.
 struct AttnMoreArgs : AttnArgs {
   const uint8_t *k_scales, *v_scales;
-  int64_t scale_ps, scale_hs, scale_ts;
+  int64_t scale_hs;
+  uint32_t scale_ps, scale_ts;
   const uint64_t *tree_mask;  // [num_tokens][tree_words]
   const int32_t *tree_depth;
   const int32_t *blocks;      // [num_tokens][kv_heads][count]
@@ -114,6 +115,11 @@ __device__ __forceinline__ float sum_groups(float v) {
   v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// From a head's first exponent byte to that of a position.
+__device__ __forceinline__ uint64_t scale_at(const AttnMoreArgs &a, int page, int slot) {
+  return (uint64_t)(uint32_t)page * a.scale_ps + (uint64_t)(uint32_t)slot * a.scale_ts;
 }
 
 // Bits j0 .. j0 + 63 of a tree's mask row; those below 0 and behind its words are 0.
@@ -286,6 +292,8 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
     return M == Mask::kBlocks ? 0 : table[inside(p) ? a.page_div((int)p) : 0];
   };
   const char *kh = (const char *)kv.k + h * kv.head_stride * (F8 ? 1 : 2), *vh = (const char *)kv.v + h * kv.head_stride * (F8 ? 1 : 2);
+  const uint8_t *eh = nullptr;  // lanes 0 .. 31 fetch K's exponents, the others V's
+  if constexpr (F8) eh = (lane < 32 ? a.k_scales : a.v_scales) + h * a.scale_hs;
   auto issue = [&](auto bufc, int tile, int page) -> uint32_t {
     const int p = first + tile * kRowPos + (lane & 31), off = p - a.page_div(p) * kv.page_tokens;
     bool ok = inside(p);
@@ -304,8 +312,7 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
     const uint32_t kb = lds_offset(&lds[decltype(bufc)::value][wave * kStage]);
     load_tile<L, LOADS, 1, 32, FULL>(kh, vh, ok ? at : -1, exist, 0, nch, kb, kb + kTile);
     if constexpr (F8) {
-      const uint8_t *e = (lane < 32 ? a.k_scales : a.v_scales) + h * a.scale_hs + page * a.scale_ps + off * a.scale_ts;
-      load_lds1(pick(ok, e), kb + 2 * kTile);
+      load_lds1(pick(ok, eh + scale_at(a, page, off)), kb + 2 * kTile);
     }
     return (uint32_t)exist;
   };
@@ -639,6 +646,11 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
   constexpr int kLoads8 = F8 ? kTilePos * L8::kCpr / 64 / kTileWaves : 1;
   uint4 raw[2][kLoads8];
   uint32_t exps[2] = {0, 0};  // of the tile's position `lane`
+  const uint8_t *keh = nullptr, *veh = nullptr;
+  if constexpr (F8) {
+    keh = a.k_scales + h * a.scale_hs;
+    veh = a.v_scales + h * a.scale_hs;
+  }
   auto issue = [&](auto bufc, int tile, int page) -> uint64_t {
     constexpr int BUF = decltype(bufc)::value;
     const int p = first + tile * kTilePos + lane;
@@ -647,16 +659,28 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
     const int64_t at = (uint64_t)(uint32_t)page * a.page16 + (uint64_t)(uint32_t)(p - a.page_div(p) * kv.page_tokens) * a.token16;
     const uint64_t there = __ballot(ok);  // bit i: the tile's position i exists
     if constexpr (F8) {
-      const int64_t e = h * a.scale_hs + page * a.scale_ps + (p - a.page_div(p) * kv.page_tokens) * a.scale_ts;
-      exps[0] = *(const uint8_t *)pick(ok, a.k_scales + e);
-      exps[1] = *(const uint8_t *)pick(ok, a.v_scales + e);
+      const uint64_t e = scale_at(a, page, p - a.page_div(p) * kv.page_tokens);
+      if (FULL && there == ~0ull) {
+        exps[0] = keh[e];
+        exps[1] = veh[e];
 #pragma unroll
-      for (int i = 0; i < kLoads8; ++i) {
-        const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L8::kCpr, ch = c % L8::kCpr;
-        const int64_t ra = shfl64(ok ? at : -1, r);
-        const bool there8 = ra >= 0 && (FULL || ch < D >> 4);
-        raw[0][i] = *reinterpret_cast<const uint4 *>(pick(there8, kh + ch * 16 + (ra << 4)));
-        raw[1][i] = *reinterpret_cast<const uint4 *>(pick(there8, vh + ch * 16 + (ra << 4)));
+        for (int i = 0; i < kLoads8; ++i) {
+          const int c = 64 * (kTileWaves * i + wave) + lane, ch = c % L8::kCpr;
+          const int64_t ra = shfl64(at, c / L8::kCpr) << 4;
+          raw[0][i] = *reinterpret_cast<const uint4 *>(kh + ch * 16 + ra);
+          raw[1][i] = *reinterpret_cast<const uint4 *>(vh + ch * 16 + ra);
+        }
+      } else {
+        exps[0] = *(const uint8_t *)pick(ok, keh + e);
+        exps[1] = *(const uint8_t *)pick(ok, veh + e);
+#pragma unroll
+        for (int i = 0; i < kLoads8; ++i) {
+          const int c = 64 * (kTileWaves * i + wave) + lane, ch = c % L8::kCpr;
+          const int64_t ra = shfl64(ok ? at : -1, c / L8::kCpr);
+          const bool here = ra >= 0 && ch < D >> 4;
+          raw[0][i] = *reinterpret_cast<const uint4 *>(pick(here, kh + ch * 16 + (ra << 4)));
+          raw[1][i] = *reinterpret_cast<const uint4 *>(pick(here, vh + ch * 16 + (ra << 4)));
+        }
       }
     } else {
       load_tile<L, L::kLoads, kTileWaves, 64, FULL>(kh, vh, ok ? at : -1, there, 64 * wave, nch,
@@ -665,21 +689,24 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
     }
     return there;
   };
-  // the rows in registers into a stage
-  auto widen = [&](auto bufc) {
-    constexpr int BUF = decltype(bufc)::value;
-    uint16_t *kb = (BUF ? sk1 : sk0) + group * kStage, *vb = (BUF ? sv1 : sv0) + group * kStage;
-#pragma unroll
-    for (int i = 0; i < kLoads8; ++i) {
-      const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L8::kCpr, ch = c % L8::kCpr;
-      const float ks = exponent(__shfl(exps[0], r)), vs = exponent(__shfl(exps[1], r));
-      const uint4 k = raw[0][i], v = raw[1][i];
-      *reinterpret_cast<bf16x8_t *>(kb + r * DP + L::k_slot(r, 2 * ch) * 8) = widen8(k.x, k.y, ks);
-      *reinterpret_cast<bf16x8_t *>(kb + r * DP + L::k_slot(r, 2 * ch + 1) * 8) = widen8(k.z, k.w, ks);
-      *reinterpret_cast<bf16x8_t *>(vb + r * DP + L::v_slot(r, 2 * ch) * 8) = widen8(v.x, v.y, vs);
-      *reinterpret_cast<bf16x8_t *>(vb + r * DP + L::v_slot(r, 2 * ch + 1) * 8) = widen8(v.z, v.w, vs);
-    }
+  // the rows in registers into a stage, in pieces of 8 codes a lane.  Where a row's chunks divide the lanes, a lane's places
+  // of the next load are the first one's some rows further on, and the layouts repeat after 16.
+  auto place = [&](int i, int is_v, int half) {
+    const int c = 64 * (kTileWaves * i + wave) + lane, r = c / L8::kCpr, ch = 2 * (c % L8::kCpr) + half;
+    return r * DP + (is_v ? L::v_slot(r, ch) : L::k_slot(r, ch)) * 8;
   };
+  constexpr int kMoreRows = 64 * kTileWaves / L8::kCpr;
+  constexpr bool kRegular = 64 * kTileWaves % L8::kCpr == 0 && (kLoads8 == 1 || kMoreRows % 16 == 0);
+  const int places[2][2] = {{place(0, 0, 0), place(0, 0, 1)}, {place(0, 1, 0), place(0, 1, 1)}};
+  auto widen = [&](auto bufc, int piece) {
+    constexpr int BUF = decltype(bufc)::value;
+    const int i = piece / 4, half = piece % 2, is_v = piece / 2 % 2;  // K's and V's pieces of each load in turn
+    uint16_t *to = (is_v ? (BUF ? sv1 : sv0) : (BUF ? sk1 : sk0)) + group * kStage + (kRegular ? places[is_v][half] + i * kMoreRows * DP : place(i, is_v, half));
+    const uint4 u = raw[is_v][i];
+    const float e = exponent(__shfl(exps[is_v], (64 * (kTileWaves * i + wave) + lane) / L8::kCpr));
+    *reinterpret_cast<bf16x8_t *>(to) = widen8(half ? u.z : u.x, half ? u.w : u.y, e);
+  };
+  constexpr int kPieces = 4 * kLoads8;
   int page = tiles > 0 ? lookup(group) : -1;
 
   // this lane's row (a row past the item's computes the item's first one and is not stored)
@@ -725,17 +752,9 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
     if constexpr (!F8) wait_vm<0>();  // this wave's loads of the tile have landed
     __syncthreads();                  // everybody's have, and nobody reads the other stage any more
     if constexpr (GR > 1) whole = (masked[BUF][0] | masked[BUF][GR - 1]) == 0;  // the groups mask together: there are barriers
-    if constexpr (F8) {
-      if (tile + GR < tiles) {
-        widen(std::integral_constant<int, 1 - BUF>{});
-        exist[1 - BUF] = ahead;
-      }
-      if (tile + 2 * GR < tiles) {
-        ahead = issue(bufc, tile + 2 * GR, page);
-        page = lookup(tile + 3 * GR);
-      }
-    } else if (tile + GR < tiles) {
-      exist[1 - BUF] = issue(std::integral_constant<int, 1 - BUF>{}, tile + GR, page);
+    const std::integral_constant<int, 1 - BUF> other{};
+    if (!F8 && tile + GR < tiles) {
+      exist[1 - BUF] = issue(other, tile + GR, page);
       page = lookup(tile + 2 * GR);
     }
     // element i of block b is position t0 + 32 b + 8 (i / 4) + 4 hf + i % 4
@@ -753,7 +772,23 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
           },
           [&](int n, uint4 kf) {
             s[n % SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf), qf[n / SB], s[n % SB], 0, 0, 0);
+            // 8-bit: the next tile (behind the last, whatever the registers hold, which nobody reads) is widened while the
+            // matrix instructions leave the vector units free
+            static_assert(!F8 || SB * KS == 2 * kPieces);
+            if (F8 && n % 2 == 0) widen(other, n / 2);
           });
+    } else if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) widen(other, i);
+    }
+    if constexpr (F8) {
+      exist[1 - BUF] = ahead;
+      if (tile + 2 * GR < tiles) {
+        ahead = issue(other, tile + 2 * GR, page);
+        page = lookup(tile + 3 * GR);
+      }
+    }
+    if (active) {
       if (!whole) {
         keep = 0;
         uint64_t nodes = 0;  // drafted nodes that this row keeps, once the tile reaches them
@@ -885,7 +920,8 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
     exist[0] = issue(std::integral_constant<int, 0>{}, group, page);
     page = lookup(group + GR);
     if constexpr (F8) {
-      widen(std::integral_constant<int, 0>{});
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) widen(std::integral_constant<int, 0>{}, i);
       if (group + GR < tiles) {
         ahead = issue(std::integral_constant<int, 0>{}, group + GR, page);
         page = lookup(group + 2 * GR);

@@ -160,11 +160,13 @@ lora_status run(const Call &c, Mask mask, AttnMoreArgs a) {
   a.token16 = (uint32_t)(kv->token_stride / unit);
   if (f8) {
     const lora_kv8_view *kv8 = reinterpret_cast<const lora_kv8_view *>(kv);
+    if (kv8->scale_page_stride > UINT32_MAX || kv8->scale_token_stride > UINT32_MAX)
+      return fail(LORA_EUNSUPPORTED, "strides of scales of 2^32 bytes and more");
     a.k_scales = kv8->k_scales;
     a.v_scales = kv8->v_scales;
-    a.scale_ps = kv8->scale_page_stride;
+    a.scale_ps = (uint32_t)kv8->scale_page_stride;
     a.scale_hs = kv8->scale_head_stride;
-    a.scale_ts = kv8->scale_token_stride;
+    a.scale_ts = (uint32_t)kv8->scale_token_stride;
   }
   a.scale2 = c.scale == 0.f ? 1.f : std::fabs(c.scale) * kLog2e;
   a.q_and = c.scale == 0.f ? 0u : ~0u;
