@@ -55,38 +55,31 @@ __global__ __launch_bounds__(kThreads) void tree_mask_kernel(const int32_t *__re
 // A thread moves one piece (16 bytes of a row, or a scale byte) of every row of its request's path, in the path's order.
 // Entries ascend, so path[i] >= i: what position base + i receives is never read later, only by copies before it, and
 // pieces of kAhead entries may be read before the first of them is written.
-constexpr int kAhead = 8;
+//
+// A wave looks up 64 entries' places side by side (path, then two page ids: a chain of two loads for
+// all of them) into LDS.
+constexpr int kAhead = 8;  // divides 64
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
+__device__ const u32x4_t g_zeros = {0, 0, 0, 0};
+
+// Pieces of entries [0, n) of up to 64; to[j].page < 0: not copied (and zeros read, so that no load waits for a branch).
 template <typename T>
-__device__ __forceinline__ void move_piece(const lora_kv_view &kv, int s, int base, const int32_t *path, int max_path, T *store,
-                                           int64_t page_stride, int64_t token_stride) {
-  int before = -1;
-  for (int i0 = 0; i0 < max_path; i0 += kAhead) {
+__device__ __forceinline__ void move_pieces(T *store, int64_t page_stride, int64_t token_stride, const Place *from,
+                                            const Place *to, int n) {
+  for (int j0 = 0; j0 < n; j0 += kAhead) {
     T piece[kAhead];
-    int64_t to[kAhead];
-    bool more = true;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int e = more && i0 + j < max_path ? path[i0 + j] : -1;
-      KV_CHECK(e < 0 || e > before, LORA_DEBUG_BAD_TOKEN);
-      more = e > before && e >= 0;
-      to[j] = -1;
-      if (more) {
-        before = e;
-        const int64_t src = (int64_t)base + e, dst = (int64_t)base + i0 + j;
-        if (src != dst) {
-          const Place a = place_of(kv, s, (int)min(src, (int64_t)INT32_MAX)), b = place_of(kv, s, (int)min(dst, (int64_t)INT32_MAX));
-          if (a.page >= 0 && b.page >= 0) {
-            piece[j] = store[a.page * page_stride + a.slot * token_stride];
-            to[j] = b.page * page_stride + b.slot * token_stride;
-          }
-        }
-      }
+      const Place x = from[j0 + j];
+      const T *at = store + (x.page * page_stride + x.slot * token_stride);
+      piece[j] = *(j0 + j < n && to[j0 + j].page >= 0 ? at : reinterpret_cast<const T *>(&g_zeros));
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (to[j] >= 0) store[to[j]] = piece[j];
-    if (!more) return;
+    for (int j = 0; j < kAhead; ++j) {
+      const Place x = to[j0 + j];
+      if (j0 + j < n && x.page >= 0) store[x.page * page_stride + x.slot * token_stride] = piece[j];
+    }
   }
 }
 
@@ -94,22 +87,45 @@ __global__ __launch_bounds__(kThreads) void keep_path_kernel(lora_kv8_view v, co
                                                              const int32_t *__restrict__ bases,
                                                              const int32_t *__restrict__ path, int max_path, int chunks,
                                                              int size, int units, int groups) {
+  __shared__ Place from[64], to[64];
+  __shared__ int count, last;
   const lora_kv_view &kv = v.kv;
   const int r = blockIdx.x / groups, u = (int)(blockIdx.x % groups) * kThreads + (int)threadIdx.x;
-  if (u >= units) return;
-  const int s = seq[r], base = bases[r];
+  const int s = seq[r], base = bases[r], lane = threadIdx.x;
   KV_CHECK(s < kv.num_seqs && (s < 0 || base >= 0), LORA_DEBUG_BAD_TOKEN);
   if (s < 0 || s >= kv.num_seqs || base < 0) return;
   const int rows = 2 * kv.kv_heads;  // of K, then of V
+  // this thread's piece of a row, or its scale byte
+  const bool piece = u < rows * chunks, scale = !piece && u < units;
+  const int row = piece ? u / chunks : scale ? u - rows * chunks : 0, h = row % kv.kv_heads;
+  const bool is_v = row >= kv.kv_heads;
+  u32x4_t *store = (u32x4_t *)((char *)(is_v ? kv.v : kv.k) + (int64_t)h * kv.head_stride * size) + (piece ? u % chunks : 0);
+  uint8_t *scales = (is_v ? v.v_scales : v.k_scales) + (int64_t)h * v.scale_head_stride;
   path += (int64_t)r * max_path;
-  if (u < rows * chunks) {
-    const int row = u / chunks, c = u % chunks, h = row % kv.kv_heads;
-    uint4 *store = (uint4 *)((char *)(row < kv.kv_heads ? kv.k : kv.v) + (int64_t)h * kv.head_stride * size) + c;
-    move_piece(kv, s, base, path, max_path, store, kv.page_stride * size / 16, kv.token_stride * size / 16);
-  } else {
-    const int row = u - rows * chunks, h = row % kv.kv_heads;
-    uint8_t *store = (row < kv.kv_heads ? v.k_scales : v.v_scales) + (int64_t)h * v.scale_head_stride;
-    move_piece(kv, s, base, path, max_path, store, v.scale_page_stride, v.scale_token_stride);
+  for (int i0 = 0; i0 < max_path; i0 += 64) {
+    if (lane < 64) {
+      const int e = i0 + lane < max_path ? path[i0 + lane] : -1;
+      const int prev = lane ? __shfl_up(e, 1) : i0 ? last : -1;
+      const uint64_t stop = __ballot(e <= prev || e < 0);
+      const int n = stop ? __builtin_ctzll(stop) : 64;
+      KV_CHECK(lane != n || e < 0, LORA_DEBUG_BAD_TOKEN);
+      Place a = {-1, 0}, b = {-1, 0};
+      if (lane < n && e != i0 + lane) {  // not where it stands already
+        a = place_of(kv, s, (int)min((int64_t)base + e, (int64_t)INT32_MAX));
+        b = place_of(kv, s, (int)min((int64_t)base + i0 + lane, (int64_t)INT32_MAX));
+      }
+      if (a.page < 0) b.page = -1;
+      from[lane] = a;
+      to[lane] = b;
+      if (lane == 63) last = e;
+      if (lane == 0) count = n;
+    }
+    __syncthreads();
+    const int n = count;
+    if (piece) move_pieces(store, kv.page_stride * size / 16, kv.token_stride * size / 16, from, to, n);
+    else if (scale) move_pieces(scales, v.scale_page_stride, v.scale_token_stride, from, to, n);
+    if (n < 64) return;
+    __syncthreads();
   }
 }
 
