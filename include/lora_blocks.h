@@ -61,12 +61,17 @@ lora_status lora_kv_bounds_update(const lora_kv_view *kv, const lora_kv_bounds *
  *   q        as for lora_kv_attn, num_tokens rows of q_heads
  *   count, sink, recent  1 <= count <= LORA_BLOCKS_MAX_COUNT; sink, recent >= 0, recent >= 1, sink + recent <= count
  *   blocks   device int32 [num_tokens][kv_heads][count]
+ *   workspace  optional device memory (NULL, 0: none), 16-byte aligned.  Where it holds what
+ *              lora_kv_block_select_workspace says, few lists that may be long are scored by a launch of their own; lists
+ *              are the same either way.  Contents on entry do not matter.  Calls that share it must not overlap, in graphs too.
  * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view, more than LORA_BLOCKS_MAX_PAGES pages in a sequence,
  * count, 2^24 tokens of all KV heads and more), LORA_EHIP. */
 lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_kv_bounds *bounds, const int32_t *token_seq,
                                  const int32_t *token_pos, int32_t num_tokens, const void *q, int64_t q_token_stride,
                                  int64_t q_head_stride, int32_t q_heads, int32_t count, int32_t sink, int32_t recent,
-                                 int32_t *blocks, hipStream_t stream);
+                                 int32_t *blocks, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+/* Workspace bytes for num_tokens tokens (0: it would not be used).  Host only.  Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view). */
+lora_status lora_kv_block_select_workspace(const lora_kv_view *kv, int32_t num_tokens, int64_t *bytes);
 
 /* lora_kv_attn over listed pages: token t and KV head h keep the positions j <= token_pos[t] on the pages
  * blocks[t][h][0 .. count) of its sequence.  Any lists are taken, in any order (a page that is listed twice counts

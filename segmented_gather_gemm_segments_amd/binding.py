@@ -165,7 +165,8 @@ EXPORTS = {
     "lora_kv_keep_path": ([_P, _P, _P, _P, _I32, _I32, _P], _I32),
     "lora_kv_bounds_row_bytes": ([_I32, _P], _I32),
     "lora_kv_bounds_update": ([_P, _P, _P, _P, _P, _I32, _I32, _P], _I32),
-    "lora_kv_block_select": ([_P, _P, _P, _P, _I32, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P], _I32),
+    "lora_kv_block_select": ([_P, _P, _P, _P, _I32, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I64, _P], _I32),
+    "lora_kv_block_select_workspace": ([_P, _I32, _P], _I32),
     "lora_kv_attn_blocks": ([_P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _P],
                             _I32),
     "lora_kv_create": ([_P, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
@@ -900,6 +901,7 @@ class KvView:
         self.index, self.device = k.get_device(), k.device
         self.num_seqs, self.max_kv = self.desc.num_seqs, self.desc.max_pages * tokens
         self.bf16, self.int32, self.fp32 = torch.bfloat16, torch.int32, torch.float32
+        self.select_bytes = {}  # by number of tokens: what lora_kv_block_select takes
 
 
 def lora_pages_copy(storage, src, dst, stream=None):
@@ -1156,10 +1158,17 @@ def lora_kv_bounds_update(view: KvView, bounds: KvBounds, seq, begin, end, max_t
             max_tokens)
 
 
+def lora_kv_block_select_workspace(view: KvView, num_tokens: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().lora_kv_block_select_workspace(view.ref, num_tokens, ctypes.byref(out)))
+    return int(out.value)
+
+
 def lora_kv_block_select(view: KvView, bounds: KvBounds, token_seq, token_pos, q, blocks, sink: int = 1, recent: int = 1,
-                         stream=None):
+                         workspace=None, stream=None):
     """The pages that token t, at position token_pos[t] of sequence token_seq[t] (int32 [T]), attends to, for each KV
-    head: blocks int32 [T, kv_heads, count], ascending, -1 behind the last.  q [T or more, q_heads, head_dim] bf16."""
+    head: blocks int32 [T, kv_heads, count], ascending, -1 behind the last.  q [T or more, q_heads, head_dim] bf16.
+    workspace: None allocates what the call takes on its stream, where it takes any."""
     d, n = view.desc, token_seq.numel()
     _i32s(view.device, ("token_seq", token_seq), ("token_pos", token_pos), ("blocks", blocks))
     _tensors(view.device, ("q", q, view.bf16))
@@ -1171,8 +1180,20 @@ def lora_kv_block_select(view: KvView, bounds: KvBounds, token_seq, token_pos, q
         _refuse(f"bounds are on {bounds.rows.device}, not {view.device}")
     if view.index < 0:
         _gpu(view.device)
+    if workspace is None:
+        need = view.select_bytes.get(n)
+        if need is None:
+            need = view.select_bytes[n] = lora_kv_block_select_workspace(view, n)
+        if need:
+            torch = _torch()
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=view.device)
+    elif not workspace.is_contiguous() or workspace.device != view.device:
+        _flat("workspace", workspace)
+        _refuse(f"workspace is on {workspace.device}, not {view.device}")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     _launch("lora_kv_block_select", view.index, stream, view.ref, bounds.ref, token_seq.data_ptr(), token_pos.data_ptr(), n,
-            q.data_ptr(), *_row_strides(q), q.shape[1], blocks.shape[2], sink, recent, blocks.data_ptr())
+            q.data_ptr(), *_row_strides(q), q.shape[1], blocks.shape[2], sink, recent, blocks.data_ptr(), wp, wb)
 
 
 def lora_kv_attn_blocks(view: KvView, plan: AttnPlan, blocks, token_pos, q, out, lse=None, scale: Optional[float] = None,

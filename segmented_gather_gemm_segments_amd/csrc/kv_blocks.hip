@@ -3,6 +3,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kv_internal.h"
 #include "kv8.h"
@@ -119,10 +120,10 @@ __global__ __launch_bounds__(kThreads) void bounds_kernel(lora_kv8_view v, lora_
 // pages a wave reads from memory in the order of the operand.  Scores become keys that order as they do, in
 // LDS; the count-th largest is found 8 bits at a time from histograms, and the list is written in the order of pages.
 //
-// Bounds cross the device once for the heads that share them, 2 head_dim + 16 bytes a page.
-constexpr int kSelect = 512;
-constexpr int kSelectWaves = kSelect / 64;
-
+// Bounds cross the device once for the heads that share them, 2 head_dim + 16 bytes a page, with 4 groups of 16 pages of
+// a wave in flight (2 where head_dim is above 128).  32 tokens, 8 KV heads of 128, up to 512 pages: SELECT_US.  One
+// compute unit reads no more than about 40 GB/s of such rows, so where lists are few and may be long a launch of its own
+// scores their pages, 256 a workgroup, into a workspace (8 lists of 8125 pages: SPLIT_US, in one launch 95).
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
 
 // Orders as the score does.
@@ -131,40 +132,66 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-template <int KEYS>
-__global__ __launch_bounds__(kSelect) void select_kernel(lora_kv_view kv, lora_kv_bounds bounds,
-                                                         const int32_t *__restrict__ token_seq,
-                                                         const int32_t *__restrict__ token_pos, const uint16_t *__restrict__ q,
-                                                         int64_t q_ts, int64_t q_hs, int group, int count, int sink, int recent,
-                                                         int32_t *__restrict__ blocks) {
-  __shared__ uint32_t keys[KEYS];
-  __shared__ __attribute__((aligned(16))) char qc[16][512];
-  __shared__ float unit[16];
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t found[2];
-  __shared__ uint32_t part[2][kSelectWaves][2];
-  const int h = blockIdx.x % kv.kv_heads, t = blockIdx.x / kv.kv_heads;
+struct Select {
+  lora_kv_view kv;
+  lora_kv_bounds bounds;
+  const int32_t *token_seq, *token_pos;
+  const uint16_t *q;
+  int64_t q_ts, q_hs;
+  int32_t group, count, sink, recent;
+  int32_t *blocks;
+  uint32_t *keys;  // [lists][max_pages], or null: scored by the workgroup that selects
+};
+
+// A list's token: its page table, its number of pages (0: none), from which its row of queries does not depend.
+struct Token {
+  const int32_t *table;
+  int n;
+};
+__device__ __forceinline__ Token token_of(const Select &a, int t) {
+  const int s = a.token_seq[t], pos = a.token_pos[t];
+  const bool good = s >= 0 && s < a.kv.num_seqs && pos >= 0 && pos < a.kv.max_pages * a.kv.page_tokens;
+  KV_CHECK(good || s < 0 || threadIdx.x != 0, LORA_DEBUG_BAD_TOKEN);
+  return {a.kv.page_table + (int64_t)(good ? s : 0) * a.kv.max_pages, good ? pos / a.kv.page_tokens + 1 : 0};
+}
+
+// Keys of pages [begin, end) of token t's sequence and KV head h, each given to store(page, key, whether it is the first for
+// its page) as often as there are 16 query heads; returns the page's key so far.  S: products of 64 numbers that a row of
+// bounds takes at most; waves [0, WAVES) of the workgroup.
+template <int WAVES, int S, typename Store>
+__device__ __forceinline__ void score(const Select &a, const Token &token, int t, int h, int begin, int end, char (*qc)[512],
+                                      float *unit, Store store) {
+  constexpr int U = S <= 4 ? 4 : 2;
+  const lora_kv_view &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 15, fg = lane >> 4;
-  int32_t *out = blocks + (int64_t)blockIdx.x * count;
-  const int s = token_seq[t], pos = token_pos[t];
-  const bool good = s >= 0 && s < kv.num_seqs && pos >= 0 && pos < kv.max_pages * kv.page_tokens;
-  KV_CHECK(good || s < 0 || tid != 0, LORA_DEBUG_BAD_TOKEN);
-  const int n = good ? pos / kv.page_tokens + 1 : 0;
-  if (n <= count) {
-    for (int i = tid; i < count; i += kSelect) out[i] = i < n ? i : -1;
-    return;
-  }
-  const int32_t *table = kv.page_table + (int64_t)s * kv.max_pages;
   const int D = kv.head_dim, steps = (2 * D + 63) / 64;
-  for (int g0 = 0; g0 < group; g0 += 16) {
+  int page[U], f[U];
+  i32x4_t b[U][S];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) page[i] = token.table[min(p0 + 16 * WAVES * i + fr, end - 1)];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      KV_CHECK((unsigned)page[i] < (unsigned)kv.num_pages || fg != 0, LORA_DEBUG_BAD_PAGE);
+      // an absent page's row is not read
+      const bool there = (unsigned)page[i] < (unsigned)kv.num_pages;
+      const char *row = (const char *)a.bounds.rows + page[i] * a.bounds.page_stride + h * a.bounds.head_stride;
+      f[i] = *(there ? reinterpret_cast<const int32_t *>(row + 64 * steps) : reinterpret_cast<const int32_t *>(&g_zeros));
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+        b[i][k] = *reinterpret_cast<const i32x4_t *>(there && k < steps ? row + 64 * k + 16 * fg : (const char *)&g_zeros);
+    }
+  };
+  const int first = begin + 16 * wave;
+  for (int g0 = 0; g0 < a.group; g0 += 16) {
+    if (first < end) load(first);  // on its way while the queries are rounded
+    if (g0) __syncthreads();       // the rows before have been read
     // the query rows in whole numbers: 32 threads a head, 8 elements each
-    __syncthreads();
-    {
-      const int g = tid >> 5, c = tid & 31;
-      const bool mine = g0 + g < group && c * 8 < D;
+    for (int g = tid >> 5; g < min(a.group - g0, 16); g += 2 * WAVES) {
+      const int c = tid & 31;
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (mine) u = *reinterpret_cast<const uint4 *>(q + t * q_ts + (h * group + g0 + g) * q_hs + c * 8);
+      if (c * 8 < D) u = *reinterpret_cast<const uint4 *>(a.q + t * a.q_ts + (h * a.group + g0 + g) * a.q_hs + c * 8);
       float m = top8(u);
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
@@ -186,46 +213,115 @@ __global__ __launch_bounds__(kSelect) void select_kernel(lora_kv_view kv, lora_k
       if (c == 0) unit[g] = exponent((uint32_t)(127 + e));
     }
     __syncthreads();
-    for (int p0 = 16 * wave; p0 < n; p0 += 16 * kSelectWaves) {
-      const int p = p0 + fr, page = p < n ? table[p] : -1;
-      const bool there = (unsigned)page < (unsigned)kv.num_pages;
-      KV_CHECK(there || p >= n || fg != 0, LORA_DEBUG_BAD_PAGE);
-      const char *row = there ? (const char *)bounds.rows + page * bounds.page_stride + h * bounds.head_stride : nullptr;
-      const int f = there ? *reinterpret_cast<const int32_t *>(row + 64 * steps) : 0;
-      i32x4_t sum = {0, 0, 0, 0};
-      for (int k = 0; k < steps; ++k) {
-        const uint4 b = *reinterpret_cast<const uint4 *>(there ? row + 64 * k + 16 * fg : (const char *)&g_zeros);
-        const uint4 a = *reinterpret_cast<const uint4 *>(&qc[fr][64 * k + 16 * fg]);
-        sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), sum, 0, 0, 0);
-      }
-      // column fr: this lane's page; rows 4 fg ..: heads
-      float best = -INFINITY;
+    for (int p0 = first; p0 < end; p0 += 16 * U * WAVES) {
+      if (p0 != first) load(p0);
+      i32x4_t sum[U];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (g0 + 4 * fg + e < group) best = fmaxf(best, (float)sum[e] * unit[4 * fg + e]);
-      best = fmaxf(best, __shfl_xor(best, 16));
-      best = fmaxf(best, __shfl_xor(best, 32));
-      best = there ? best * exponent((uint32_t)(127 + min(max(f, -50), 50))) : -INFINITY;
-      if (fg == 0 && p < n) {
-        const uint32_t key = p < sink || p >= n - recent ? ~0u : key_of(best);
-        keys[p] = g0 == 0 ? key : max(keys[p], key);
+      for (int i = 0; i < U; ++i) sum[i] = i32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        if (k >= steps) break;
+        const i32x4_t x = *reinterpret_cast<const i32x4_t *>(&qc[fr][64 * k + 16 * fg]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) sum[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, b[i][k], sum[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        // column fr: this lane's page; rows 4 fg ..: heads
+        const int p = p0 + 16 * WAVES * i + fr;
+        float best = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g0 + 4 * fg + e < a.group) best = fmaxf(best, (float)sum[i][e] * unit[4 * fg + e]);
+        best = fmaxf(best, __shfl_xor(best, 16));
+        best = fmaxf(best, __shfl_xor(best, 32));
+        best = (unsigned)page[i] < (unsigned)kv.num_pages ? best * exponent((uint32_t)(127 + min(max(f[i], -50), 50))) : -INFINITY;
+        if (fg == 0 && p < end) store(p, key_of(best), g0 == 0);
       }
     }
   }
-  // the count-th largest key, from its highest 8 bits to its lowest
-  uint32_t prefix = 0, fixed = 0, need = (uint32_t)count;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    __syncthreads();
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kSelect)
-      if ((keys[i] & fixed) == prefix) atomicAdd(&hist[keys[i] >> shift & 255], 1u);
+}
+
+constexpr int kScorePages = 256;  // of a workgroup that only scores: one turn of its 4 waves (two above head_dim 128)
+
+template <int S>
+__global__ __launch_bounds__(256) void score_kernel(Select a, int parts) {
+  __shared__ __attribute__((aligned(16))) char qc[16][512];
+  __shared__ float unit[16];
+  const int part = blockIdx.x % parts, list = blockIdx.x / parts, h = list % a.kv.kv_heads, t = list / a.kv.kv_heads;
+  const Token token = token_of(a, t);
+  const int begin = part * kScorePages, end = min(token.n, begin + kScorePages);
+  if (token.n <= a.count || begin >= end) return;
+  uint32_t *keys = a.keys + (int64_t)list * a.kv.max_pages;
+  score<4, S>(a, token, t, h, begin, end, qc, unit, [&](int p, uint32_t key, bool first) { keys[p] = first ? key : max(keys[p], key); });
+}
+
+template <int KEYS, int THREADS, int S>
+__global__ __launch_bounds__(THREADS) void select_kernel(Select a) {
+  constexpr int kWaves = THREADS / 64;
+  __shared__ uint32_t keys[KEYS];
+  __shared__ __attribute__((aligned(16))) char qc[16][512];
+  __shared__ float unit[16];
+  __shared__ uint32_t hist[256], found[3], range[kWaves][2], part[kWaves][2];
+  const int h = blockIdx.x % a.kv.kv_heads, t = blockIdx.x / a.kv.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Token token = token_of(a, t);
+  const int n = token.n, count = a.count, sink = a.sink, recent = a.recent;
+  int32_t *out = a.blocks + (int64_t)blockIdx.x * count;
+  if (n <= count) {
+    for (int i = tid; i < count; i += THREADS) out[i] = i < n ? i : -1;
+    return;
+  }
+  if (a.keys) {
+    const uint32_t *from = a.keys + (int64_t)blockIdx.x * a.kv.max_pages;
+    for (int i = tid; i < n; i += THREADS) keys[i] = from[i];
+  } else {
+    score<kWaves, S>(a, token, t, h, 0, n, qc, unit, [&](int p, uint32_t key, bool first) { keys[p] = first ? key : max(keys[p], key); });
+  }
+  // Of the keys between the first and the last pages, which are listed anyway, the need-th largest: 8 bits at a time from the
+  // highest in which they differ.  Counted from the least of them, so that their first digits spread over the bins (a
+  // bin's additions come one after the other).
+  uint32_t need = (uint32_t)(count - sink - recent);
+  uint32_t least = ~0u, most = 0;
+  if (tid < 256) hist[tid] = 0;
+  __syncthreads();
+  for (int i = sink + tid; i < n - recent; i += THREADS) {
+    least = min(least, keys[i]);
+    most = max(most, keys[i]);
+  }
+  for (int x = 1; x < 64; x <<= 1) {
+    least = min(least, (uint32_t)__shfl_xor(least, x));
+    most = max(most, (uint32_t)__shfl_xor(most, x));
+  }
+  if (lane == 0) {
+    range[wave][0] = least;
+    range[wave][1] = most;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    least = min(least, range[w][0]);
+    most = max(most, range[w][1]);
+  }
+  int left = need ? 32 - __clz(most - least) : 0;  // bits not looked at yet
+  uint32_t prefix = 0;                              // the others, of the key that is looked for
+  bool whole = need == 0;                           // all keys from the prefix on are listed
+  if (whole) prefix = most - least + 1;
+  while (left > 0 && !whole) {
+    const int bits = min(left, 8), shift = left - bits;
+    for (int i = sink + tid; i < n - recent; i += THREADS) {
+      const uint32_t key = keys[i] - least;
+      if (left == 32 || key >> left == prefix) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1u);
+    }
     __syncthreads();
     if (wave == 0) {
       // keys of higher digits than this lane's 4
       uint32_t bin[4], all = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) all += bin[x] = hist[4 * lane + x];
+      for (int x = 0; x < 4; ++x) {
+        all += bin[x] = hist[4 * lane + x];
+        hist[4 * lane + x] = 0;  // for the next digit
+      }
       uint32_t above = all;
       for (int x = 1; x < 64; x <<= 1) {
         const uint32_t y = __shfl_down(above, x);
@@ -237,38 +333,57 @@ __global__ __launch_bounds__(kSelect) void select_kernel(lora_kv_view kv, lora_k
         if (above < need && above + bin[x] >= need) {
           found[0] = 4 * lane + x;
           found[1] = need - above;
+          found[2] = above + bin[x] == need;
         }
         above += bin[x];
       }
     }
     __syncthreads();
-    prefix |= found[0] << shift;
-    fixed |= 255u << shift;
+    prefix = prefix << bits | found[0];
     need = found[1];
+    whole = found[2];
+    left = shift;
   }
-  // all keys above it and the first `need` that equal it, in the order of pages
-  uint32_t more = 0, same = 0;  // in the pages before
-  for (int p0 = 0, turn = 0; p0 < n; p0 += kSelect, turn ^= 1) {
-    const int p = p0 + tid;
-    const uint32_t key = p < n ? keys[p] : 0;
-    const uint64_t gt = __ballot(p < n && key > prefix), eq = __ballot(p < n && key == prefix);
-    if (lane == 0) {
-      part[turn][wave][0] = __popcll(gt);
-      part[turn][wave][1] = __popcll(eq);
-    }
-    __syncthreads();
-    const uint64_t below = (1ull << lane) - 1;
-    uint32_t g = more + __popcll(gt & below), e = same + __popcll(eq & below);
+  // Where a digit's keys are all listed the lower ones do not matter; else the prefix is the whole key, and of those that
+  // equal it the first `need` are listed.  In the order of pages: each wave counts its share, then writes it.
+  const int share = ((n + kWaves - 1) / kWaves + 63) / 64 * 64, begin = wave * share, end = min(n, begin + share);
+  auto which = [&](int p, bool &over, bool &level) {
+    const uint32_t key = p < end ? keys[p] - least : 0, high = left == 32 ? 0 : key >> left;
+    const bool anyway = p < end && (p < sink || p >= n - recent), on = p < end && !anyway;
+    over = anyway || (on && (high > prefix || (whole && high == prefix)));
+    level = on && !whole && high == prefix;
+  };
+  uint32_t more = 0, same = 0;
+  for (int p0 = begin; p0 < end; p0 += 64) {
+    bool over, level;
+    which(p0 + lane, over, level);
+    more += __popcll(__ballot(over));
+    same += __popcll(__ballot(level));
+  }
+  if (lane == 0) {
+    part[wave][0] = more;
+    part[wave][1] = same;
+  }
+  __syncthreads();
+  more = same = 0;  // in the pages before
 #pragma unroll
-    for (int w = 0; w < kSelectWaves; ++w) {
-      g += w < wave ? part[turn][w][0] : 0;
-      e += w < wave ? part[turn][w][1] : 0;
-      more += part[turn][w][0];
-      same += part[turn][w][1];
-    }
-    if (p < n && (key > prefix || (key == prefix && e < need))) out[g + min(e, need)] = p;
+  for (int w = 0; w < kWaves; ++w) {
+    more += w < wave ? part[w][0] : 0;
+    same += w < wave ? part[w][1] : 0;
+  }
+  for (int p0 = begin; p0 < end; p0 += 64) {
+    bool over, level;
+    which(p0 + lane, over, level);
+    const uint64_t gt = __ballot(over), eq = __ballot(level), below = (1ull << lane) - 1;
+    const uint32_t g = more + __popcll(gt & below), e = same + __popcll(eq & below);
+    if (over || (level && e < need)) out[g + min(e, need)] = p0 + lane;
+    more += __popcll(gt);
+    same += __popcll(eq);
   }
 }
+
+// Whether a call's pages are scored by a launch of their own: few lists that may be long.
+bool splits(const lora_kv_view *kv, int64_t lists) { return lists > 0 && lists <= 64 && kv->max_pages > 512; }
 
 lora_status launched(const char *what) {
   const hipError_t e = hipGetLastError();
@@ -309,11 +424,20 @@ extern "C" lora_status lora_kv_bounds_update(const lora_kv_view *kv, const lora_
   return launched("bounds launch");
 }
 
+extern "C" lora_status lora_kv_block_select_workspace(const lora_kv_view *kv, int32_t num_tokens, int64_t *bytes) {
+  const lora_status st = check_view(kv);
+  if (st != LORA_OK) return st;
+  if (!bytes || num_tokens < 0) return fail(LORA_EINVAL, "%d tokens, or null bytes", num_tokens);
+  const int64_t lists = (int64_t)num_tokens * kv->kv_heads;
+  *bytes = splits(kv, lists) ? lists * kv->max_pages * (int64_t)sizeof(uint32_t) : 0;
+  return ok();
+}
+
 extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_kv_bounds *bounds,
                                             const int32_t *token_seq, const int32_t *token_pos, int32_t num_tokens,
                                             const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads,
-                                            int32_t count, int32_t sink, int32_t recent, int32_t *blocks,
-                                            hipStream_t stream) {
+                                            int32_t count, int32_t sink, int32_t recent, int32_t *blocks, void *workspace,
+                                            int64_t workspace_bytes, hipStream_t stream) {
   lora_status st = check_view(kv);
   if (st == LORA_OK) st = check_bounds(bounds);
   if (st != LORA_OK) return st;
@@ -330,13 +454,33 @@ extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_k
   if (num_tokens == 0) return ok();
   const bool some = kv->num_pages > 0 && kv->num_seqs > 0 && kv->max_pages > 0;
   if (!token_seq || !token_pos || !q || !blocks || (some && !bounds->rows)) return fail(LORA_EINVAL, "null pointer");
+  if (workspace_bytes < 0 || ((uintptr_t)workspace & 15)) return fail(LORA_EINVAL, "workspace of %lld bytes must be 16-byte aligned", (long long)workspace_bytes);
   if (((uintptr_t)q & 15) || !aligned4(token_seq) || !aligned4(token_pos) || !aligned4(blocks))
     return fail(LORA_EINVAL, "q must be 16-byte aligned, the other arrays 4-byte");
-  // the keys' LDS leaves a compute unit several workgroups where sequences are short
-  const auto kernel = kv->max_pages <= 2048 ? select_kernel<2048> : kv->max_pages <= 8192 ? select_kernel<8192>
-                                                                                          : select_kernel<LORA_BLOCKS_MAX_PAGES>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(num_tokens * kv->kv_heads)), dim3(kSelect), 0, stream, *kv, *bounds, token_seq,
-                     token_pos, (const uint16_t *)q, q_token_stride, q_head_stride, q_heads / kv->kv_heads, count, sink, recent,
-                     blocks);
+  const int64_t lists = (int64_t)num_tokens * kv->kv_heads, need = lists * kv->max_pages * (int64_t)sizeof(uint32_t);
+  const int steps = (2 * kv->head_dim + 63) / 64, size = steps <= 2 ? 2 : steps <= 4 ? 4 : 8;
+  Select a{*kv, *bounds, token_seq, token_pos, (const uint16_t *)q, q_token_stride, q_head_stride, q_heads / kv->kv_heads, count,
+           sink, recent, blocks, nullptr};
+  if (splits(kv, lists) && workspace && workspace_bytes >= need) {
+    a.keys = (uint32_t *)workspace;
+    const int parts = (kv->max_pages + kScorePages - 1) / kScorePages;
+    const auto kernel = size == 2 ? score_kernel<2> : size == 4 ? score_kernel<4> : score_kernel<8>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(lists * parts)), dim3(256), 0, stream, a, parts);
+  }
+  // Threads of a workgroup: 512 where every compute unit has one of them at most, for a shorter way over the pages (256 lists of up
+  // to 512 pages: 12.4 us, with 256 threads 15.2), else 256 (1812 lists of up to 209: 16.8 us, with 512 threads 28); 1024 for
+  // long sequences, whose keys leave a compute unit few workgroups.
+  auto launch = [&](auto keys, auto threads) {
+    constexpr int K = decltype(keys)::value, T = decltype(threads)::value;
+    const auto kernel = size == 2 ? select_kernel<K, T, 2> : size == 4 ? select_kernel<K, T, 4> : select_kernel<K, T, 8>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)lists), dim3(T), 0, stream, a);
+  };
+  const std::integral_constant<int, 256> small{};
+  const std::integral_constant<int, 512> medium{};
+  const std::integral_constant<int, 1024> large{};
+  if (kv->max_pages > 8192) launch(std::integral_constant<int, LORA_BLOCKS_MAX_PAGES>{}, large);
+  else if (kv->max_pages > 2048) launch(std::integral_constant<int, 8192>{}, large);
+  else if (lists <= 256) launch(std::integral_constant<int, 2048>{}, medium);
+  else launch(std::integral_constant<int, 2048>{}, small);
   return launched("page selection launch");
 }

@@ -172,9 +172,12 @@ extern "C" lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t 
       int64_t share = even(kind == 1 && uneven ? 2 * kAimUnits[1] : kAimUnits[kind]);
       // Row items of uneven spans aim at twice the units, which the device takes longest first (64 / 8 heads of 128, 64
       // tokens over 256 to 8192 positions: 250 us, else 275).
-      if (kind == 0 && !few && widest > share * 3 / 2) share = even(2 * kAimUnits[0]);
-      // those are cut while that leaves each compute unit one at most (4 trees of 26 over 175 to 700: 20 us uncut, 30 cut)
+      if (kind == 0 && widest > share * 3 / 2) share = even(2 * kAimUnits[0]);
+      // Row items of few trees are cut while that leaves each compute unit one at most (4 trees of 26 over 175 to 700: 20 us
+      // uncut, 30 cut), and those of lists, whose spans are all the same, to one for each (64 / 8 heads of 128, lists of
+      // 4096 positions: 32 tokens 96.7 us uncut, 101 in two; 8 tokens 44 uncut, 32 in two, 30.6 in four).
       if (kind == 0 && few) share = 2 * (int64_t)tiles[0].size() * kv_heads > kComputeUnits ? widest : even(kComputeUnits);
+      if (kind == 0 && listed) share = even(kComputeUnits);
       share = std::max(kMinRange[kind], share);
       std::vector<Tile> ranges;
       for (const Tile &t : tiles[kind]) {
