@@ -317,10 +317,13 @@ class ServingBlock:
     holds the adapters' rows.  Weights and adapters are seeded; the arithmetic is the library's.
 
     ``step(hidden, seqs, new_tokens)`` runs the new tokens of some sequences (one each for decode, a chunk for a prompt)
-    through the block and returns their output; ``fork``, ``free`` and ``compact`` act on the cache."""
+    through the block and returns their output; ``fork``, ``free`` and ``compact`` of ``kv`` act on the cache.
+    ``draft`` runs trees of drafted tokens instead, and ``accept`` keeps a path of each.  fp8: the cache holds 8-bit rows.
+    bounds: its pages hold the bounds of their keys, and ``step`` can attend to a few pages of each sequence."""
 
     def __init__(self, d_model: int, q_heads: int, kv_heads: int, head_dim: int, num_adapters: int, rank: int,
-                 max_seqs: int, max_pages: int, pool_pages: int, group: int = 128, seed: int = 0, device="cuda"):
+                 max_seqs: int, max_pages: int, pool_pages: int, group: int = 128, seed: int = 0, device="cuda",
+                 fp8: bool = False, bounds: bool = False):
         torch = _torch()
         device = torch.device(device)
         if device.type == "cuda" and device.index is None:
@@ -364,7 +367,8 @@ class ServingBlock:
                     a = (torch.randn((num_adapters, rank, k), generator=gen, device=device) * k ** -0.5).bfloat16()
                     b = (torch.randn((num_adapters, rank, n), generator=gen, device=device) * rank ** -0.5).bfloat16()
                     self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rank, a, b, rank_dev, ranks)
-            self.kv = B.KvCache(self.pool, kv_heads, head_dim, max_seqs, max_pages)
+            self.kv = B.KvCache(self.pool, kv_heads, head_dim, max_seqs, max_pages, fp8=fp8, bounds=bounds)
+            self._drafts = {}  # sequence: (its length before the draft, nodes)
 
     def project(self, name, x, y, token_adapter):
         """y = W x + B (A x), the base from 4-bit codes, the delta of each token's adapter.  x and y are contiguous, and
@@ -391,9 +395,9 @@ class ServingBlock:
                 B._refuse(f"{name} {tuple(rows.shape)}: {(t, width)} wanted for {t} adapter ids")
         return t
 
-    def step(self, hidden, seqs, new_tokens, token_adapter):
-        """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device.  A call that
-        is refused leaves the cache as it is."""
+    def _grow(self, hidden, seqs, new_tokens, token_adapter):
+        """Checks a step, extends its sequences and returns (seqs, new tokens, lengths, starts, and on the device each
+        token's sequence and position); None where it has no tokens."""
         torch = _torch()
         seqs, new_tokens = [int(s) for s in seqs], [int(n) for n in new_tokens]
         t = self._rows(token_adapter, ("hidden", hidden, self.d_model))
@@ -401,18 +405,118 @@ class ServingBlock:
             B._refuse(f"{len(seqs)} sequences grow by {new_tokens}, hidden has {t} tokens")
         self.kv.extend(seqs, new_tokens)
         if t == 0:
-            return torch.empty_like(hidden)
+            return None
         lens = [self.kv.length(s) for s in seqs]
         starts = np.concatenate([[0], np.cumsum(new_tokens)]).astype(np.int32)
         seq = np.repeat(np.asarray(seqs, np.int32), new_tokens)
         pos = np.concatenate([np.arange(n - q, n, dtype=np.int32) for q, n in zip(new_tokens, lens)])
-        to = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(self.device)
-        plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim).to(self.device)
-        return self.run(hidden, plan, to(seq), to(pos), token_adapter)
+        return seqs, new_tokens, lens, starts, self._ints(seq), self._ints(pos)
 
-    def run(self, hidden, plan, token_seq, token_pos, token_adapter):
+    def _ints(self, values):
+        return _torch().from_numpy(np.ascontiguousarray(values, np.int32)).to(self.device)
+
+    def step(self, hidden, seqs, new_tokens, token_adapter, pages: Optional[int] = None, sink: int = 1, recent: int = 2):
+        """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device.  A call that
+        is refused leaves the cache as it is.  pages: each token attends to that many pages of its sequence at most for
+        each KV head, the first `sink`, the last `recent` and those that the bounds of their keys choose."""
+        torch = _torch()
+        if pages is not None:
+            if self.kv.bounds is None:
+                B._refuse("pages are chosen by the bounds of their keys: make the block with bounds=True")
+            if not 0 <= sink < sink + recent <= pages <= B.LORA_BLOCKS_MAX_COUNT or recent < 1:
+                B._refuse(f"{pages} pages, the first {sink} and the last {recent} among them")
+        grown = self._grow(hidden, seqs, new_tokens, token_adapter)
+        if grown is None:
+            return torch.empty_like(hidden)
+        seqs, new_tokens, lens, starts, seq, pos = grown
+        ranges = self._ranges(seqs, [n - q for q, n in zip(new_tokens, lens)], lens)
+        if pages is None:
+            plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim).to(self.device)
+            return self.run(hidden, plan, seq, pos, token_adapter, ranges)
+        view, t = self.kv.view, int(starts[-1])
+        most = min(pages, max(-(-n // view.desc.page_tokens) for n in lens)) * view.desc.page_tokens
+        plan = B.lora_kv_attn_plan(np.arange(t + 1), np.repeat(seqs, new_tokens), [most] * t, self.q_heads, self.kv_heads,
+                                   self.head_dim, blocks=True).to(self.device)
+        blocks = torch.empty((t, self.kv_heads, pages), dtype=torch.int32, device=self.device)
+
+        def attend(q, out):
+            B.lora_kv_block_select(view, self.kv.bounds, seq, pos, q, blocks, sink=sink, recent=recent)
+            B.lora_kv_attn_blocks(view, plan, blocks, pos, q, out)
+        return self._run(hidden, seq, pos, token_adapter, ranges, attend)
+
+    def draft(self, hidden, seqs, parents, token_adapter):
+        """Runs a tree of drafted tokens for each sequence: parents lists, for each of them, its nodes' parents (a number
+        below the node's own, or -1 for the context); hidden [T, d_model] of all nodes.  The nodes take the sequences' next
+        positions until ``accept`` keeps a path of them."""
+        torch = _torch()
+        parents = [[int(p) for p in row] for row in parents]
+        for row in parents:
+            if len(row) > B.LORA_TREE_MAX_NODES or any(not -1 <= p < i for i, p in enumerate(row)):
+                B._refuse(f"parents {row[:8]}...: each is -1 or the number of an earlier node, {B.LORA_TREE_MAX_NODES} nodes at most")
+        grown = self._grow(hidden, seqs, [len(row) for row in parents], token_adapter)
+        if grown is None:
+            return torch.empty_like(hidden)
+        seqs, nodes, lens, starts, seq, pos = grown
+        self._drafts.update({s: (n - q, q) for s, q, n in zip(seqs, nodes, lens) if q})
+        plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim, tree=True).to(self.device)
+        tree = B.Tree(int(starts[-1]), max(nodes), self.device)
+        dev_starts, dev_parents = self._ints(starts), self._ints(np.concatenate([np.asarray(row, np.int32) for row in parents]))
+
+        def attend(q, out):
+            B.lora_tree_mask(dev_starts, dev_parents, tree)
+            B.lora_kv_attn_tree(self.kv.view, plan, tree, q, out)
+        return self._run(hidden, seq, pos, token_adapter, self._ranges(seqs, [n - q for q, n in zip(nodes, lens)], lens), attend)
+
+    def accept(self, seqs, paths):
+        """Ends the drafts of some sequences: each keeps the nodes paths[r] (ascending: a node comes behind its ancestors,
+        which are among them) and drops the others.  Nothing may have changed a sequence since its draft, nor another
+        hold pages that the draft grew into (a fork of it).  A call that is refused leaves the cache as it is."""
+        seqs, paths = [int(s) for s in seqs], [[int(n) for n in p] for p in paths]
+        if len(seqs) != len(paths) or len(set(seqs)) != len(seqs):
+            B._refuse(f"{len(seqs)} sequences and {len(paths)} paths, or a sequence twice")
+        B._not_capturing("a path cannot be accepted")
+        page_tokens, bases, own = self.kv.view.desc.page_tokens, [], []
+        for s, path in zip(seqs, paths):
+            base, nodes = self._drafts.get(s, (0, 0))
+            if nodes == 0 or self.kv.length(s) != base + nodes:
+                B._refuse(f"sequence {s} has no draft, or has changed since")
+            if any(b <= a for a, b in zip(path, path[1:])) or (path and not 0 <= path[0] <= path[-1] < nodes):
+                B._refuse(f"path {path[:8]} of a tree of {nodes} nodes")
+            bases.append(base)
+            own += self.kv.pages(s)[base // page_tokens:].tolist()
+        if self.kv.stats()["shared"]:
+            held = np.concatenate([self.kv.pages(s) for s in range(self.kv.view.num_seqs)])
+            if (np.bincount(held, minlength=self.kv.view.desc.num_pages)[own] > 1).any():
+                B._refuse("another sequence holds pages of a draft")
+        rows = np.full((len(seqs), max([len(p) for p in paths] + [1])), -1, np.int32)
+        for r, path in enumerate(paths):
+            rows[r, :len(path)] = path
+        with B._On(self.device, None):
+            B.lora_kv_keep_path(self.kv.view, self._ints(seqs), self._ints(bases), self._ints(rows))
+            for s, base, path in zip(seqs, bases, paths):
+                self.kv.truncate(s, base + len(path))
+                del self._drafts[s]
+            # the page that a draft began on may hold bounds of nodes that are gone
+            self._bounds(self._ranges(seqs, [max(b - 1, 0) for b in bases], [b + len(p) for b, p in zip(bases, paths)]))
+
+    def _ranges(self, seqs, begins, ends):
+        """Positions whose pages' bounds have to be written, on the device; None without bounds."""
+        if self.kv.bounds is None or not seqs:
+            return None
+        return (*(self._ints(x) for x in (seqs, begins, ends)), max(e - b for b, e in zip(begins, ends)))
+
+    def _bounds(self, ranges):
+        if ranges is not None:
+            B.lora_kv_bounds_update(self.kv.view, self.kv.bounds, *ranges)
+
+    def run(self, hidden, plan, token_seq, token_pos, token_adapter, ranges=None):
         """The device work of a step, launches only (every buffer is new; the plan and indices may serve many layers).
-        Rows behind the plan's tokens are padding (token_seq -1, token_adapter -1): what stands in their y is unspecified."""
+        Rows behind the plan's tokens are padding (token_seq -1, token_adapter -1): what stands in their y is unspecified.
+        ranges: of a cache with bounds, (seq, begin, end, most positions) for lora_kv_bounds_update."""
+        return self._run(hidden, token_seq, token_pos, token_adapter, ranges,
+                         lambda q, out: B.lora_kv_attn(self.kv.view, plan, q, out))
+
+    def _run(self, hidden, token_seq, token_pos, token_adapter, ranges, attend):
         torch = _torch()
         t = self._rows(token_adapter, ("hidden", hidden, self.d_model))
         new = lambda n: torch.empty((t, n), dtype=torch.bfloat16, device=self.device)
@@ -422,8 +526,9 @@ class ServingBlock:
             for name, y in (("q", q), ("k", k), ("v", v)):
                 self._project(name, hidden, y, token_adapter)
             B.lora_kv_append(self.kv.view, heads(k, self.kv_heads), heads(v, self.kv_heads), token_seq, token_pos)
+            self._bounds(ranges)
             out = new(self.q_heads * self.head_dim)
-            B.lora_kv_attn(self.kv.view, plan, heads(q, self.q_heads), heads(out, self.q_heads))
+            attend(heads(q, self.q_heads), heads(out, self.q_heads))
             y = new(self.d_model)
             self._project("o", out, y, token_adapter)
         return y
