@@ -584,6 +584,7 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
 // rows, each reading K and V for itself, 22.1 ms.  Heads above 128 leave a SIMD one wave, and those above 192 spill 78
 // registers a lane (2048 tokens over 8192, 32 / 8 heads: of 128 0.29 ms, of 192 0.54, of 256 0.70).
 constexpr int kTileWaves = 4;
+constexpr unsigned kUnits = 256;  // compute units
 constexpr int kTilePos = 64;
 template <int DP>
 struct TileLayout : Layout<DP> {
@@ -627,6 +628,14 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
   }
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = wid / kTileWaves, wave = wid % kTileWaves;
+  // Two workgroups share a compute unit, a wave of each a SIMD.  At equal priority both end late and at once, and where the last
+  // round of them is not full half the device then waits for it; with one favoured the next workgroup starts sooner (8
+  // chunks of 256 over 4096, 64 / 8 heads of 128, 640 workgroups: 171 us, else 204; 32 / 8 of 64, 16 of 256 over 2048: 61 and
+  // 72).  In full rounds it costs a little (a chunk of 4096 over 8192, 32 / 8 of 64, 1024 workgroups: 291 us, favoured
+  // 309), and over many rounds it gives little.  Bits 3:0 of the hardware's id register are the wave's slot in its SIMD.
+  if (GR == 1 && DP <= 128 && gridDim.x > 2 * kUnits && gridDim.x < 16 * kUnits && gridDim.x % (2 * kUnits) != 0 &&
+      (__builtin_amdgcn_s_getreg(4 | 3 << 11) & 1))
+    __builtin_amdgcn_s_setprio(1);
   const int fr = lane & 31, hf = lane >> 5;
   const int D = FULL ? DP : kv.head_dim, nch = D >> 3;
 
@@ -989,8 +998,6 @@ __global__ __launch_bounds__(64 * kTileWaves * GR, DP <= 128 ? 2 : 1) void attn_
   }
 }
 
-constexpr unsigned kComputeUnits = 256;
-
 // Heads of 64, 128 and 256, the usual ones, have kernels without the checks that shorter rows need (chunks of 64
 // over 512 positions, 12 heads of 64: 12.8 us, with the checks 13.8; 8 chunks of 128 over 4096: 171 and 178).
 template <int DP>
@@ -1006,7 +1013,7 @@ void launch_rows(const ArgsOf<F8, M> &a, unsigned grid, hipStream_t stream) {
   constexpr int W = (DP <= 64 ? 4 : DP <= 128 ? 2 : 1) * (F8 && DP > 64 ? 2 : 1);  // 8-bit stages take half the LDS
   const auto wide = full<DP>(a) ? attn_rows_kernel<DP, 2 * W, kFull<DP>, F8, M> : attn_rows_kernel<DP, 2 * W, false, F8, M>;
   const auto slim = full<DP>(a) ? attn_rows_kernel<DP, W, kFull<DP>, F8, M> : attn_rows_kernel<DP, W, false, F8, M>;
-  if (grid <= kComputeUnits) hipLaunchKernelGGL(wide, dim3(grid), dim3(128 * W), 0, stream, a);
+  if (grid <= kUnits) hipLaunchKernelGGL(wide, dim3(grid), dim3(128 * W), 0, stream, a);
   else hipLaunchKernelGGL(slim, dim3(grid), dim3(64 * W), 0, stream, a);
 }
 
@@ -1017,7 +1024,7 @@ void launch_tiles(const ArgsOf<F8, M> &a, unsigned grid, hipStream_t stream) {
   constexpr int G2 = DP <= 128 ? 2 : 1;  // what the LDS holds
   const auto one = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>, 1, F8, M> : attn_tile_kernel<DP, false, 1, F8, M>;
   const auto two = full<DP>(a) ? attn_tile_kernel<DP, kFull<DP>, G2, F8, M> : attn_tile_kernel<DP, false, G2, F8, M>;
-  if (grid <= kComputeUnits) hipLaunchKernelGGL(two, dim3(grid), dim3(64 * kTileWaves * G2), 0, stream, a);
+  if (grid <= kUnits) hipLaunchKernelGGL(two, dim3(grid), dim3(64 * kTileWaves * G2), 0, stream, a);
   else hipLaunchKernelGGL(one, dim3(grid), dim3(64 * kTileWaves), 0, stream, a);
 }
 
