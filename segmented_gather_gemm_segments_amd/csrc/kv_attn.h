@@ -328,6 +328,11 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
   const int64_t pos = (int64_t)it.pos0 + tok;
   const int hi = a.causal ? (int)max(pos, (int64_t)-1) : INT32_MAX;
   int lo = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+  // every row of the item keeps the positions in [lo_all, hi_all] (a node is at most as deep as its number)
+  const int64_t last = (int64_t)it.pos0 + (it.row0 + it.rows - 1) / a.group;
+  const int lo_all = a.window ? (int)max(last - a.window + 1, (int64_t)0) : 0;
+  int hi_all = a.causal ? (int)max((int64_t)it.pos0 + it.row0 / a.group, (int64_t)-1) : INT32_MAX;
+  if constexpr (M == Mask::kTree) hi_all = min(hi_all, max(it.pos0, 0) - 1);
   if constexpr (M == Mask::kTree)
     lo = a.window ? (int)max((int64_t)it.pos0 + min(max(a.tree_depth[it.q_begin + tok], 0), tok) - a.window + 1, (int64_t)0) : 0;
   bf16x8_t qf[KS];
@@ -386,27 +391,35 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
           sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[s], sc[half], 0, 0, 0);
         }
     }
-    // which drafted nodes this row keeps, once the tile reaches them
-    uint32_t nodes = 0;
-    if constexpr (M == Mask::kTree)
-      if ((int64_t)t0 + kRowPos > it.pos0)
-        nodes = (uint32_t)tree_bits(a.tree_mask + (int64_t)(it.q_begin + tok) * a.tree_words, a.tree_words, (int64_t)t0 - it.pos0);
     // scores: element e of this lane is position t0 + 4 fg + e (e < 4) or t0 + 16 + 4 fg + e - 4
     float s8[8];
-    uint32_t keep = 0;
+    uint32_t keep = 255;
     bool hole = false;  // an existing position that this row does not keep
     float mt = -INFINITY;
+    if (there == ~0u && t0 + (kRowPos - 1) <= hi_all && t0 >= lo_all) {  // every row keeps all of the tile
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = (e < 4 ? 4 * fg + e : 16 + 4 * fg + e - 4), p = t0 + i;
-      const bool ex = there >> i & 1;
-      bool ok = ex;
-      if constexpr (M == Mask::kCausal) ok = ex && p <= hi && p >= lo;
-      if constexpr (M == Mask::kTree) ok = ex && p <= hi && (p < it.pos0 ? p >= lo : (nodes >> i & 1));
-      s8[e] = ok ? sc[e >> 2][e & 3] : -INFINITY;
-      keep |= (uint32_t)ok << e;
-      hole |= ex && !ok;
-      mt = fmaxf(mt, s8[e]);
+      for (int e = 0; e < 8; ++e) {
+        s8[e] = sc[e >> 2][e & 3];
+        mt = fmaxf(mt, s8[e]);
+      }
+    } else {
+      uint32_t nodes = 0;  // drafted nodes that this row keeps, once the tile reaches them
+      if constexpr (M == Mask::kTree)
+        if ((int64_t)t0 + kRowPos > it.pos0)
+          nodes = (uint32_t)tree_bits(a.tree_mask + (int64_t)(it.q_begin + tok) * a.tree_words, a.tree_words, (int64_t)t0 - it.pos0);
+      keep = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = (e < 4 ? 4 * fg + e : 16 + 4 * fg + e - 4), p = t0 + i;
+        const bool ex = there >> i & 1;
+        bool ok = ex;
+        if constexpr (M == Mask::kCausal) ok = ex && p <= hi && p >= lo;
+        if constexpr (M == Mask::kTree) ok = ex && p <= hi && (p < it.pos0 ? p >= lo : (nodes >> i & 1));
+        s8[e] = ok ? sc[e >> 2][e & 3] : -INFINITY;
+        keep |= (uint32_t)ok << e;
+        hole |= ex && !ok;
+        mt = fmaxf(mt, s8[e]);
+      }
     }
     mt = max_groups(mt);
     // the running maximum may lag by kSlack (see the tile items)
@@ -1013,8 +1026,23 @@ void launch_rows(const ArgsOf<F8, M> &a, unsigned grid, hipStream_t stream) {
   constexpr int W = (DP <= 64 ? 4 : DP <= 128 ? 2 : 1) * (F8 && DP > 64 ? 2 : 1);  // 8-bit stages take half the LDS
   const auto wide = full<DP>(a) ? attn_rows_kernel<DP, 2 * W, kFull<DP>, F8, M> : attn_rows_kernel<DP, 2 * W, false, F8, M>;
   const auto slim = full<DP>(a) ? attn_rows_kernel<DP, W, kFull<DP>, F8, M> : attn_rows_kernel<DP, W, false, F8, M>;
-  if (grid <= kUnits) hipLaunchKernelGGL(wide, dim3(grid), dim3(128 * W), 0, stream, a);
-  else hipLaunchKernelGGL(slim, dim3(grid), dim3(64 * W), 0, stream, a);
+  // Many workgroups of half the waves again, where there are more than a compute unit holds: items are short then, and what
+  // counts is how many begin and end side by side (in 8 bits, 256 tokens over 75 to 300, 32 / 8 heads of 128: 29 us, else 40;
+  // 64 over 128 to 512, 64 / 64: 73 and 92; 64 over 8192, 64 / 8, 1000 workgroups: 145 and 135.  Lists of 480 positions, 1812
+  // workgroups, heads of 64: 21.1 and 25.4, bf16 27.4 and 36.6; of 2048 positions in 8 bits, 2048 workgroups, heads of
+  // 128: 181 and 167).  bf16 rows with causal masks keep the waves that their sums have always been joined in.
+  bool many = (F8 || M != Mask::kCausal) && W > 1 && grid >= (M == Mask::kBlocks ? 4 : 5) * kUnits;
+  if constexpr (M == Mask::kBlocks) many = many && !(F8 && (int64_t)a.count * a.kv.page_tokens > 1024);
+  if (many) {
+    if constexpr ((F8 || M != Mask::kCausal) && W > 1) {
+      const auto thin = full<DP>(a) ? attn_rows_kernel<DP, W / 2, kFull<DP>, F8, M> : attn_rows_kernel<DP, W / 2, false, F8, M>;
+      hipLaunchKernelGGL(thin, dim3(grid), dim3(32 * W), 0, stream, a);
+    }
+  } else if (grid <= kUnits) {
+    hipLaunchKernelGGL(wide, dim3(grid), dim3(128 * W), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL(slim, dim3(grid), dim3(64 * W), 0, stream, a);
+  }
 }
 
 template <int DP, bool F8, Mask M>
