@@ -120,10 +120,12 @@ __global__ __launch_bounds__(kThreads) void bounds_kernel(lora_kv8_view v, lora_
 // pages a wave reads from memory in the order of the operand.  Scores become keys that order as they do, in
 // LDS; the count-th largest is found 8 bits at a time from histograms, and the list is written in the order of pages.
 //
-// Bounds cross the device once for the heads that share them, 2 head_dim + 16 bytes a page, with 4 groups of 16 pages of
-// a wave in flight (2 where head_dim is above 128).  32 tokens, 8 KV heads of 128, up to 512 pages: SELECT_US.  One
-// compute unit reads no more than about 40 GB/s of such rows, so where lists are few and may be long a launch of its own
-// scores their pages, 256 a workgroup, into a workspace (8 lists of 8125 pages: SPLIT_US, in one launch 95).
+// Bounds cross the device once for the heads that share them, 2 head_dim + 16 bytes a page.  A wave keeps 4 groups of 16
+// pages in flight where its workgroup has a compute unit to itself; 2 where several share one and registers decide how many
+// (1024 lists of up to 125 pages: 11.6 us, with 4 groups 18.3), or head_dim is above 128.  32 tokens, 8 KV heads of 128,
+// up to 512 pages: 11.8 us.  One compute unit reads no more than about 40 GB/s of such rows, so where lists are few and may
+// be long a launch of its own scores their pages, 256 a workgroup, into a workspace (8 lists of 8125 pages: 21.5 us, in one
+// launch 95).
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
 
 // Orders as the score does.
@@ -161,7 +163,7 @@ __device__ __forceinline__ Token token_of(const Select &a, int t) {
 template <int WAVES, int S, typename Store>
 __device__ __forceinline__ void score(const Select &a, const Token &token, int t, int h, int begin, int end, char (*qc)[512],
                                       float *unit, Store store) {
-  constexpr int U = S <= 4 ? 4 : 2;
+  constexpr int U = S <= 4 && WAVES > 4 ? 4 : 2;
   const lora_kv_view &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 15, fg = lane >> 4;
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(THREADS) void select_kernel(Select a) {
   // bin's additions come one after the other).
   uint32_t need = (uint32_t)(count - sink - recent);
   uint32_t least = ~0u, most = 0;
-  if (tid < 256) hist[tid] = 0;
+  for (int i = tid; i < 256; i += THREADS) hist[i] = 0;
   __syncthreads();
   for (int i = sink + tid; i < n - recent; i += THREADS) {
     least = min(least, keys[i]);
@@ -467,20 +469,23 @@ extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_k
     const auto kernel = size == 2 ? score_kernel<2> : size == 4 ? score_kernel<4> : score_kernel<8>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(lists * parts)), dim3(256), 0, stream, a, parts);
   }
-  // Threads of a workgroup: 512 where every compute unit has one of them at most, for a shorter way over the pages (256 lists of up
-  // to 512 pages: 12.4 us, with 256 threads 15.2), else 256 (1812 lists of up to 209: 16.8 us, with 512 threads 28); 1024 for
-  // long sequences, whose keys leave a compute unit few workgroups.
+  // Threads of a workgroup: 512 where every compute unit has one of them at most, for a shorter way over the pages (256 lists of
+  // up to 512 pages: 11.8 us, with 256 threads 15.2); 256 up to five a compute unit (1024 lists of up to 125 pages: 11.6 us,
+  // with 128 threads 12.6); then 128, for fewer waves that wait for one wave's part (1812 lists of up to 209 pages: 12.5 us,
+  // with 256 threads 16.1); 1024 for long sequences, whose keys leave a compute unit few workgroups.
   auto launch = [&](auto keys, auto threads) {
     constexpr int K = decltype(keys)::value, T = decltype(threads)::value;
     const auto kernel = size == 2 ? select_kernel<K, T, 2> : size == 4 ? select_kernel<K, T, 4> : select_kernel<K, T, 8>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)lists), dim3(T), 0, stream, a);
   };
+  const std::integral_constant<int, 128> least{};
   const std::integral_constant<int, 256> small{};
   const std::integral_constant<int, 512> medium{};
   const std::integral_constant<int, 1024> large{};
   if (kv->max_pages > 8192) launch(std::integral_constant<int, LORA_BLOCKS_MAX_PAGES>{}, large);
   else if (kv->max_pages > 2048) launch(std::integral_constant<int, 8192>{}, large);
   else if (lists <= 256) launch(std::integral_constant<int, 2048>{}, medium);
-  else launch(std::integral_constant<int, 2048>{}, small);
+  else if (lists <= 1280) launch(std::integral_constant<int, 2048>{}, small);
+  else launch(std::integral_constant<int, 2048>{}, least);
   return launched("page selection launch");
 }
