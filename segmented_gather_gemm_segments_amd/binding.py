@@ -901,7 +901,6 @@ class KvView:
         self.index, self.device = k.get_device(), k.device
         self.num_seqs, self.max_kv = self.desc.num_seqs, self.desc.max_pages * tokens
         self.bf16, self.int32, self.fp32 = torch.bfloat16, torch.int32, torch.float32
-        self.select_bytes = {}  # by number of tokens: what lora_kv_block_select takes
 
 
 def lora_pages_copy(storage, src, dst, stream=None):
@@ -1181,9 +1180,7 @@ def lora_kv_block_select(view: KvView, bounds: KvBounds, token_seq, token_pos, q
     if view.index < 0:
         _gpu(view.device)
     if workspace is None:
-        need = view.select_bytes.get(n)
-        if need is None:
-            need = view.select_bytes[n] = lora_kv_block_select_workspace(view, n)
+        need = lora_kv_block_select_workspace(view, n)
         if need:
             torch = _torch()
             with torch.cuda.stream(stream):

@@ -298,7 +298,7 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
     const int p = first + tile * kRowPos + (lane & 31), off = p - a.page_div(p) * kv.page_tokens;
     bool ok = inside(p);
     if constexpr (M == Mask::kBlocks) {
-      const int begin = max(first + tile * kRowPos, it.kv_begin), end = min((int64_t)first + (tile + 1) * kRowPos, (int64_t)it.kv_end);
+      const int begin = max(first + tile * kRowPos, it.kv_begin), end = (int)min(first + ((int64_t)tile + 1) * kRowPos, (int64_t)it.kv_end);
       const int lo = a.page_div(begin);
       if (lo < page0 || a.page_div(end - 1) >= page0 + 64) fetch(lo);  // 32 positions lie on 32 pages at most
       page = __shfl(ids, a.page_div(p) - page0);

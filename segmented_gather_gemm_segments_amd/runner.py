@@ -368,7 +368,7 @@ class ServingBlock:
                     b = (torch.randn((num_adapters, rank, n), generator=gen, device=device) * rank ** -0.5).bfloat16()
                     self.delta[name] = B.Weights(B.LORA_BF16, k, n, rank, rank, a, b, rank_dev, ranks)
             self.kv = B.KvCache(self.pool, kv_heads, head_dim, max_seqs, max_pages, fp8=fp8, bounds=bounds)
-            self._drafts = {}  # sequence: (its length before the draft, nodes)
+            self._drafts = {}  # sequence: (its length before the draft, its nodes' parents)
 
     def project(self, name, x, y, token_adapter):
         """y = W x + B (A x), the base from 4-bit codes, the delta of each token's adapter.  x and y are contiguous, and
@@ -404,6 +404,9 @@ class ServingBlock:
         if len(seqs) != len(new_tokens) or any(n < 0 for n in new_tokens) or sum(new_tokens) != t:
             B._refuse(f"{len(seqs)} sequences grow by {new_tokens}, hidden has {t} tokens")
         self.kv.extend(seqs, new_tokens)
+        for s, n in zip(seqs, new_tokens):
+            if n:
+                self._drafts.pop(s, None)  # it goes on as it is
         if t == 0:
             return None
         lens = [self.kv.length(s) for s in seqs]
@@ -457,7 +460,7 @@ class ServingBlock:
         if grown is None:
             return torch.empty_like(hidden)
         seqs, nodes, lens, starts, seq, pos = grown
-        self._drafts.update({s: (n - q, q) for s, q, n in zip(seqs, nodes, lens) if q})
+        self._drafts.update({s: (n - len(row), row) for s, row, n in zip(seqs, parents, lens) if row})
         plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim, tree=True).to(self.device)
         tree = B.Tree(int(starts[-1]), max(nodes), self.device)
         dev_starts, dev_parents = self._ints(starts), self._ints(np.concatenate([np.asarray(row, np.int32) for row in parents]))
@@ -468,20 +471,20 @@ class ServingBlock:
         return self._run(hidden, seq, pos, token_adapter, self._ranges(seqs, [n - q for q, n in zip(nodes, lens)], lens), attend)
 
     def accept(self, seqs, paths):
-        """Ends the drafts of some sequences: each keeps the nodes paths[r] (ascending: a node comes behind its ancestors,
-        which are among them) and drops the others.  Nothing may have changed a sequence since its draft, nor another
-        hold pages that the draft grew into (a fork of it).  A call that is refused leaves the cache as it is."""
+        """Ends the drafts of some sequences: each keeps the nodes paths[r] (none, or one below the context and then each
+        time a successor of the node before) and drops the others.  Nothing may have changed a sequence since its draft, nor
+        another hold pages that the draft grew into (a fork of it).  A call that is refused leaves the cache as it is."""
         seqs, paths = [int(s) for s in seqs], [[int(n) for n in p] for p in paths]
         if len(seqs) != len(paths) or len(set(seqs)) != len(seqs):
             B._refuse(f"{len(seqs)} sequences and {len(paths)} paths, or a sequence twice")
         B._not_capturing("a path cannot be accepted")
         page_tokens, bases, own = self.kv.view.desc.page_tokens, [], []
         for s, path in zip(seqs, paths):
-            base, nodes = self._drafts.get(s, (0, 0))
-            if nodes == 0 or self.kv.length(s) != base + nodes:
+            base, parents = self._drafts.get(s, (0, []))
+            if not parents or self.kv.length(s) != base + len(parents):
                 B._refuse(f"sequence {s} has no draft, or has changed since")
-            if any(b <= a for a, b in zip(path, path[1:])) or (path and not 0 <= path[0] <= path[-1] < nodes):
-                B._refuse(f"path {path[:8]} of a tree of {nodes} nodes")
+            if any(not 0 <= n < len(parents) or parents[n] != up for up, n in zip([-1] + path, path)):
+                B._refuse(f"{path[:8]} is no path from the context of a tree of {len(parents)} nodes")
             bases.append(base)
             own += self.kv.pages(s)[base // page_tokens:].tolist()
         if self.kv.stats()["shared"]:
@@ -500,9 +503,11 @@ class ServingBlock:
             self._bounds(self._ranges(seqs, [max(b - 1, 0) for b in bases], [b + len(p) for b, p in zip(bases, paths)]))
 
     def _ranges(self, seqs, begins, ends):
-        """Positions whose pages' bounds have to be written, on the device; None without bounds."""
+        """Positions whose pages' bounds have to be written, on the device (a sequence with none is skipped); None without
+        bounds."""
         if self.kv.bounds is None or not seqs:
             return None
+        seqs = [s if b < e else -1 for s, b, e in zip(seqs, begins, ends)]
         return (*(self._ints(x) for x in (seqs, begins, ends)), max(e - b for b, e in zip(begins, ends)))
 
     def _bounds(self, ranges):

@@ -188,8 +188,11 @@ def test_what_accept_and_draft_refuse(monkeypatch):
     store = w.block.pool.storage.clone()
     for seqs, paths in (([0], [[1, 0]]), ([0], [[0, 3]]), ([0], [[-1]]), ([0, 0], [[0], [0]]), ([0], [[0], [1]]), ([2], [[0]])):
         refused(seqs, paths)
+    for path in ([1, 2], [0, 2], [2]):       # nodes whose ancestors would go
+        refused([0], [path])
     w.block.kv.fork(0, [2])
     refused([0], [[1, 2]])                   # a fork holds the draft's pages
+    refused([0], [[0, 1, 2]])
     assert torch.equal(w.block.pool.storage.view(torch.int16), store.view(torch.int16)) and w.block.kv.length(0) == 23
     w.block.accept([1], [[1]])
     refused([1], [[0]])                      # over already
@@ -201,6 +204,28 @@ def test_what_accept_and_draft_refuse(monkeypatch):
         plain.block.step(*[plain.hidden(1)[0], [0], [1], plain.hidden(1)[1]], pages=3)
     with pytest.raises(B.LoraError):
         w.block.step(*[w.hidden(1)[0], [0], [1], w.hidden(1)[1]], pages=2, sink=1, recent=2)
+
+
+def test_drafts_dropped_and_replaced(monkeypatch):
+    """A draft accepted with no node of it, over a context that has none either; one that a step or a second draft follows."""
+    w = Watched(monkeypatch, False)
+    run = lambda call, n, *args: call(w.hidden(n)[0], *args, w.hidden(n)[1])
+    run(w.block.draft, 3, [0], [[-1, 0, 0]])
+    w.block.accept([0], [[]])
+    assert w.block.kv.length(0) == 0
+    run(w.block.step, 9, [0, 1], [9, 0])
+    run(w.block.draft, 3, [0, 1], [[-1, 0, 0], []])
+    run(w.block.draft, 2, [0], [[-1, 0]])    # the first draft's nodes are context now
+    with pytest.raises(B.LoraError):
+        w.block.accept([0], [[0, 2]])
+    w.block.accept([0], [[0]])
+    assert w.block.kv.length(0) == 13
+    run(w.block.draft, 3, [0], [[-1, 0, 0]])
+    w.block.kv.free([0])
+    run(w.block.step, 16, [0], [16])         # as long as the draft was
+    with pytest.raises(B.LoraError):
+        w.block.accept([0], [[0]])
+    assert w.block.kv.length(0) == 16
 
 
 def test_debug_build_reports_bad_places():
