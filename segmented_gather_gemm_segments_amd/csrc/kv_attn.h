@@ -241,7 +241,8 @@ __device__ __forceinline__ void load_tile(const char *k, const char *v, int64_t 
 //
 // 8-bit rows stay codes in LDS, half the bytes for each tile.  K's are widened as they are read, times the row's power of two;
 // V's without theirs, which multiplies the softmax weight instead (exactly, before it is rounded), since an
-// operand of V holds many positions.
+// operand of V holds many positions.  The batch of 64 tokens above in 8 bits, 680 MB: 126 us with its join, 5.4 TB/s.  Lists of
+// 64 pages of 64, 32 tokens, 64 / 8 heads of 128 in bf16, 537 MB: 96.6 us, 5.6 TB/s.
 constexpr int kRowPos = 32;
 
 template <int DP, bool F8>

@@ -93,7 +93,9 @@ __global__ __launch_bounds__(kThreads) void append_kernel(lora_kv_view kv, const
 }
 
 // Append to an 8-bit cache: P lanes, a power of two, per row (8 elements of K and of V each, those past head_dim idle), so
-// that the row's largest magnitude is an exchange between lanes and each row is read once.
+// that the row's largest magnitude is an exchange between lanes and each row is read once.  Bound by HBM where tokens are many
+// (11902 tokens, 8 heads of 128, 73 MB: 16.9 us, 4.4 TB/s), by the launch and a chain of three loads where they are few (256
+// tokens: 3.7 us).  A thread a row's 8 elements of both K and V gives two loads in flight and no second place to look up.
 template <int P>
 __global__ __launch_bounds__(kThreads) void append8_kernel(lora_kv8_view v, const uint16_t *__restrict__ k_new,
                                                            const uint16_t *__restrict__ v_new, int64_t token_stride,
@@ -131,7 +133,8 @@ __global__ __launch_bounds__(kThreads) void append8_kernel(lora_kv8_view v, cons
   }
 }
 
-// Rows read back: a thread takes 8 elements of a K row and of the V row beside it.
+// Rows read back: a thread takes 8 elements of a K row and of the V row beside it.  Bound by HBM, and by what it writes
+// (55126 tokens, 8 heads of 128 from 8 bits, 340 MB: 68.6 us, 4.95 TB/s, as fast as a plain copy); 200 tokens 2.9 us.
 template <bool F8>
 __global__ __launch_bounds__(kThreads) void read_kernel(lora_kv8_view v, uint16_t *__restrict__ k_out,
                                                         uint16_t *__restrict__ v_out, int64_t token_stride,
