@@ -419,6 +419,8 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
         s8[e] = ok ? sc[e >> 2][e & 3] : -INFINITY;
         keep |= (uint32_t)ok << e;
         hole |= ex && !ok;
+        // a position that is not kept may have any byte for its factor; absent ones have 0
+        if constexpr (F8 && M != Mask::kBlocks) vs[e] = ok ? vs[e] : 0.f;
         mt = fmaxf(mt, s8[e]);
       }
     }
@@ -487,9 +489,8 @@ __global__ __launch_bounds__(64 * W) void attn_rows_kernel(ArgsOf<F8, M> a) {
       }
     }
     if constexpr (F8) {
-      // a position that is not kept may have any byte for its factor
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p8[e] = keep >> e & 1 ? p8[e] * vs[e] : 0.f;
+      for (int e = 0; e < 8; ++e) p8[e] *= vs[e];
     }
     // rounded for the product only, as in the tile items
     const bf16x8_t pf = __builtin_bit_cast(
