@@ -120,6 +120,10 @@ def parse():
                     help="a decode step of the 70B-shape layer's attention block for 64 sequences of about CONTEXT "
                          "cached positions: 4-bit base projections with 64 rank-16 adapters' deltas, append and "
                          "attention over KV pages in the adapters' pool")
+    ap.add_argument("--kv-fp8", action="store_true", help="with --serving: the cache holds 8-bit rows")
+    ap.add_argument("--kv-pages", type=int, default=0, metavar="COUNT",
+                    help="with --serving: each token attends to that many pages (63 positions each, of 8-bit rows 123) of its "
+                         "sequence at most, chosen by the bounds of their keys")
     ap.add_argument("--floor", action="store_true",
                     help="only time bare streaming reads and a read-modify-write of given sizes "
                          "and workgroup counts (the device's floors for launches of that size)")
@@ -874,20 +878,40 @@ def run_floor(args, torch):
 def bench_serving(args, torch):
     """One decode step of the attention block (8192 wide, 64 query heads, 8 KV heads of 128, 64 rank-16
     adapters): q, k, v and o from 4-bit weights plus deltas, append, attention over 64 sequences of --serving
-    positions, as one graph; and the same launches in parts, each part a graph of its own."""
+    positions, as one graph; and the same launches in parts, each part a graph of its own.  With 8-bit rows or
+    selected pages the contexts are appended, so that the cache's exponents and bounds are those of its rows."""
     from segmented_gather_gemm_segments_amd import binding as B
     from segmented_gather_gemm_segments_amd import runner as R
     d, heads, kv_heads, dim, n_ad, rank, seqs, ctx = 8192, 64, 8, 128, 64, 16, 64, args.serving
-    pages = -(-(ctx + 1) // 64)
-    block = R.ServingBlock(d, heads, kv_heads, dim, n_ad, rank, seqs, pages, seqs * pages + 4 * n_ad + 8, seed=1)
-    block.pool.storage[:] = torch.randn(block.pool.storage.shape[1:], device="cuda").bfloat16() * 0.1
+    fp8, count = args.kv_fp8, args.kv_pages
+    pages = -(-(ctx + 1) // 64) + (1 + ctx // 512 if count else 0)  # a page ends in its bounds: fewer positions
+    block = R.ServingBlock(d, heads, kv_heads, dim, n_ad, rank, seqs, pages, seqs * pages + 4 * n_ad + 8, seed=1, fp8=fp8,
+                           bounds=count > 0)
+    plain = not fp8 and not count
+    if plain:
+        block.pool.storage[:] = torch.randn(block.pool.storage.shape[1:], device="cuda").bfloat16() * 0.1
     block.kv.extend(list(range(seqs)), [ctx] * seqs)
+    if not plain:
+        all_seqs = torch.arange(seqs, dtype=torch.int32, device="cuda")
+        for p0 in range(0, ctx, 1024):
+            n = min(1024, ctx - p0)
+            at = torch.arange(p0, p0 + n, dtype=torch.int32, device="cuda").repeat(seqs)
+            k, v = (torch.randn((seqs * n, kv_heads, dim), device="cuda").bfloat16() * 0.1 for _ in range(2))
+            B.lora_kv_append(block.kv.view, k, v, all_seqs.repeat_interleave(n), at)
+        if count:
+            B.lora_kv_bounds_update(block.kv.view, block.kv.bounds, all_seqs, torch.zeros_like(all_seqs),
+                                    torch.full_like(all_seqs, ctx), ctx)
     block.kv.extend(list(range(seqs)), [1] * seqs)
     stream = torch.cuda.Stream()
     ids = torch.arange(seqs, dtype=torch.int32, device="cuda") % n_ad
     seq = torch.arange(seqs, dtype=torch.int32, device="cuda")
     pos = torch.full((seqs,), ctx, dtype=torch.int32, device="cuda")
-    plan = B.lora_kv_attn_plan(list(range(seqs + 1)), list(range(seqs)), [ctx + 1] * seqs, heads, kv_heads, dim).to("cuda")
+    page_tokens = block.kv.view.desc.page_tokens
+    reach = min(count, -(-(ctx + 1) // page_tokens)) * page_tokens if count else ctx + 1
+    plan = B.lora_kv_attn_plan(list(range(seqs + 1)), list(range(seqs)), [reach] * seqs, heads, kv_heads, dim,
+                               blocks=count > 0).to("cuda")
+    blocks = torch.empty((seqs, kv_heads, max(count, 1)), dtype=torch.int32, device="cuda")
+    ranges = (seq, pos, pos + 1, 1) if count else None
     hidden = torch.randn((seqs, d), device="cuda").bfloat16()
     q, o, y = (torch.zeros((seqs, d), dtype=torch.bfloat16, device="cuda") for _ in range(3))
     k, v = (torch.zeros((seqs, kv_heads * dim), dtype=torch.bfloat16, device="cuda") for _ in range(2))
@@ -900,9 +924,18 @@ def bench_serving(args, torch):
         for name, src, dst in (("q", hidden, q), ("k", hidden, k), ("v", hidden, v), ("o", o, y)):
             B.lora_bgmv_fused(block.delta[name], ids, src, dst)
 
+    def attention(q, o):
+        if count:
+            B.lora_kv_block_select(block.kv.view, block.kv.bounds, seq, pos, q, blocks)
+            B.lora_kv_attn_blocks(block.kv.view, plan, blocks, pos, q, o)
+        else:
+            B.lora_kv_attn(block.kv.view, plan, q, o)
+
     def attend():
         B.lora_kv_append(block.kv.view, k.view(seqs, kv_heads, dim), v.view(seqs, kv_heads, dim), seq, pos)
-        B.lora_kv_attn(block.kv.view, plan, q.view(seqs, heads, dim), o.view(seqs, heads, dim))
+        if count:
+            B.lora_kv_bounds_update(block.kv.view, block.kv.bounds, *ranges)
+        attention(q.view(seqs, heads, dim), o.view(seqs, heads, dim))
 
     def on_stream(f):
         def run():
@@ -912,9 +945,9 @@ def bench_serving(args, torch):
     torch.cuda.synchronize()
     parts = {n: graph_span(torch, stream, [on_stream(f)] * args.steps, 3)
              for n, f in (("base_w4", base), ("delta", delta), ("append_attention", attend))}
-    step = graph_span(torch, stream, [on_stream(lambda: block.run(hidden, plan, seq, pos, ids))] * args.steps, 3)
+    step = graph_span(torch, stream, [on_stream(lambda: block.run(hidden, plan, seq, pos, ids, ranges, attention))] * args.steps, 3)
     print(json.dumps({"serving": {"sequences": seqs, "context": ctx, "d_model": d, "q_heads": heads, "kv_heads": kv_heads,
-                                  "head_dim": dim, "adapters": n_ad, "rank": rank, "steps": args.steps,
+                                  "head_dim": dim, "kv_rows": "fp8" if fp8 else "bf16", "kv_pages": count or None, "adapters": n_ad, "rank": rank, "steps": args.steps,
                                   "us_per_step": round(step * 1e6, 2), "tokens_per_s_per_layer": round(seqs / step, 1),
                                   "us_parts": {n: round(t * 1e6, 2) for n, t in parts.items()}}}), flush=True)
 

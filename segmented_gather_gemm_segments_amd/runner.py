@@ -514,12 +514,13 @@ class ServingBlock:
         if ranges is not None:
             B.lora_kv_bounds_update(self.kv.view, self.kv.bounds, *ranges)
 
-    def run(self, hidden, plan, token_seq, token_pos, token_adapter, ranges=None):
+    def run(self, hidden, plan, token_seq, token_pos, token_adapter, ranges=None, attend=None):
         """The device work of a step, launches only (every buffer is new; the plan and indices may serve many layers).
         Rows behind the plan's tokens are padding (token_seq -1, token_adapter -1): what stands in their y is unspecified.
-        ranges: of a cache with bounds, (seq, begin, end, most positions) for lora_kv_bounds_update."""
+        ranges: of a cache with bounds, (seq, begin, end, most positions) for lora_kv_bounds_update.  attend(q, out): the
+        attention, where it is another than lora_kv_attn with the plan."""
         return self._run(hidden, token_seq, token_pos, token_adapter, ranges,
-                         lambda q, out: B.lora_kv_attn(self.kv.view, plan, q, out))
+                         attend or (lambda q, out: B.lora_kv_attn(self.kv.view, plan, q, out)))
 
     def _run(self, hidden, token_seq, token_pos, token_adapter, ranges, attend):
         torch = _torch()
