@@ -65,7 +65,7 @@ lora_status lora_kv_bounds_update(const lora_kv_view *kv, const lora_kv_bounds *
  *              lora_kv_block_select_workspace says, few lists that may be long are scored by a launch of their own; lists
  *              are the same either way.  Contents on entry do not matter.  Calls that share it must not overlap, in graphs too.
  * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view, more than LORA_BLOCKS_MAX_PAGES pages in a sequence,
- * count, 2^24 tokens of all KV heads and more), LORA_EHIP. */
+ * count, 2^24 tokens of all KV heads and more, 2^22 where sequences may have more than 2048 pages), LORA_EHIP. */
 lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_kv_bounds *bounds, const int32_t *token_seq,
                                  const int32_t *token_pos, int32_t num_tokens, const void *q, int64_t q_token_stride,
                                  int64_t q_head_stride, int32_t q_heads, int32_t count, int32_t sink, int32_t recent,

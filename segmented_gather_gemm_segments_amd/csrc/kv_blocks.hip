@@ -385,6 +385,8 @@ __global__ __launch_bounds__(THREADS) void select_kernel(Select a) {
   }
 }
 
+constexpr int kMostKeys = 2048;  // of a workgroup of 512 threads or fewer
+
 // Whether a call's pages are scored by a launch of their own: few lists that may be long.
 bool splits(const lora_kv_view *kv, int64_t lists) { return lists > 0 && lists <= 64 && kv->max_pages > 512; }
 
@@ -453,14 +455,16 @@ extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_k
     return fail(LORA_EUNSUPPORTED, "sequences of up to %d pages, not %d", kv->max_pages, LORA_BLOCKS_MAX_PAGES);
   if (q_token_stride < 0 || q_head_stride < 0 || q_token_stride % 8 || q_head_stride % 8)
     return fail(LORA_EINVAL, "strides of q must be multiples of 8 elements, not negative");
-  if ((int64_t)num_tokens * kv->kv_heads >= 1 << 24) return fail(LORA_EUNSUPPORTED, "too many tokens for one launch");
+  const int64_t lists = (int64_t)num_tokens * kv->kv_heads;
+  if (lists >= 1 << 24 || too_many(lists, kv->max_pages > kMostKeys ? 1024 : 256))
+    return fail(LORA_EUNSUPPORTED, "too many tokens for one launch");
   if (num_tokens == 0) return ok();
   const bool some = kv->num_pages > 0 && kv->num_seqs > 0 && kv->max_pages > 0;
   if (!token_seq || !token_pos || !q || !blocks || (some && !bounds->rows)) return fail(LORA_EINVAL, "null pointer");
   if (workspace_bytes < 0 || ((uintptr_t)workspace & 15)) return fail(LORA_EINVAL, "workspace of %lld bytes must be 16-byte aligned", (long long)workspace_bytes);
   if (((uintptr_t)q & 15) || !aligned4(token_seq) || !aligned4(token_pos) || !aligned4(blocks))
     return fail(LORA_EINVAL, "q must be 16-byte aligned, the other arrays 4-byte");
-  const int64_t lists = (int64_t)num_tokens * kv->kv_heads, need = lists * kv->max_pages * (int64_t)sizeof(uint32_t);
+  const int64_t need = lists * kv->max_pages * (int64_t)sizeof(uint32_t);
   const int steps = (2 * kv->head_dim + 63) / 64, size = steps <= 2 ? 2 : steps <= 4 ? 4 : 8;
   Select a{*kv, *bounds, token_seq, token_pos, (const uint16_t *)q, q_token_stride, q_head_stride, q_heads / kv->kv_heads, count,
            sink, recent, blocks, nullptr};
@@ -484,9 +488,9 @@ extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_k
   const std::integral_constant<int, 512> medium{};
   const std::integral_constant<int, 1024> large{};
   if (kv->max_pages > 8192) launch(std::integral_constant<int, LORA_BLOCKS_MAX_PAGES>{}, large);
-  else if (kv->max_pages > 2048) launch(std::integral_constant<int, 8192>{}, large);
-  else if (lists <= 256) launch(std::integral_constant<int, 2048>{}, medium);
-  else if (lists <= 1280) launch(std::integral_constant<int, 2048>{}, small);
-  else launch(std::integral_constant<int, 2048>{}, least);
+  else if (kv->max_pages > kMostKeys) launch(std::integral_constant<int, 8192>{}, large);
+  else if (lists <= 256) launch(std::integral_constant<int, kMostKeys>{}, medium);
+  else if (lists <= 1280) launch(std::integral_constant<int, kMostKeys>{}, small);
+  else launch(std::integral_constant<int, kMostKeys>{}, least);
   return launched("page selection launch");
 }

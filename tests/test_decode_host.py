@@ -270,6 +270,16 @@ def test_bounds_and_selection_refusals():
     assert L().lora_kv_block_select_workspace(ref(view8()), 1, None) == B.LORA_EINVAL
 
 
+def test_selection_stays_within_one_launch():
+    """2^22 lists of 1024 threads would be 2^32."""
+    def select(tokens, max_pages, blocks):
+        v, b = view8(max_pages=max_pages), B.lora_kv_bounds(4096, 512, 144)
+        return L().lora_kv_block_select(ref(v), ref(b), 16, 16, tokens, 16, 256, 64, 4, 4, 1, 1, blocks, None, 0, None)
+    for max_pages, most in ((2048, 2**24 - 1), (2049, 2**22 - 1), (32768, 2**22 - 1)):
+        assert select(most // 2 + 1, max_pages, None) == B.LORA_EUNSUPPORTED
+        assert select(most // 2, max_pages, None) == B.LORA_EINVAL  # taken as far as the null pointer
+
+
 # ---------------------------------------------------------------- refusals of the binding, on tensors
 def test_binding_refusals():
     torch = pytest.importorskip("torch")
