@@ -57,7 +57,8 @@ lora_status lora_kv_attn_tree(const lora_kv_view *kv, const lora_attn_plan *plan
  * A request whose seq is negative is skipped (padding), one >= num_seqs or with a negative base too
  * (LORA_DEBUG_BAD_TOKEN); a position outside the sequence's pages (LORA_DEBUG_BAD_TOKEN) or on an absent page
  * (LORA_DEBUG_BAD_PAGE) skips its copy.  No two requests may write the same page, nor one read what another
- * writes.  Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view, 2^24 workgroups and more), LORA_EHIP.     */
+ * writes.  Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view, 2^24 workgroups and more, rows of a position in 2^31 pieces of 16
+ * bytes and more), LORA_EHIP.     */
 lora_status lora_kv_keep_path(const lora_kv_view *kv, const int32_t *seq, const int32_t *base, const int32_t *path,
                               int32_t num_reqs, int32_t max_path, hipStream_t stream);
 

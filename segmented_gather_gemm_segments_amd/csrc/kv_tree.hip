@@ -172,7 +172,7 @@ extern "C" lora_status lora_kv_keep_path(const lora_kv_view *kv, const int32_t *
   const bool f8 = kv->dtype == LORA_FP8_E4M3;
   const int size = f8 ? 1 : 2, chunks = kv->head_dim * size / 16;
   const int64_t units = 2 * (int64_t)kv->kv_heads * (chunks + (f8 ? 1 : 0)), groups = (units + kThreads - 1) / kThreads;
-  if (groups * num_reqs >= 1 << 24) return fail(LORA_EUNSUPPORTED, "paths too many for one launch");
+  if (groups * num_reqs >= 1 << 24 || units > INT32_MAX) return fail(LORA_EUNSUPPORTED, "paths too many for one launch");
   hipLaunchKernelGGL(keep_path_kernel, dim3((unsigned)(groups * num_reqs)), dim3(kThreads), 0, stream, view8(kv), seq, base,
                      path, max_path, chunks, size, (int)units, (int)groups);
   const hipError_t e = hipGetLastError();

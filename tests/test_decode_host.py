@@ -280,6 +280,11 @@ def test_selection_stays_within_one_launch():
         assert select(most // 2, max_pages, None) == B.LORA_EINVAL  # taken as far as the null pointer
 
 
+def test_path_pieces_are_counted_in_31_bits():
+    v = view8(kv_heads=2**27, head_dim=128)
+    assert L().lora_kv_keep_path(ref(v), 16, 16, 16, 1, 4, None) == B.LORA_EUNSUPPORTED
+
+
 # ---------------------------------------------------------------- refusals of the binding, on tensors
 def test_binding_refusals():
     torch = pytest.importorskip("torch")
