@@ -160,22 +160,30 @@ __device__ __forceinline__ Token token_of(const Select &a, int t) {
 
 // Keys of pages [begin, end) of token t's sequence and KV head h, each given to store(page, key, whether it is the first for
 // its page) as often as there are 16 query heads; returns the page's key so far.  S: products of 64 numbers that a row of
-// bounds takes at most; waves [0, WAVES) of the workgroup.
-template <int WAVES, int S, typename Store>
+// bounds takes at most; waves [0, WAVES) of the workgroup, with U groups of 16 pages in flight each.
+template <int WAVES, int U, int S, typename Store>
 __device__ __forceinline__ void score(const Select &a, const Token &token, int t, int h, int begin, int end, char (*qc)[512],
                                       float *unit, Store store) {
-  constexpr int U = S <= 4 && WAVES > 4 ? 4 : 2;
   const lora_kv_view &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 15, fg = lane >> 4;
   const int D = kv.head_dim, steps = (2 * D + 63) / 64;
-  int page[U], f[U];
+  // the next turn's pages are looked up a load sooner, where registers are left for it (320 lists of up to 1000 pages: 28 us,
+  // else 31; heads of 256, 694 lists of up to 469: 23 and 21.4)
+  constexpr bool kAhead = S <= 4;
+  constexpr int kTurn = 16 * U * WAVES;
+  const int first = begin + 16 * wave;
+  int page[U], next[U], f[U];
   i32x4_t b[U][S];
-  auto load = [&](int p0) {
+  auto look_up = [&](int p0) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) page[i] = token.table[min(p0 + 16 * WAVES * i + fr, end - 1)];
+    for (int i = 0; i < U; ++i) next[i] = token.table[min(p0 + 16 * WAVES * i + fr, end - 1)];
+  };
+  auto load = [&](int p0) {
+    if (!kAhead) look_up(p0);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
+      page[i] = next[i];
       KV_CHECK((unsigned)page[i] < (unsigned)kv.num_pages || fg != 0, LORA_DEBUG_BAD_PAGE);
       // an absent page's row is not read
       const bool there = (unsigned)page[i] < (unsigned)kv.num_pages;
@@ -185,8 +193,9 @@ __device__ __forceinline__ void score(const Select &a, const Token &token, int t
       for (int k = 0; k < S; ++k)
         b[i][k] = *reinterpret_cast<const i32x4_t *>(there && k < steps ? row + 64 * k + 16 * fg : (const char *)&g_zeros);
     }
+    if (kAhead) look_up(p0 + kTurn < end ? p0 + kTurn : first);
   };
-  const int first = begin + 16 * wave;
+  if (kAhead) look_up(first);
   for (int g0 = 0; g0 < a.group; g0 += 16) {
     if (first < end) load(first);  // on its way while the queries are rounded
     if (g0) __syncthreads();       // the rows before have been read
@@ -216,7 +225,7 @@ __device__ __forceinline__ void score(const Select &a, const Token &token, int t
       if (c == 0) unit[g] = exponent((uint32_t)(127 + e));
     }
     __syncthreads();
-    for (int p0 = first; p0 < end; p0 += 16 * U * WAVES) {
+    for (int p0 = first; p0 < end; p0 += kTurn) {
       if (p0 != first) load(p0);
       i32x4_t sum[U];
 #pragma unroll
@@ -245,7 +254,7 @@ __device__ __forceinline__ void score(const Select &a, const Token &token, int t
   }
 }
 
-constexpr int kScorePages = 256;  // of a workgroup that only scores: one turn of its 4 waves (two above head_dim 128)
+constexpr int kScorePages = 256;  // of a workgroup that only scores: two turns of its 4 waves
 
 template <int S>
 __global__ __launch_bounds__(256) void score_kernel(Select a, int parts) {
@@ -256,7 +265,7 @@ __global__ __launch_bounds__(256) void score_kernel(Select a, int parts) {
   const int begin = part * kScorePages, end = min(token.n, begin + kScorePages);
   if (token.n <= a.count || begin >= end) return;
   uint32_t *keys = a.keys + (int64_t)list * a.kv.max_pages;
-  score<4, S>(a, token, t, h, begin, end, qc, unit, [&](int p, uint32_t key, bool first) { keys[p] = first ? key : max(keys[p], key); });
+  score<4, 2, S>(a, token, t, h, begin, end, qc, unit, [&](int p, uint32_t key, bool first) { keys[p] = first ? key : max(keys[p], key); });
 }
 
 template <int KEYS, int THREADS, int S>
@@ -279,7 +288,7 @@ __global__ __launch_bounds__(THREADS) void select_kernel(Select a) {
     const uint32_t *from = a.keys + (int64_t)blockIdx.x * a.kv.max_pages;
     for (int i = tid; i < n; i += THREADS) keys[i] = from[i];
   } else {
-    score<kWaves, S>(a, token, t, h, 0, n, qc, unit, [&](int p, uint32_t key, bool first) { keys[p] = first ? key : max(keys[p], key); });
+    score<kWaves, (S <= 4 && THREADS > 256) ? 4 : 2, S>(a, token, t, h, 0, n, qc, unit, [&](int p, uint32_t key, bool first) { keys[p] = first ? key : max(keys[p], key); });
   }
   // Of the keys between the first and the last pages, which are listed anyway, the need-th largest: 8 bits at a time from the
   // highest in which they differ.  Counted from the least of them, so that their first digits spread over the bins (a
