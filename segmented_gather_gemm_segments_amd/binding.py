@@ -1140,6 +1140,17 @@ class KvBounds:
         ps, hs = (st if n > 1 else 0 for n, st in zip(rows.shape[:2], rows.stride()))
         self.rows, self.desc = rows, lora_kv_bounds(_dptr(rows), ps, hs)
         self.ref, self.index = ctypes.byref(self.desc), rows.get_device()
+        self.pages, self.heads = d.num_pages, (d.kv_heads, d.head_dim)
+
+
+def _bounds_of(view: KvView, bounds: KvBounds):
+    """Checks that the bounds have a row for every page and head of this view, which need not be the one they were made with."""
+    d = view.desc
+    if bounds.index != view.index:
+        _refuse(f"bounds are on {bounds.rows.device}, not {view.device}")
+    if bounds.pages < d.num_pages or bounds.heads != (d.kv_heads, d.head_dim):
+        _refuse(f"bounds of {bounds.pages} pages, {bounds.heads[0]} KV heads of {bounds.heads[1]}: the view has {d.num_pages}, "
+                f"{d.kv_heads} of {d.head_dim}")
 
 
 def lora_kv_bounds_update(view: KvView, bounds: KvBounds, seq, begin, end, max_tokens: int, stream=None):
@@ -1149,8 +1160,7 @@ def lora_kv_bounds_update(view: KvView, bounds: KvBounds, seq, begin, end, max_t
     n = seq.numel()
     if begin.numel() != n or end.numel() != n:
         _refuse(f"{n} sequences, {begin.numel()} first and {end.numel()} last positions")
-    if bounds.index != view.index:
-        _refuse(f"bounds are on {bounds.rows.device}, not {view.device}")
+    _bounds_of(view, bounds)
     if view.index < 0:
         _gpu(view.device)
     _launch("lora_kv_bounds_update", view.index, stream, view.ref, bounds.ref, seq.data_ptr(), begin.data_ptr(), end.data_ptr(), n,
@@ -1175,8 +1185,7 @@ def lora_kv_block_select(view: KvView, bounds: KvBounds, token_seq, token_pos, q
             blocks.shape[0] < n or blocks.shape[1] != d.kv_heads):
         _refuse(f"{n} sequences, {token_pos.numel()} positions, q {tuple(q.shape)} and blocks {tuple(blocks.shape)} for "
                 f"{d.kv_heads} KV heads of {d.head_dim}")
-    if bounds.index != view.index:
-        _refuse(f"bounds are on {bounds.rows.device}, not {view.device}")
+    _bounds_of(view, bounds)
     if view.index < 0:
         _gpu(view.device)
     if workspace is None:

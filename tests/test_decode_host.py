@@ -320,3 +320,20 @@ def test_binding_refusals():
                  lambda: B.lora_kv_block_select(view, bounds, i(0), i(0), q, blocks[:, :1]), lambda: B.lora_kv_attn_blocks(view, plan, blocks[:, 0], i(0), q, q),
                  lambda: B.lora_kv_attn_blocks(view, plan, blocks, i(), q, q), lambda: B.lora_kv_read(view, i(0), i(0), rows.float(), rows)):
         refused(B.LORA_EINVAL, call)
+
+
+@pytest.mark.parametrize("pages,heads,dim", [(5, 2, 64), (4, 4, 64), (4, 1, 64), (4, 2, 48), (4, 2, 40), (4, 2, 128)])
+def test_bounds_of_another_view(pages, heads, dim):
+    """Rows that a view's pages, heads or head size would pass the end of, or read as another's, are refused by name."""
+    torch = pytest.importorskip("torch")
+    table, i = torch.zeros((1, 4), dtype=torch.int32), lambda *x: torch.tensor(x, dtype=torch.int32)
+    make = lambda p, h, d: B.KvView(*(torch.zeros((p, h, 8, d), dtype=torch.bfloat16) for _ in "kv"), table)
+    bounds = B.KvBounds(make(4, 2, 64), torch.zeros((4, 2, B.lora_kv_bounds_row_bytes(64)), dtype=torch.uint8))
+    view = make(pages, heads, dim)
+    for call in (lambda v, h, d: B.lora_kv_bounds_update(v, bounds, i(0), i(0), i(1), 1),
+                 lambda v, h, d: B.lora_kv_block_select(v, bounds, i(0), i(0), torch.zeros((1, 4, d), dtype=torch.bfloat16), torch.zeros((1, h, 4), dtype=torch.int32))):
+        with pytest.raises(B.LoraError, match="bounds of 4 pages, 2 KV heads of 64"):
+            call(view, heads, dim)
+        for fits in (make(4, 2, 64), make(3, 2, 64)):
+            with pytest.raises(B.LoraError, match="on a GPU"):  # refused for its device alone
+                call(fits, 2, 64)
