@@ -70,7 +70,8 @@ lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_kv_bounds *b
                                  const int32_t *token_pos, int32_t num_tokens, const void *q, int64_t q_token_stride,
                                  int64_t q_head_stride, int32_t q_heads, int32_t count, int32_t sink, int32_t recent,
                                  int32_t *blocks, void *workspace, int64_t workspace_bytes, hipStream_t stream);
-/* Workspace bytes for num_tokens tokens (0: it would not be used).  Host only.  Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view). */
+/* Workspace bytes for num_tokens tokens (0: it would not be used).  Host only.  Errors: LORA_EINVAL, LORA_EUNSUPPORTED (the view
+ * and the number of tokens that lora_kv_block_select refuses).                                              */
 lora_status lora_kv_block_select_workspace(const lora_kv_view *kv, int32_t num_tokens, int64_t *bytes);
 
 /* lora_kv_attn over listed pages: token t and KV head h keep the positions j <= token_pos[t] on the pages

@@ -1168,6 +1168,7 @@ def lora_kv_bounds_update(view: KvView, bounds: KvBounds, seq, begin, end, max_t
 
 
 def lora_kv_block_select_workspace(view: KvView, num_tokens: int) -> int:
+    """Bytes of workspace; refuses a view and a number of tokens that lora_kv_block_select would."""
     out = ctypes.c_int64(0)
     _check(lib().lora_kv_block_select_workspace(view.ref, num_tokens, ctypes.byref(out)))
     return int(out.value)

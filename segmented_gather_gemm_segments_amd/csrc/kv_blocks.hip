@@ -404,6 +404,16 @@ lora_status launched(const char *what) {
   return e == hipSuccess ? ok() : hip_fail(e, what);
 }
 
+// Checks that one launch can list the pages of so many tokens.
+lora_status check_lists(const lora_kv_view *kv, int32_t num_tokens) {
+  if (kv->max_pages > LORA_BLOCKS_MAX_PAGES)
+    return fail(LORA_EUNSUPPORTED, "sequences of up to %d pages, not %d", kv->max_pages, LORA_BLOCKS_MAX_PAGES);
+  const int64_t lists = (int64_t)num_tokens * kv->kv_heads;
+  if (lists >= 1 << 24 || too_many(lists, kv->max_pages > kMostKeys ? 1024 : 256))
+    return fail(LORA_EUNSUPPORTED, "too many tokens for one launch");
+  return LORA_OK;
+}
+
 lora_status check_bounds(const lora_kv_bounds *b) {
   if (!b) return fail(LORA_EINVAL, "null bounds");
   if (((uintptr_t)b->rows & 15) || b->page_stride < 0 || b->head_stride < 0 || b->page_stride % 16 || b->head_stride % 16)
@@ -439,9 +449,10 @@ extern "C" lora_status lora_kv_bounds_update(const lora_kv_view *kv, const lora_
 }
 
 extern "C" lora_status lora_kv_block_select_workspace(const lora_kv_view *kv, int32_t num_tokens, int64_t *bytes) {
-  const lora_status st = check_view(kv);
+  lora_status st = check_view(kv);
   if (st != LORA_OK) return st;
   if (!bytes || num_tokens < 0) return fail(LORA_EINVAL, "%d tokens, or null bytes", num_tokens);
+  if ((st = check_lists(kv, num_tokens)) != LORA_OK) return st;
   const int64_t lists = (int64_t)num_tokens * kv->kv_heads;
   *bytes = splits(kv, lists) ? lists * kv->max_pages * (int64_t)sizeof(uint32_t) : 0;
   return ok();
@@ -460,13 +471,10 @@ extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_k
   if (count < 1 || sink < 0 || recent < 1 || (int64_t)sink + recent > count)
     return fail(LORA_EINVAL, "lists of %d pages, the first %d and the last %d among them", count, sink, recent);
   if (count > LORA_BLOCKS_MAX_COUNT) return fail(LORA_EUNSUPPORTED, "lists of %d pages, not 1..%d", count, LORA_BLOCKS_MAX_COUNT);
-  if (kv->max_pages > LORA_BLOCKS_MAX_PAGES)
-    return fail(LORA_EUNSUPPORTED, "sequences of up to %d pages, not %d", kv->max_pages, LORA_BLOCKS_MAX_PAGES);
   if (q_token_stride < 0 || q_head_stride < 0 || q_token_stride % 8 || q_head_stride % 8)
     return fail(LORA_EINVAL, "strides of q must be multiples of 8 elements, not negative");
+  if ((st = check_lists(kv, num_tokens)) != LORA_OK) return st;
   const int64_t lists = (int64_t)num_tokens * kv->kv_heads;
-  if (lists >= 1 << 24 || too_many(lists, kv->max_pages > kMostKeys ? 1024 : 256))
-    return fail(LORA_EUNSUPPORTED, "too many tokens for one launch");
   if (num_tokens == 0) return ok();
   const bool some = kv->num_pages > 0 && kv->num_seqs > 0 && kv->max_pages > 0;
   if (!token_seq || !token_pos || !q || !blocks || (some && !bounds->rows)) return fail(LORA_EINVAL, "null pointer");

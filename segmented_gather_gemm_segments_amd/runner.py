@@ -7,6 +7,7 @@ Used by the GPU tests, the benchmark and the smoke check.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional
 
@@ -395,32 +396,52 @@ class ServingBlock:
                 B._refuse(f"{name} {tuple(rows.shape)}: {(t, width)} wanted for {t} adapter ids")
         return t
 
-    def _grow(self, hidden, seqs, new_tokens, token_adapter):
-        """Checks a step, extends its sequences and returns (seqs, new tokens, lengths, starts, and on the device each
-        token's sequence and position); None where it has no tokens."""
-        torch = _torch()
+    def _new(self, hidden, seqs, new_tokens, token_adapter):
+        """Checks the rows of a step; returns its sequences, new tokens and number of tokens."""
         seqs, new_tokens = [int(s) for s in seqs], [int(n) for n in new_tokens]
         t = self._rows(token_adapter, ("hidden", hidden, self.d_model))
         if len(seqs) != len(new_tokens) or any(n < 0 for n in new_tokens) or sum(new_tokens) != t:
             B._refuse(f"{len(seqs)} sequences grow by {new_tokens}, hidden has {t} tokens")
-        self.kv.extend(seqs, new_tokens)
-        for s, n in zip(seqs, new_tokens):
-            if n:
-                self._drafts.pop(s, None)  # it goes on as it is
-        if t == 0:
-            return None
-        lens = [self.kv.length(s) for s in seqs]
+        return seqs, new_tokens, t
+
+    def _places(self, seqs, new_tokens):
+        """What a step will need, before any sequence grows: lengths after it, starts, on the device each token's sequence and
+        position, and the ranges whose bounds change."""
+        B._not_capturing("sequences cannot grow")
+        lens = [max(self.kv.length(s), 0) + n for s, n in zip(seqs, new_tokens)]
+        if max(lens) > self.kv.view.max_kv:
+            B._refuse(f"sequences of {lens[:8]} positions, the cache holds {self.kv.view.max_kv} of each")
         starts = np.concatenate([[0], np.cumsum(new_tokens)]).astype(np.int32)
         seq = np.repeat(np.asarray(seqs, np.int32), new_tokens)
         pos = np.concatenate([np.arange(n - q, n, dtype=np.int32) for q, n in zip(new_tokens, lens)])
-        return seqs, new_tokens, lens, starts, self._ints(seq), self._ints(pos)
+        return lens, starts, self._ints(seq), self._ints(pos), self._ranges(seqs, [n - q for q, n in zip(new_tokens, lens)], lens)
+
+    @contextlib.contextmanager
+    def _grown(self, seqs, new_tokens):
+        """The sequences longer by their new tokens, which end their drafts (the sequence goes on as it is).  A body that
+        raises leaves both as they were."""
+        before = [self.kv.length(s) for s in seqs]
+        self.kv.extend(seqs, new_tokens)
+        drafts = {s: self._drafts.pop(s) for s, n in zip(seqs, new_tokens) if n and s in self._drafts}
+        try:
+            yield
+        except BaseException:
+            self._drafts.update(drafts)
+            for s, n in zip(seqs, before):
+                self.kv.free([s]) if n < 0 else self.kv.truncate(s, n)
+            # the page that a growth began on may hold bounds of rows that are gone
+            page = self.kv.view.desc.page_tokens
+            part = [(s, n) for s, n, new in zip(seqs, before, new_tokens) if new and n > 0 and n % page]
+            if self.kv.bounds is not None and part:
+                self._bounds(self._ranges([s for s, _ in part], [n - 1 for _, n in part], [n for _, n in part]))
+            raise
 
     def _ints(self, values):
         return _torch().from_numpy(np.ascontiguousarray(values, np.int32)).to(self.device)
 
     def step(self, hidden, seqs, new_tokens, token_adapter, pages: Optional[int] = None, sink: int = 1, recent: int = 2):
         """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device.  A call that
-        is refused leaves the cache as it is.  pages: each token attends to that many pages of its sequence at most for
+        raises leaves the sequences and drafts as they are.  pages: each token attends to that many pages of its sequence at most for
         each KV head, the first `sink`, the last `recent` and those that the bounds of their keys choose."""
         torch = _torch()
         if pages is not None:
@@ -428,47 +449,55 @@ class ServingBlock:
                 B._refuse("pages are chosen by the bounds of their keys: make the block with bounds=True")
             if not 0 <= sink < sink + recent <= pages <= B.LORA_BLOCKS_MAX_COUNT or recent < 1:
                 B._refuse(f"{pages} pages, the first {sink} and the last {recent} among them")
-        grown = self._grow(hidden, seqs, new_tokens, token_adapter)
-        if grown is None:
+        seqs, new_tokens, t = self._new(hidden, seqs, new_tokens, token_adapter)
+        if t == 0:
+            self.kv.extend(seqs, new_tokens)
             return torch.empty_like(hidden)
-        seqs, new_tokens, lens, starts, seq, pos = grown
-        ranges = self._ranges(seqs, [n - q for q, n in zip(new_tokens, lens)], lens)
+        view = self.kv.view
+        if pages is not None:
+            need = B.lora_kv_block_select_workspace(view, t)  # refuses what the selection would
+        lens, starts, seq, pos, ranges = self._places(seqs, new_tokens)
         if pages is None:
             plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim).to(self.device)
-            return self.run(hidden, plan, seq, pos, token_adapter, ranges)
-        view, t = self.kv.view, int(starts[-1])
+            with self._grown(seqs, new_tokens):
+                return self.run(hidden, plan, seq, pos, token_adapter, ranges)
         most = min(pages, max(-(-n // view.desc.page_tokens) for n in lens)) * view.desc.page_tokens
         plan = B.lora_kv_attn_plan(np.arange(t + 1), np.repeat(seqs, new_tokens), [most] * t, self.q_heads, self.kv_heads,
                                    self.head_dim, blocks=True).to(self.device)
         blocks = torch.empty((t, self.kv_heads, pages), dtype=torch.int32, device=self.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
 
         def attend(q, out):
-            B.lora_kv_block_select(view, self.kv.bounds, seq, pos, q, blocks, sink=sink, recent=recent)
+            B.lora_kv_block_select(view, self.kv.bounds, seq, pos, q, blocks, sink=sink, recent=recent, workspace=workspace)
             B.lora_kv_attn_blocks(view, plan, blocks, pos, q, out)
-        return self._run(hidden, seq, pos, token_adapter, ranges, attend)
+        with self._grown(seqs, new_tokens):
+            return self._run(hidden, seq, pos, token_adapter, ranges, attend)
 
     def draft(self, hidden, seqs, parents, token_adapter):
         """Runs a tree of drafted tokens for each sequence: parents lists, for each of them, its nodes' parents (a number
         below the node's own, or -1 for the context); hidden [T, d_model] of all nodes.  The nodes take the sequences' next
-        positions until ``accept`` keeps a path of them."""
+        positions until ``accept`` keeps a path of them.  A call that raises leaves the sequences and drafts as they are."""
         torch = _torch()
         parents = [[int(p) for p in row] for row in parents]
         for row in parents:
             if len(row) > B.LORA_TREE_MAX_NODES or any(not -1 <= p < i for i, p in enumerate(row)):
                 B._refuse(f"parents {row[:8]}...: each is -1 or the number of an earlier node, {B.LORA_TREE_MAX_NODES} nodes at most")
-        grown = self._grow(hidden, seqs, [len(row) for row in parents], token_adapter)
-        if grown is None:
+        seqs, nodes, t = self._new(hidden, seqs, [len(row) for row in parents], token_adapter)
+        if t == 0:
+            self.kv.extend(seqs, nodes)
             return torch.empty_like(hidden)
-        seqs, nodes, lens, starts, seq, pos = grown
-        self._drafts.update({s: (n - len(row), row) for s, row, n in zip(seqs, parents, lens) if row})
+        lens, starts, seq, pos, ranges = self._places(seqs, nodes)
         plan = B.lora_kv_attn_plan(starts, seqs, lens, self.q_heads, self.kv_heads, self.head_dim, tree=True).to(self.device)
-        tree = B.Tree(int(starts[-1]), max(nodes), self.device)
+        tree = B.Tree(t, max(nodes), self.device)
         dev_starts, dev_parents = self._ints(starts), self._ints(np.concatenate([np.asarray(row, np.int32) for row in parents]))
 
         def attend(q, out):
             B.lora_tree_mask(dev_starts, dev_parents, tree)
             B.lora_kv_attn_tree(self.kv.view, plan, tree, q, out)
-        return self._run(hidden, seq, pos, token_adapter, self._ranges(seqs, [n - q for q, n in zip(nodes, lens)], lens), attend)
+        with self._grown(seqs, nodes):
+            y = self._run(hidden, seq, pos, token_adapter, ranges, attend)
+        self._drafts.update({s: (n - len(row), row) for s, row, n in zip(seqs, parents, lens) if row})
+        return y
 
     def accept(self, seqs, paths):
         """Ends the drafts of some sequences: each keeps the nodes paths[r] (none, or one below the context and then each
@@ -494,21 +523,26 @@ class ServingBlock:
         rows = np.full((len(seqs), max([len(p) for p in paths] + [1])), -1, np.int32)
         for r, path in enumerate(paths):
             rows[r, :len(path)] = path
+        # the page that a draft began on may hold bounds of nodes that are gone
+        ranges = self._ranges(seqs, [max(b - 1, 0) for b in bases], [b + len(p) for b, p in zip(bases, paths)])
         with B._On(self.device, None):
             B.lora_kv_keep_path(self.kv.view, self._ints(seqs), self._ints(bases), self._ints(rows))
             for s, base, path in zip(seqs, bases, paths):
                 self.kv.truncate(s, base + len(path))
                 del self._drafts[s]
-            # the page that a draft began on may hold bounds of nodes that are gone
-            self._bounds(self._ranges(seqs, [max(b - 1, 0) for b in bases], [b + len(p) for b, p in zip(bases, paths)]))
+            self._bounds(ranges)
 
     def _ranges(self, seqs, begins, ends):
         """Positions whose pages' bounds have to be written, on the device (a sequence with none is skipped); None without
-        bounds."""
+        bounds.  Refuses what lora_kv_bounds_update would, so that it can be asked before anything changes."""
         if self.kv.bounds is None or not seqs:
             return None
         seqs = [s if b < e else -1 for s, b, e in zip(seqs, begins, ends)]
-        return (*(self._ints(x) for x in (seqs, begins, ends)), max(e - b for b, e in zip(begins, ends)))
+        d, most = self.kv.view.desc, max(e - b for b, e in zip(begins, ends))
+        pages = min((most + d.page_tokens - 2) // d.page_tokens + 1, d.max_pages)
+        if pages * d.kv_heads * len(seqs) >= 1 << 24:
+            raise B.LoraError(B.LORA_EUNSUPPORTED, f"bounds of {len(seqs)} ranges of up to {pages} pages, {d.kv_heads} heads each")
+        return (*(self._ints(x) for x in (seqs, begins, ends)), most)
 
     def _bounds(self, ranges):
         if ranges is not None:
