@@ -441,8 +441,8 @@ class ServingBlock:
 
     def step(self, hidden, seqs, new_tokens, token_adapter, pages: Optional[int] = None, sink: int = 1, recent: int = 2):
         """hidden [T, d_model] of the new tokens, sequence by sequence; token_adapter int32 [T] on the device.  A call that
-        raises leaves the sequences and drafts as they are.  pages: each token attends to that many pages of its sequence at most for
-        each KV head, the first `sink`, the last `recent` and those that the bounds of their keys choose."""
+        raises leaves the sequences and drafts as they are.  pages: each token attends to that many pages of its sequence
+        at most for each KV head, the first `sink`, the last `recent` and those that the bounds of their keys choose."""
         torch = _torch()
         if pages is not None:
             if self.kv.bounds is None:
@@ -523,8 +523,9 @@ class ServingBlock:
         rows = np.full((len(seqs), max([len(p) for p in paths] + [1])), -1, np.int32)
         for r, path in enumerate(paths):
             rows[r, :len(path)] = path
-        # the page that a draft began on may hold bounds of nodes that are gone
-        ranges = self._ranges(seqs, [max(b - 1, 0) for b in bases], [b + len(p) for b, p in zip(bases, paths)])
+        # the page that a draft began on may hold bounds of nodes that are gone; one that ends where it began holds none, and
+        # may be another sequence's too
+        ranges = self._ranges(seqs, [b - 1 if b % page_tokens else b for b in bases], [b + len(p) for b, p in zip(bases, paths)])
         with B._On(self.device, None):
             B.lora_kv_keep_path(self.kv.view, self._ints(seqs), self._ints(bases), self._ints(rows))
             for s, base, path in zip(seqs, bases, paths):

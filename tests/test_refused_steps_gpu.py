@@ -1,4 +1,5 @@
-"""Refused steps of the serving block on the GPU: the cache goes on as one that never saw them, bit for bit."""
+"""Refused steps of the serving block on the GPU, after which the cache goes on as one that never saw them, bit for bit; and drafts of
+forks accepted where their pages part."""
 import pytest
 
 from segmented_gather_gemm_segments_amd import binding as B
@@ -67,3 +68,24 @@ def test_a_step_that_fails_late(monkeypatch, fp8):
         assert [block.kv.length(s) for s in range(4)] == [4 * page + 5, 22, -1, -1]
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_siblings_accepted_at_a_page_border(fp8):
+    """The page before the drafts is both forks': its bounds are not written."""
+    block = make(fp8)
+    page = block.kv.stats()["page_tokens"]
+    call(block.step, 2 * page, 1, [0], [2 * page])
+    block.kv.fork(0, [1])
+    call(block.draft, 5, 2, [0, 1], [[-1, 0, 0], [-1, -1]])
+    shared = torch.from_numpy(block.kv.pages(0)[:2]).cuda().long()
+    block.kv.bounds.rows[shared] = 0x55
+    block.accept([0, 1], [[0, 2], []])
+    assert bool((block.kv.bounds.rows[shared] == 0x55).all())
+    assert [block.kv.length(s) for s in (0, 1)] == [2 * page + 2, 2 * page]
+    own = int(block.kv.pages(0)[2])
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    got = block.kv.bounds.rows[own].clone()
+    fresh = torch.zeros_like(block.kv.bounds.rows)
+    B.lora_kv_bounds_update(block.kv.view, B.KvBounds(block.kv.view, fresh), i32(0), i32(2 * page), i32(2 * page + 2), 2)
+    assert torch.equal(got[..., :-12], fresh[own][..., :-12])

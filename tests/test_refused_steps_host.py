@@ -147,3 +147,23 @@ def test_a_sequence_that_was_not_in_use_is_not_afterwards(monkeypatch):
     with pytest.raises(B.LoraError):
         grow(b, [0, 2], [3, 0])
     assert state(b) == ([-1] * 4, [[]] * 4, {}, 0)
+
+
+@pytest.mark.parametrize("paths", [[[0, 1], [1]], [[], [0]], [[], []]])
+def test_siblings_accepted_at_a_page_border(monkeypatch, paths):
+    """Forks whose context ends with a page share it: no two ranges of bounds touch it, and none has to."""
+    b = Block(monkeypatch)
+    grow(b, [0], [2 * b.page])
+    b.kv.fork(0, [1, 2])
+    grow(b, [2], [3])  # and one that ends within a page
+    b.draft(rows(6), [0, 1, 2], [[-1, 0], [-1, -1], [-1, -1]], ids(6))
+    shared, b.calls[:] = b.kv.pages(0)[:2].tolist(), []
+    b.accept([0, 1, 2], [*paths, []])
+    written = []
+    for name, args in b.calls:
+        if name == "lora_kv_bounds_update":
+            for s, begin, end in zip(*(x.tolist() for x in args[2:5])):
+                if s >= 0:
+                    written += b.kv.pages(s)[begin // b.page: -(-end // b.page)].tolist()
+    assert len(written) == len(set(written)) and not set(written) & set(shared)
+    assert set(written) == {int(b.kv.pages(s)[2]) for s, p in ((0, paths[0]), (1, paths[1]), (2, [0])) if p}
