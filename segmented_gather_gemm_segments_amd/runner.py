@@ -534,16 +534,23 @@ class ServingBlock:
             self._bounds(ranges)
 
     def _ranges(self, seqs, begins, ends):
-        """Positions whose pages' bounds have to be written, on the device (a sequence with none is skipped); None without
+        """Positions whose pages' bounds have to be written, on the device (a sequence with none has no range); None without
         bounds.  Refuses what lora_kv_bounds_update would, so that it can be asked before anything changes."""
         if self.kv.bounds is None or not seqs:
             return None
-        seqs = [s if b < e else -1 for s, b, e in zip(seqs, begins, ends)]
-        d, most = self.kv.view.desc, max(e - b for b, e in zip(begins, ends))
-        pages = min((most + d.page_tokens - 2) // d.page_tokens + 1, d.max_pages)
-        if pages * d.kv_heads * len(seqs) >= 1 << 24:
-            raise B.LoraError(B.LORA_EUNSUPPORTED, f"bounds of {len(seqs)} ranges of up to {pages} pages, {d.kv_heads} heads each")
-        return (*(self._ints(x) for x in (seqs, begins, ends)), most)
+        # The call has workgroups for as many pages of every range as the longest one holds: ranges are cut at page borders to
+        # a mean one's pages, so that a prompt beside many single tokens takes as many as there are pages, about.
+        d = self.kv.view.desc
+        page = d.page_tokens
+        held = [-(-e // page) - b // page if b < e else 0 for b, e in zip(begins, ends)]
+        most = max(1, -(-sum(held) // len(held)))
+        cut = [(s, max(b, j * page), min(e, (j + most) * page)) for s, b, e, n in zip(seqs, begins, ends, held)
+               for j in range(b // page, b // page + n, most)]
+        longest = max([e - b for _, b, e in cut] + [0])
+        pages = min((longest + page - 2) // page + 1, d.max_pages)
+        if pages * d.kv_heads * len(cut) >= 1 << 24:
+            raise B.LoraError(B.LORA_EUNSUPPORTED, f"bounds of {len(cut)} ranges of up to {pages} pages, {d.kv_heads} heads each")
+        return (*(self._ints([r[i] for r in cut]) for i in range(3)), longest)
 
     def _bounds(self, ranges):
         if ranges is not None:

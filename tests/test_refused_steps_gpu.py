@@ -89,3 +89,19 @@ def test_siblings_accepted_at_a_page_border(fp8):
     fresh = torch.zeros_like(block.kv.bounds.rows)
     B.lora_kv_bounds_update(block.kv.view, B.KvBounds(block.kv.view, fresh), i32(0), i32(2 * page), i32(2 * page + 2), 2)
     assert torch.equal(got[..., :-12], fresh[own][..., :-12])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bounds_of_a_prompt_beside_single_tokens(fp8):
+    """Ranges cut into pieces write what whole ones write."""
+    block = make(fp8)
+    page = block.kv.stats()["page_tokens"]
+    call(block.step, 30, 1, [1, 2, 3], [15, 14, 1])
+    call(block.step, 7 * page + 8, 2, [0, 1, 2, 3], [7 * page + 5, 1, 2, 0])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    lens = [block.kv.length(s) for s in range(4)]
+    fresh = torch.zeros_like(block.kv.bounds.rows)
+    B.lora_kv_bounds_update(block.kv.view, B.KvBounds(block.kv.view, fresh), i32([0, 1, 2, 3]), i32([0] * 4), i32(lens), max(lens))
+    for s in range(4):
+        pages = torch.from_numpy(block.kv.pages(s)).cuda().long()
+        assert torch.equal(block.kv.bounds.rows[pages][..., :-12], fresh[pages][..., :-12])

@@ -167,3 +167,32 @@ def test_siblings_accepted_at_a_page_border(monkeypatch, paths):
                     written += b.kv.pages(s)[begin // b.page: -(-end // b.page)].tolist()
     assert len(written) == len(set(written)) and not set(written) & set(shared)
     assert set(written) == {int(b.kv.pages(s)[2]) for s, p in ((0, paths[0]), (1, paths[1]), (2, [0])) if p}
+
+
+@pytest.mark.parametrize("seqs,begins,lens", [([0, 1, 2], [0, 5, 7], [700, 1, 0]), ([0, 1], [3, 9], [1, 1]), ([0, 1, 2], [15, 40, 0], [300, 300, 300]),
+                                              ([1], [3], [500]), ([2, 0], [4, 8], [0, 0])])
+def test_ranges_cover_the_pages_once(monkeypatch, seqs, begins, lens):
+    """Cut ranges name every page of the whole ones once, with the same last position, and none is longer than said."""
+    b = Block(monkeypatch, max_pages=100)
+    ends = [x + n for x, n in zip(begins, lens)]
+    *cut, most = b._ranges(seqs, begins, ends)
+    got = {}
+    for s, begin, end in zip(*(x.tolist() for x in cut)):
+        assert 0 <= begin < end and end - begin <= most
+        for j in range(begin // b.page, -(-end // b.page)):
+            assert (s, j) not in got
+            got[s, j] = min(end, (j + 1) * b.page)
+    assert got == {(s, j): min(e, (j + 1) * b.page) for s, x, e in zip(seqs, begins, ends) if x < e for j in range(x // b.page, -(-e // b.page))}
+
+
+def test_a_long_prompt_beside_many_tokens(monkeypatch):
+    """128Ki positions in pages of 16 beside 255 single tokens, 8 KV heads: 2^24 workgroups as whole ranges, and no reason to refuse
+    the step that a block without bounds takes."""
+    b = Block(monkeypatch)
+    for field, value in (("kv_heads", 8), ("page_tokens", 16), ("max_pages", 8192)):
+        setattr(b.kv.view.desc, field, value)
+    *cut, most = b._ranges(list(range(256)), [0] + [77] * 255, [1 << 17] + [78] * 255)
+    workgroups = ((most + 14) // 16 + 1) * 8 * len(cut[0])
+    assert workgroups < 4 * 8 * (8192 + 255)  # of its pages and heads, a small multiple
+    *cut, most = b._ranges([0, 1, 2], [5, 9, 30], [6, 10, 31])
+    assert (cut[0].tolist(), most) == ([0, 1, 2], 1)
