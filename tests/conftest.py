@@ -13,10 +13,15 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU")
 
 
+def pytest_collection_finish(session):
+    gc.collect()
+    gc.freeze()  # what the imports made is not looked through again, so that the collection below is quick
+
+
 def pytest_runtest_setup(item):
     # A test that catches an error keeps itself, and a graph it captured, in a cycle (the error's traceback holds its frame).
     # Collected while another test captures, that graph's end would be an error inside a destructor: it goes here.
-    if item.get_closest_marker("gpu") and any(word in item.name for word in ("capture", "graph", "replay")):
+    if item.get_closest_marker("gpu"):
         gc.collect()
 
 
