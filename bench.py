@@ -122,7 +122,7 @@ def parse():
                          "attention over KV pages in the adapters' pool")
     ap.add_argument("--kv-fp8", action="store_true", help="with --serving: the cache holds 8-bit rows")
     ap.add_argument("--kv-pages", type=int, default=0, metavar="COUNT",
-                    help="with --serving: each token attends to that many pages (63 positions each, of 8-bit rows 123) of its "
+                    help="with --serving: each token attends to that many pages (63 positions each, of 8-bit rows 125) of its "
                          "sequence at most, chosen by the bounds of their keys")
     ap.add_argument("--floor", action="store_true",
                     help="only time bare streaming reads and a read-modify-write of given sizes "

@@ -108,6 +108,14 @@ def test_positions_of_a_page(fp8, bounds, heads, dim):
     assert kv.stats()["pages"] == 2
 
 
+def test_positions_of_the_benchmarks_pages():
+    """What bench.py's help says a page of its serving block holds: 16 rows of 8192, 8 KV heads of 128, with bounds."""
+    import pathlib
+    held = [B.KvCache(HostPool(2, row_width=8192), 8, 128, 2, 2, host_only=True, fp8=fp8, bounds=True).stats()["page_tokens"] for fp8 in (False, True)]
+    text = " ".join((pathlib.Path(__file__).parent.parent / "bench.py").read_text().replace('"', " ").split())
+    assert f"{held[0]} positions each, of 8-bit rows {held[1]}" in text
+
+
 def test_cache_refusals():
     make = lambda **kw: B.KvCache(HostPool(6), **{**dict(kv_heads=2, head_dim=64, max_seqs=2, max_pages=4, host_only=True), **kw})
     refused(B.LORA_EUNSUPPORTED, make, head_dim=72, fp8=True)
