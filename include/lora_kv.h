@@ -180,6 +180,9 @@ lora_status lora_kv_attn_plan(const int32_t *q_starts, const int32_t *seq, const
  *   lse        device fp32 [num_tokens][q_heads], or NULL
  *   scale      factor of the products, finite (the usual one is head_dim^-1/2); a row whose scores pass
  *              2^127 in magnitude has unspecified results
+ *   V          rows whose largest magnitude is 0 or within 2^-92 .. 2^100, for up to 2^19 positions: weights run up to 2^8 on the
+ *              way, so that sums of larger rows may pass 2^128, and a weight of an 8-bit row, which is rounded with the row's
+ *              factor, loses bits below 2^-126
  *   workspace  device, 16-byte aligned, at least plan->workspace_bytes (NULL with 0);
  *              contents on entry do not matter.  Calls that share it must not
  *              overlap, in graphs too.
