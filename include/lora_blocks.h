@@ -52,9 +52,12 @@ lora_status lora_kv_bounds_update(const lora_kv_view *kv, const lora_kv_bounds *
  * in ascending order, then -1.
  *     score = max over the query heads g of the KV head of  2^(f + s_g) sum_d max(Q_gd H_d, Q_gd L_d),
  * Q_g the query row in whole numbers of steps 2^s_g: s_g from the row as f from a page's bounds, Q rounded to nearest even,
- * within -127 .. 127, elements that are not finite counting as 0.  The sum bounds <Q, K> in these units; the
+ * within -127 .. 127, elements that are not finite counting as 0.  The sum bounds <Q, K> of the rounded query; the
  * whole numbers stay below 2^24, so scores are exact in fp32 and lists are the same on every machine.  An absent page
- * scores -inf.
+ * scores -inf.  One step serves all dimensions of a page: where a few hold keys many times larger than the others', bounds of
+ * the others are coarse and lists differ more from those of unrounded bounds (64 of 512 random pages of 64 keys of 128,
+ * 8 query heads: 88 to 92 % the same pages; with two dimensions 10 times larger 30 to 64 %, 80 times 32 to 40 %, and up
+ * to a seventh less of the softmax's weight on them).
  *   token_seq, token_pos  device int32 [num_tokens]; a token whose seq is negative (padding) or outside
  *                         [0, num_seqs), or whose position is not within the sequence's pages, lists -1 only (debug build:
  *                         LORA_DEBUG_BAD_TOKEN unless padding)

@@ -1028,11 +1028,14 @@ void launch_rows(const ArgsOf<F8, M> &a, unsigned grid, hipStream_t stream) {
   constexpr int W = (DP <= 64 ? 4 : DP <= 128 ? 2 : 1) * (F8 && DP > 64 ? 2 : 1);  // 8-bit stages take half the LDS
   const auto wide = full<DP>(a) ? attn_rows_kernel<DP, 2 * W, kFull<DP>, F8, M> : attn_rows_kernel<DP, 2 * W, false, F8, M>;
   const auto slim = full<DP>(a) ? attn_rows_kernel<DP, W, kFull<DP>, F8, M> : attn_rows_kernel<DP, W, false, F8, M>;
-  // Many workgroups of half the waves again, where there are more than a compute unit holds: items are short then, and what
-  // counts is how many begin and end side by side (in 8 bits, 256 tokens over 75 to 300, 32 / 8 heads of 128: 29 us, else 40;
+  // Many workgroups of half the waves again, where there are more than a compute unit holds: what counts for short items is how
+  // many begin and end side by side (in 8 bits, 256 tokens over 75 to 300, 32 / 8 heads of 128: 29 us, else 40;
   // 64 over 128 to 512, 64 / 64: 73 and 92; 64 over 8192, 64 / 8, 1000 workgroups: 145 and 135.  Lists of 480 positions, 1812
   // workgroups, heads of 64: 21.1 and 25.4, bf16 27.4 and 36.6; of 2048 positions in 8 bits, 2048 workgroups, heads of
-  // 128: 181 and 167).  bf16 rows with causal masks keep the waves that their sums have always been joined in.
+  // 128: 181 and 167).  The rule does not know how long the items of tokens are, and long ones are slower by it with heads of
+  // 256, and with others in the first such grids alone (8-bit, 1280 workgroups, up to 1024 / 2048 / 8192 positions, half and all:
+  // 64 / 8 of 128 41 and 47, 79 and 86, 285 and 283; 32 / 8 of 64 23 and 26, 41 and 42, 163 and 143; 16 / 8 of 256 93 and 95, 181
+  // and 167, 707 and 602; 4096 workgroups of up to 8192, 64 / 8 of 128: 871 and 851).  bf16 rows with causal masks keep the waves that their sums have always been joined in.
   bool many = (F8 || M != Mask::kCausal) && W > 1 && grid >= (M == Mask::kBlocks ? 4 : 5) * kUnits;
   if constexpr (M == Mask::kBlocks) many = many && !(F8 && (int64_t)a.count * a.kv.page_tokens > 1024);
   if (many) {

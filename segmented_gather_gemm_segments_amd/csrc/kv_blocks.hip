@@ -31,8 +31,10 @@ __device__ __forceinline__ uint32_t byte4(const int *c) {
 
 // ----------------------------------------------------------------- bounds
 // A workgroup per page of a range and KV head: threads take 8 dimensions of every R-th key, then thread d joins dimension d's R
-// values through LDS.  Reads the page's keys once: 32 pages of 64 keys, 8 KV heads of 128, 7.0 us, most of it the launch and a
-// chain of range, page and keys; a workgroup for each page keeps that chain one page long.
+// values through LDS.  Reads the page's keys once: 32 pages of 64 keys, 8 KV heads of 128, 7 us from memory, 4.9 from the last
+// cache, most of it the launch and a chain of range, page and keys; a workgroup for each page keeps that chain one page long.
+// The 33 pages of a prompt's chunk of 2048 take as long.  The grid has the longest range's pages for every range: that chunk beside
+// 255 single tokens, 51 us as it comes and 13.4 with its range cut into pieces of two pages.
 constexpr int kThreads = 256;
 
 template <bool F8>
@@ -124,7 +126,8 @@ __global__ __launch_bounds__(kThreads) void bounds_kernel(lora_kv8_view v, lora_
 // Bounds cross the device once for the heads that share them, 2 head_dim + 16 bytes a page.  A wave keeps 4 groups of 16
 // pages in flight where its workgroup has a compute unit to itself; 2 where several share one and registers decide how many
 // (1024 lists of up to 125 pages: 11.6 us, with 4 groups 18.3), or head_dim is above 128.  32 tokens, 8 KV heads of 128,
-// up to 512 pages: 11.8 us.  One compute unit reads no more than about 40 GB/s of such rows, so where lists are few and may
+// up to 512 pages, 23 MB of rows: 11.8 us back to back, where the last cache holds them, 14.2 from memory (a decoder reads its
+// K and V in between).  Times below are of the first kind.  One compute unit reads no more than about 40 GB/s of such rows, so where lists are few and may
 // be long a launch of its own scores their pages, 256 a workgroup, into a workspace (8 lists of 8125 pages: 21.5 us, in one
 // launch 95).
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
@@ -169,7 +172,8 @@ __device__ __forceinline__ void score(const Select &a, const Token &token, int t
   const int fr = lane & 15, fg = lane >> 4;
   const int D = kv.head_dim, steps = (2 * D + 63) / 64;
   // the next turn's pages are looked up a load sooner, where registers are left for it (320 lists of up to 1000 pages: 28 us,
-  // else 31; heads of 256, 694 lists of up to 469: 23 and 21.4)
+  // else 31; heads of 256, 694 lists of up to 469: 23 and 21.4).  Lists of few turns lose a little by it: 784 of up to 250 pages
+  // 15.2 us, else 14.2.
   constexpr bool kAhead = S <= 4;
   constexpr int kTurn = 16 * U * WAVES;
   const int first = begin + 16 * wave;
@@ -494,7 +498,9 @@ extern "C" lora_status lora_kv_block_select(const lora_kv_view *kv, const lora_k
   // Threads of a workgroup: 512 where every compute unit has one of them at most, for a shorter way over the pages (256 lists of
   // up to 512 pages: 11.8 us, with 256 threads 15.2); 256 up to five a compute unit (1024 lists of up to 125 pages: 11.6 us,
   // with 128 threads 12.6); then 128, for fewer waves that wait for one wave's part (1812 lists of up to 209 pages: 12.5 us,
-  // with 256 threads 16.1); 1024 for long sequences, whose keys leave a compute unit few workgroups.
+  // with 256 threads 16.1); 1024 for long sequences, whose keys leave a compute unit few workgroups.  Lengths are on the device,
+  // so the table's width stands for them, and short sequences in a wide table pay for it: lists of up to 100 pages in a table of
+  // up to 2048 and of more, 8 lists 8.0 and 10 us, 256 lists 8.2 and 11, 2048 lists 17 and 70.
   auto launch = [&](auto keys, auto threads) {
     constexpr int K = decltype(keys)::value, T = decltype(threads)::value;
     const auto kernel = size == 2 ? select_kernel<K, T, 2> : size == 4 ? select_kernel<K, T, 4> : select_kernel<K, T, 8>;
