@@ -407,7 +407,8 @@ class ServingBlock:
     def _places(self, seqs, new_tokens):
         """What a step will need, before any sequence grows: lengths after it, starts, on the device each token's sequence and
         position, and the ranges whose bounds change."""
-        B._not_capturing("sequences cannot grow")
+        with B._On(self.device, None):
+            B._not_capturing("sequences cannot grow")
         lens = [max(self.kv.length(s), 0) + n for s, n in zip(seqs, new_tokens)]
         if max(lens) > self.kv.view.max_kv:
             B._refuse(f"sequences of {lens[:8]} positions, the cache holds {self.kv.view.max_kv} of each")
@@ -509,7 +510,8 @@ class ServingBlock:
         seqs, paths = [int(s) for s in seqs], [[int(n) for n in p] for p in paths]
         if len(seqs) != len(paths) or len(set(seqs)) != len(seqs):
             B._refuse(f"{len(seqs)} sequences and {len(paths)} paths, or a sequence twice")
-        B._not_capturing("a path cannot be accepted")
+        with B._On(self.device, None):
+            B._not_capturing("a path cannot be accepted")
         page_tokens, bases, own = self.kv.view.desc.page_tokens, [], []
         for s, path in zip(seqs, paths):
             base, parents = self._drafts.get(s, (0, []))

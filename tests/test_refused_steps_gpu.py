@@ -105,3 +105,29 @@ def test_bounds_of_a_prompt_beside_single_tokens(fp8):
     for s in range(4):
         pages = torch.from_numpy(block.kv.pages(s)).cuda().long()
         assert torch.equal(block.kv.bounds.rows[pages][..., :-12], fresh[pages][..., :-12])
+
+
+def test_nothing_grows_in_a_capture():
+    """Refused before anything is uploaded, which would end the capture: it goes on, and its graph replays."""
+    block = make(False)
+    call(block.step, 30, 1, [0, 1], [20, 10])
+    call(block.draft, 2, 2, [1], [[-1, 0]])
+    h, ids, x = torch.zeros((2, D_MODEL), dtype=torch.bfloat16, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    refusals = []
+    with torch.cuda.graph(graph, stream=stream):
+        x.add_(1)
+        for f in (lambda: block.step(h, [0], [2], ids), lambda: block.step(h, [0], [2], ids, pages=3),
+                  lambda: block.draft(h, [0], [[-1, 0]], ids), lambda: block.accept([1], [[0]])):
+            try:
+                f()
+            except B.LoraError as e:
+                refusals.append(e.status)
+        x.add_(1)
+    assert refusals == [B.LORA_EINVAL] * 4 and [block.kv.length(s) for s in (0, 1)] == [20, 12]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((x == 2).all())
+    block.accept([1], [[0]])
+    assert block.kv.length(1) == 11
