@@ -38,6 +38,8 @@ lora_status lora_kv_get_bounds(const lora_kv *kv, lora_kv_bounds *bounds);
  *   max_tokens       host bound of end[r] - begin[r]; pages of a longer range past that many
  *                    positions are not written (LORA_DEBUG_BAD_TOKEN)
  * Absent pages are skipped (LORA_DEBUG_BAD_PAGE).  No two ranges may touch the same page.
+ * The launch has as many workgroups for every range as max_tokens positions have pages: long ranges beside short ones are
+ * better cut at page borders.
  * Errors: LORA_EINVAL, LORA_EUNSUPPORTED (view, 2^24 workgroups and more), LORA_EHIP.                          */
 lora_status lora_kv_bounds_update(const lora_kv_view *kv, const lora_kv_bounds *bounds, const int32_t *seq,
                                   const int32_t *begin, const int32_t *end, int32_t n, int32_t max_tokens,
